@@ -333,6 +333,99 @@ int k3moe_ep_dispatch(k3moe_handle *h, const int32_t *idx, int tokens_per_rank, 
                       const int32_t *counts, int n_ranks, const k3moe_ep_plan *plan, int32_t *dest_rank,
                       int32_t *dest_row, void *workspace, size_t workspace_bytes, cudaStream_t stream);
 
+/* ------------------------------------------------------------ training step of the routed experts
+ * No counterpart in the sources' engines, which only run the layer: the operators that train or
+ * fine-tune the routed experts on 16-bit weights (the K3 report review's QAT passage trains them
+ * on higher-precision weights).  They need no handle.  One step over T tokens, top K:
+ *   rows_plan     the routing's pairs in expert order: row ranges and each pair's row
+ *   rows_gather   the tokens' latent rows in that order
+ *   group_mm      gate and up products of every expert's rows, [rows, 2 I]
+ *   glu_dropout   a = dropout(act(gate) up), the mask never stored
+ *   group_mm      the down product
+ *   rows_combine  the weighted sum of each token's rows
+ * and backwards: rows_combine_grad, group_mm_grad_x / _w, glu_dropout_grad (the same seed and
+ * offset give the same mask), group_mm_grad_x / _w, rows_combine without weights.
+ *
+ * Conventions beyond those above:
+ *   - dtype, out_dtype: K3MOE_TYPE_*.  Leading dimensions ld* are in elements and at least the row
+ *     length.  Sums are held in fp32 and rounded once, to the output's type, to nearest even.
+ *   - offsets: device int32 [n_experts + 1], non-decreasing, from >= 0 to <= rows: expert e owns
+ *     rows offsets[e] .. offsets[e+1] - 1.  Rows before offsets[0] and from offsets[n_experts] on
+ *     belong to no expert: never written, and not read into any result.
+ *   - status: device int32 [4], caller-owned and zeroed by the caller once: the first device-side
+ *     error is recorded in it as in the handle's status word (K3MOE_ERR_RANGE: offsets or a row
+ *     number outside its range; K3MOE_ERR_TIMEOUT).  With bad offsets a product writes nothing.
+ *   - An output that overlaps an input is K3MOE_ERR_ALIAS, except where a call says otherwise.
+ *   - Every call only enqueues kernels on `stream`: no allocation, no synchronisation (capturable). */
+#define K3MOE_TYPE_F32  0
+#define K3MOE_TYPE_BF16 1
+#define K3MOE_TYPE_F16  2
+
+#define K3MOE_TRAIN_MAX_EXPERTS 1024
+
+/* Pairs (t, k) with idx[t][k] - first_expert = e in [0, n_experts) in order of e, then of (t, k):
+ * pos [T, K] receives each pair's row and -1 for every other pair (an expert of another rank, or
+ * -1 for a dropped pair), offsets [n_experts + 1] the experts' row ranges.  A token may name an
+ * expert twice.  T >= 0, K >= 1, T * K < 2^31. */
+size_t k3moe_rows_plan_workspace_bytes(int T, int K, int n_experts);
+int k3moe_rows_plan(const int32_t *idx, int T, int K, int first_expert, int n_experts, int32_t *offsets,
+                    int32_t *pos, void *workspace, size_t workspace_bytes, cudaStream_t stream);
+
+/* out[pos[t][k]] = x[t] for every pos >= 0.  x [T, D], out [n_rows, D]; rows that no pair names are
+ * left as they are.  F16 or BF16. */
+int k3moe_rows_gather(const void *x, int64_t ldx, const int32_t *pos, int T, int K, int D, int dtype, void *out,
+                      int64_t ldo, int n_rows, int32_t *status, cudaStream_t stream);
+
+/* z[t] = sum over k in order, pos[t][k] >= 0, of weights[t][k] y[pos[t][k]] (weights NULL: all 1);
+ * a token without rows gives zeros.  weights fp32 [T, K].  This is also rows_gather's gradient. */
+int k3moe_rows_combine(const void *y, int64_t ldy, int n_rows, const int32_t *pos, const float *weights, int T, int K,
+                       int D, int dtype, void *z, int64_t ldz, int32_t *status, cudaStream_t stream);
+
+/* Gradient of rows_combine: dy[pos[t][k]] = weights[t][k] dz[t] and dweights[t][k] = <dz[t], y[pos[t][k]]>
+ * (0 where pos < 0).  dy may be y itself (the same pointer and ldy). */
+int k3moe_rows_combine_grad(const void *dz, int64_t lddz, const void *y, int64_t ldy, int n_rows, const int32_t *pos,
+                            const float *weights, int T, int K, int D, int dtype, void *dy, int64_t lddy,
+                            float *dweights, int32_t *status, cudaStream_t stream);
+
+/* Products grouped by expert, for the rows r of every expert e; weights w [n_experts][n_out][n_in]
+ * with row stride ldw and expert stride stride_w (elements):
+ *   group_mm         y[r]  = W_e x[r]                       y  [rows, n_out]
+ *   group_mm_grad_x  dx[r] = W_e^T dy[r]                    dx [rows, n_in]
+ *   group_mm_grad_w  dW_e  = sum_r dy[r] x[r]^T             dw [n_experts][n_out][n_in]
+ * dtype F16 or BF16 for all inputs; out_dtype the same or F32.  accumulate (grad_w, F32 only): dw
+ * is added to; otherwise an expert without rows gets zeros.  Results do not depend on timing.
+ * Tensor-core kernels run where every row starts on a 16-byte boundary (pointers 16-byte aligned,
+ * leading dimensions and strides multiples of 16 bytes), CUDA-core kernels elsewhere. */
+int k3moe_group_mm(const int32_t *offsets, int n_experts, int rows, int n_in, int n_out, const void *x, int64_t ldx,
+                   const void *w, int64_t ldw, int64_t stride_w, int dtype, void *y, int64_t ldy, int out_dtype,
+                   int32_t *status, cudaStream_t stream);
+int k3moe_group_mm_grad_x(const int32_t *offsets, int n_experts, int rows, int n_in, int n_out, const void *dy,
+                          int64_t lddy, const void *w, int64_t ldw, int64_t stride_w, int dtype, void *dx,
+                          int64_t lddx, int out_dtype, int32_t *status, cudaStream_t stream);
+int k3moe_group_mm_grad_w(const int32_t *offsets, int n_experts, int rows, int n_in, int n_out, const void *dy,
+                          int64_t lddy, const void *x, int64_t ldx, int dtype, void *dw, int64_t lddw,
+                          int64_t stride_dw, int out_dtype, int accumulate, int32_t *status, cudaStream_t stream);
+
+/* Dropout.  Element i (row-major index without padding) is kept when word i mod 4 of Philox4x32-10
+ * (Salmon, Moraes, Dror and Shaw, "Parallel random numbers: as easy as 1, 2, 3", 2011) with counter
+ * (i / 4, offset) as two 64-bit little-endian halves and key seed is at least floor(p 2^32); kept
+ * elements are multiplied by 1 / (1 - p).  0 <= p < 1; p = 0 keeps all. */
+
+/* a[r][c] = dropout(act(g, u)) with g = gu[r][c], u = gu[r][width + c].  gu [rows, 2 width], a [rows,
+ * width]; act K3MOE_ACT_*, betas as in k3moe_config (<= 0: 4 and 25).  F16 or BF16. */
+int k3moe_glu_dropout(const void *gu, int64_t ldgu, int rows, int width, int dtype, int act, float situ_beta,
+                      float situ_linear_beta, double p, uint64_t seed, uint64_t offset, void *a, int64_t lda,
+                      cudaStream_t stream);
+/* Its gradient: dgu [rows, 2 width] from da [rows, width] and gu.  dgu may be gu itself (the same
+ * pointer and leading dimension). */
+int k3moe_glu_dropout_grad(const void *da, int64_t ldda, const void *gu, int64_t ldgu, int rows, int width, int dtype,
+                           int act, float situ_beta, float situ_linear_beta, double p, uint64_t seed, uint64_t offset,
+                           void *dgu, int64_t lddgu, cudaStream_t stream);
+/* out = dropout(x) [+ residual], n contiguous elements, F32, F16 or BF16.  residual may be NULL; out
+ * may be x or residual.  Its gradient for x is the same call on the output's gradient without a residual. */
+int k3moe_dropout(const void *x, const void *residual, int64_t n, int dtype, double p, uint64_t seed, uint64_t offset,
+                  void *out, cudaStream_t stream);
+
 /* ------------------------------------------------------------ profiling
  * Stage timing with CUDA events recorded on the launching stream around each
  * stage of k3moe_forward (a ring of 256 forwards), plus a count of kernel

@@ -21,13 +21,17 @@ ERR_CODE = {v: k for k, v in ERR.items()}
 PATH_AUTO, PATH_GENERIC, PATH_TENSOR = 0, 1, 2
 ROUTER_F32, ROUTER_BF16 = 0, 1
 ACT_SILU, ACT_SITU = 0, 1
+TYPE_F32, TYPE_BF16, TYPE_F16 = 0, 1, 2
 
 EXPORTS = ["k3moe_create", "k3moe_persistent_bytes", "k3moe_load_weights", "k3moe_workspace_bytes",
            "k3moe_forward", "k3moe_forward_host", "k3moe_status", "k3moe_destroy", "k3moe_strerror",
            "k3moe_path_for", "k3moe_debug_dequant", "k3moe_debug_wait_timeout",
            "k3moe_profile_enable", "k3moe_profile_read", "k3moe_stage_name", "k3moe_qb_workspace_bytes",
            "k3moe_qb_bias", "k3moe_ep_plan_compute", "k3moe_ep_dispatch_workspace_bytes", "k3moe_ep_dispatch",
-           "k3moe_route_static", "k3moe_mma_peak"]
+           "k3moe_route_static", "k3moe_mma_peak",
+           "k3moe_rows_plan_workspace_bytes", "k3moe_rows_plan", "k3moe_rows_gather", "k3moe_rows_combine",
+           "k3moe_rows_combine_grad", "k3moe_group_mm", "k3moe_group_mm_grad_x", "k3moe_group_mm_grad_w",
+           "k3moe_glu_dropout", "k3moe_glu_dropout_grad", "k3moe_dropout"]
 STAGES = ["router", "down_proj", "topk", "permute", "gate_up", "expert_down", "combine_norm",
           "up_proj", "shared", "finish", "prep", "shared_down"]
 
@@ -105,6 +109,19 @@ def lib():
         L.k3moe_ep_dispatch.argtypes = [vp, vp, i, i, vp, i, C.POINTER(EpPlan), vp, vp, vp, sz, vp]
         L.k3moe_route_static.argtypes = [vp, vp, i, vp, vp, vp]
         L.k3moe_mma_peak.argtypes = [i, i, i, vp, C.POINTER(C.c_float), vp]
+        l, u, f, d = C.c_int64, C.c_uint64, C.c_float, C.c_double
+        L.k3moe_rows_plan_workspace_bytes.argtypes = [i, i, i]
+        L.k3moe_rows_plan_workspace_bytes.restype = sz
+        L.k3moe_rows_plan.argtypes = [vp, i, i, i, i, vp, vp, vp, sz, vp]
+        L.k3moe_rows_gather.argtypes = [vp, l, vp, i, i, i, i, vp, l, i, vp, vp]
+        L.k3moe_rows_combine.argtypes = [vp, l, i, vp, vp, i, i, i, i, vp, l, vp, vp]
+        L.k3moe_rows_combine_grad.argtypes = [vp, l, vp, l, i, vp, vp, i, i, i, i, vp, l, vp, vp, vp]
+        L.k3moe_group_mm.argtypes = [vp, i, i, i, i, vp, l, vp, l, l, i, vp, l, i, vp, vp]
+        L.k3moe_group_mm_grad_x.argtypes = [vp, i, i, i, i, vp, l, vp, l, l, i, vp, l, i, vp, vp]
+        L.k3moe_group_mm_grad_w.argtypes = [vp, i, i, i, i, vp, l, vp, l, i, vp, l, l, i, i, vp, vp]
+        L.k3moe_glu_dropout.argtypes = [vp, l, i, i, i, i, f, f, d, u, u, vp, l, vp]
+        L.k3moe_glu_dropout_grad.argtypes = [vp, l, vp, l, i, i, i, i, f, f, d, u, u, vp, l, vp]
+        L.k3moe_dropout.argtypes = [vp, vp, l, i, d, u, u, vp, vp]
         for name in EXPORTS:
             getattr(L, name)
         _lib = L
