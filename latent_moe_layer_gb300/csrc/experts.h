@@ -71,3 +71,6 @@ struct K3Group {
     int *status;
 };
 int k3_group_generic(int mode, const K3Group &g, cudaStream_t st);
+// Whether the tensor-core kernels take it (every row on a 16-byte boundary), and their launch.
+bool k3_group_tc_fits(int mode, const K3Group &g);
+int k3_group_tc(int mode, const K3Group &g, cudaStream_t st);

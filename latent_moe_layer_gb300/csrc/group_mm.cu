@@ -170,7 +170,7 @@ static int group_run(const K3Group &g, int mode, cudaStream_t st)
 {
     const int rc = group_check(g, mode);
     if (rc) return rc > 0 ? K3MOE_OK : rc;
-    return k3_group_generic(mode, g, st);
+    return k3_group_tc_fits(mode, g) ? k3_group_tc(mode, g, st) : k3_group_generic(mode, g, st);
 }
 
 extern "C" int k3moe_group_mm(const int32_t *offsets, int n_experts, int rows, int n_in, int n_out, const void *x,

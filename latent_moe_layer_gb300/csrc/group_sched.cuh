@@ -60,6 +60,22 @@ __device__ __forceinline__ bool group_tiles(const int32_t *__restrict__ offsets,
     return true;
 }
 
+// All threads of the CTA: whether the offsets are non-decreasing within [0, rows] (else K3MOE_ERR_RANGE is recorded).
+template <int THREADS>
+__device__ __forceinline__ bool group_offsets_ok(const int32_t *__restrict__ offsets, int E, int rows, int *status)
+{
+    bool bad = false;
+    for (int e = threadIdx.x; e < E; e += THREADS) {
+        const int a = offsets[e], b = offsets[e + 1];
+        bad |= a < 0 || b < a || b > rows;
+    }
+    if (__syncthreads_or(bad)) {
+        if (threadIdx.x == 0) set_status(status, K3MOE_ERR_RANGE, -1);
+        return false;
+    }
+    return true;
+}
+
 // The expert holding tile index t: the last e with s_tile[e] <= t (empty experts share a prefix
 // value, so the last of them is the one with tiles).
 __device__ __forceinline__ int group_find(const int *s_tile, int E, int t)

@@ -1,0 +1,481 @@
+// Products grouped by expert on the tensor cores (k3moe_group_mm, _grad_x, _grad_w): tcgen05 over CTA
+// pairs, TMA-fed, persistent.
+//
+// One tile is D[256 x N] (+)= A[256 x c] B[N x c]^T, c the contraction, fp32 accumulators in TMEM:
+//   mm       A = W_e rows (c = n_in contiguous),       B = x rows,  N = up to 256 of the expert's rows
+//   grad_x   A = W_e columns (c = n_out, MN-major),    B = dy rows, N as above
+//   grad_w   A = dy columns (c = rows, MN-major),      B = x columns (MN-major), N = 256
+// The weights are the M side in mm and grad_x, so a group's raggedness costs at most 15 padding columns
+// (N is a multiple of 16), its rows past the end are columns that are computed and not stored, and NaN or
+// infinities there reach nothing else.  In grad_w the rows are the contraction: the rows of the last
+// 16-row step that lie beyond the group (the next expert's) are set to zero in shared memory first.
+//
+// Each CTA of the pair loads its 128 rows of A and its half of B, 64 contraction values a stage: 32 KB
+// of shared-memory writes per CTA feed a 256 x 256 x 64 step, half of what two single-CTA tiles of
+// 128 x 256 need.  Two accumulator sets (2 x 256 TMEM columns) let the epilogue of one tile overlap the
+// next tile's MMAs.
+#include <cudaTypedefs.h>
+
+#include "experts.h"
+#include "group_sched.cuh"
+#include "pair.cuh"
+
+namespace k3 {
+
+constexpr int GT_BK = 64, GT_TILE_M = 256, GT_TILE_N = 256;
+constexpr int GT_A_BYTES = 128 * GT_BK * 2, GT_STAGE = 2 * GT_A_BYTES;
+constexpr int GT_EPI_WARPS = 8, GT_THREADS = 128 + 32 * GT_EPI_WARPS;   // TMA, MMA, tail, idle, epilogue
+
+template <int MODE>
+struct GroupSmem {
+    static constexpr int NS = MODE == K3_GROUP_GRAD_W ? 5 : 6;
+    static constexpr int OFF_OUT = NS * GT_STAGE;                       // grad_w: two 4 KB output boxes a warp
+    static constexpr int OUT_BYTES = MODE == K3_GROUP_GRAD_W ? GT_EPI_WARPS * 2 * 4096 : 0;
+    static constexpr int OFF_BAR = OFF_OUT + OUT_BYTES;
+    static constexpr int N_BAR = 3 * NS + 5;                            // full, empty, tail; tfull, tempty x 2; drain
+    static constexpr int OFF_INT = OFF_BAR + N_BAR * 8 + 8;
+    // grad_w needs no tile table and reads the offsets from memory, which leaves room for its fifth stage
+    static constexpr int N_INT = MODE == K3_GROUP_GRAD_W ? 0 : 2 * (K3MOE_TRAIN_MAX_EXPERTS + 1) + 34;
+    static constexpr int BYTES = OFF_INT + N_INT * 4 + 1024;
+    static_assert(BYTES <= kMaxSmem, "shared memory");
+};
+
+struct GroupMaps {
+    CUtensorMap a;           // mm: box 64 x 128 rows; grad_x, grad_w: box 64 x 64
+    CUtensorMap b[5];        // mm, grad_x: boxes of 128, 64, 32, 16, 8 rows; grad_w: b[0], box 64 x 64
+    CUtensorMap out;         // grad_w
+};
+
+struct GroupTcArgs {
+    const int32_t *offsets;
+    int E, rows, M, Nc;      // M: the tile-row extent; Nc: grad_w's column extent (n_in)
+    int K;                   // contraction of mm and grad_x
+    int expert_coord;        // 0: one weight for all experts
+    int bf16, accumulate;
+    void *out;
+    int64_t ldo;
+    int *status;
+};
+
+struct GroupJob {
+    int e, m0, c0, n, steps, last;   // first row and column of the tile; columns; stages; contraction values of the last stage
+};
+
+template <int MODE>
+__device__ __forceinline__ GroupJob group_job(const GroupTcArgs &a, const int *s_off, const int *s_tile, int mb, int cb,
+                                              int job)
+{
+    GroupJob j;
+    if (MODE == K3_GROUP_GRAD_W) {
+        // expert by expert, so that its rows of dy and x stay in L2
+        j.e = job / (mb * cb);
+        const int w = job - j.e * mb * cb;
+        j.m0 = (w / cb) * GT_TILE_M;
+        j.c0 = (w % cb) * GT_TILE_N;
+        j.n = GT_TILE_N;
+        const int k = s_off[j.e + 1] - s_off[j.e];
+        j.steps = (k + GT_BK - 1) / GT_BK;
+        j.last = k - (j.steps - 1) * GT_BK;
+    } else {
+        // an expert's row tiles next to each other on the same block of weights
+        j.e = group_find(s_tile, a.E, job / mb);
+        const int w = job - s_tile[j.e] * mb, t = s_tile[j.e + 1] - s_tile[j.e];
+        const int rows = s_off[j.e + 1] - s_off[j.e], width = group_tile_width(rows, GT_TILE_N, 16);
+        j.m0 = (w / t) * GT_TILE_M;
+        const int first = (w % t) * width;
+        j.c0 = s_off[j.e] + first;
+        j.n = min(width, rows - first);
+        j.steps = (a.K + GT_BK - 1) / GT_BK;
+        j.last = a.K - (j.steps - 1) * GT_BK;
+    }
+    return j;
+}
+
+// `rows` (a multiple of 8, at most 128) rows of B from row `row`: boxes of 128 .. 8 rows, largest first.
+__device__ __forceinline__ void load_rows(const CUtensorMap *maps, uint32_t dst, uint32_t bar, int k, int row, int rows)
+{
+#pragma unroll
+    for (int i = 0; i < 5; ++i) {
+        const int box = 128 >> i;
+        if (rows & box) {
+            tma_load_2d_pair(dst, maps + i, bar, k, row);
+            dst += box * 128;
+            row += box;
+        }
+    }
+}
+
+template <int MODE, class O>
+__global__ void __launch_bounds__(GT_THREADS, 1) group_tc_kernel(const __grid_constant__ GroupMaps maps,
+                                                                 const GroupTcArgs args)
+{
+    griddep_enter();
+    using SM = GroupSmem<MODE>;
+    constexpr int NS = SM::NS;
+    constexpr bool W = MODE == K3_GROUP_GRAD_W;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = (uint8_t *)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
+    uint64_t *full = (uint64_t *)(smem + SM::OFF_BAR), *empty = full + NS, *tail = empty + NS;
+    uint64_t *tfull = tail + NS, *tempty = tfull + 2, *drain = tempty + 2;
+    uint32_t *tmem_holder = (uint32_t *)(drain + 1);
+    volatile int *abort_flag = (volatile int *)(tmem_holder + 1);
+    int *s_int = (int *)(smem + SM::OFF_INT), *s_tile = s_int + K3MOE_TRAIN_MAX_EXPERTS + 1;
+    const int *s_off = W ? args.offsets : s_int;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t rank = cluster_ctarank();
+
+    // every CTA reads the same offsets, so all agree on a refusal
+    if (W ? !group_offsets_ok<GT_THREADS>(args.offsets, args.E, args.rows, args.status)
+          : !group_tiles<GT_THREADS>(args.offsets, args.E, args.rows, GT_TILE_N, s_int, s_tile,
+                                     s_tile + K3MOE_TRAIN_MAX_EXPERTS + 1, args.status))
+        return;
+    const int mb = (args.M + GT_TILE_M - 1) / GT_TILE_M, cb = W ? (args.Nc + GT_TILE_N - 1) / GT_TILE_N : 1;
+    const int jobs = W ? args.E * mb * cb : s_tile[args.E] * mb;
+    const int first = (int)cluster_id_x(), stride = (int)ncluster_x();
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < NS; ++i) {
+            mbar_init(smem_u32(full + i), 2);            // both CTAs' loads (or their zeroed tails)
+            mbar_init(smem_u32(empty + i), 1);
+            mbar_init(smem_u32(tail + i), 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(smem_u32(tfull + i), 1);
+            mbar_init(smem_u32(tempty + i), 2 * GT_EPI_WARPS);
+        }
+        mbar_init(smem_u32(drain), 1);
+        *abort_flag = 0;
+        mbar_fence_init();
+    }
+    if (warp == 1) tmem_alloc_pair(smem_u32(tmem_holder), 512);
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync();                                      // barriers of both CTAs before any remote arrival
+    tc_fence_after();
+    const uint32_t tmem = *tmem_holder;
+
+    if (warp == 0 && lane == 0) {
+        // ------------------------------------------------------------ TMA producer (each CTA its half)
+        prefetch_tmap(&maps.a);
+        for (int i = 0; i < (W ? 1 : 5); ++i) prefetch_tmap(&maps.b[i]);
+        uint32_t it = 0, tails = 0;
+        bool ok = true;
+        for (int job = first; job < jobs && ok; job += stride) {
+            const GroupJob j = group_job<MODE>(args, s_off, s_tile, mb, cb, job);
+            const int half = W ? 128 : ((j.n + 15) & ~15) / 2;           // this CTA's share of B's rows
+            const int m = j.m0 + 128 * (int)rank, e = args.expert_coord * j.e;
+            const uint32_t bytes = GT_A_BYTES + half * 128;
+            for (int s = 0; s < j.steps; ++s, ++it) {
+                const int slot = it % NS;
+                if (!pair_wait(smem_u32(empty + slot), ((it / NS) & 1) ^ 1, abort_flag, args.status, 61)) {
+                    ok = false;
+                    break;
+                }
+                const uint32_t a_dst = smem_u32(smem + slot * GT_STAGE), b_dst = a_dst + GT_A_BYTES;
+                uint32_t bar = cluster_addr(smem_u32(full + slot), 0);
+                if (W && s == j.steps - 1 && (j.last & 15)) {
+                    // the tail warp zeroes the foreign rows before it arrives for this CTA
+                    bar = smem_u32(tail + tails % NS);
+                    ++tails;
+                    mbar_expect_tx(bar, bytes);
+                } else {
+                    mbar_expect_tx_cluster(bar, bytes);
+                }
+                const int k = s * GT_BK;
+                if (MODE == K3_GROUP_MM) {
+                    tma_load_3d_pair(a_dst, &maps.a, bar, k, m, e);
+                } else if (MODE == K3_GROUP_GRAD_X) {
+                    tma_load_3d_pair(a_dst, &maps.a, bar, m, k, e);
+                    tma_load_3d_pair(a_dst + GT_A_BYTES / 2, &maps.a, bar, m + 64, k, e);
+                }
+                if (!W) {
+                    load_rows(maps.b, b_dst, bar, k, j.c0 + half * (int)rank, half);
+                } else {
+                    const int r = s_off[j.e] + k, c = j.c0 + 128 * (int)rank;
+                    tma_load_2d_pair(a_dst, &maps.a, bar, m, r);
+                    tma_load_2d_pair(a_dst + GT_A_BYTES / 2, &maps.a, bar, m + 64, r);
+                    tma_load_2d_pair(b_dst, &maps.b[0], bar, c, r);
+                    tma_load_2d_pair(b_dst + GT_A_BYTES / 2, &maps.b[0], bar, c + 64, r);
+                }
+            }
+        }
+        // the pair's last releases of this CTA's slots land before it may exit
+        const uint32_t n = it < (uint32_t)NS ? it : (uint32_t)NS;
+        for (uint32_t q = 0; ok && q < n; ++q) {
+            const uint32_t i2 = it - 1 - q;
+            ok = pair_wait(smem_u32(empty + i2 % NS), (i2 / NS) & 1, abort_flag, args.status, 62);
+        }
+    } else if (warp == 1 && lane == 0 && rank == 0) {
+        // ------------------------------------------------------------ MMA issuer (even CTA, for both)
+        const uint32_t major = (MODE == K3_GROUP_MM ? 0 : IDESC_A_MN) | (W ? IDESC_B_MN : 0);
+        uint32_t it = 0, tc = 0;
+        bool ok = true;
+        for (int job = first; job < jobs && ok; job += stride) {
+            const GroupJob j = group_job<MODE>(args, s_off, s_tile, mb, cb, job);
+            if (W && j.steps == 0) continue;
+            const uint32_t idesc = idesc_f16(GT_TILE_M, (j.n + 15) & ~15, args.bf16) | major;
+            const int acc = (int)(tc & 1);
+            if (!pair_wait(smem_u32(tempty + acc), ((tc >> 1) & 1) ^ 1, abort_flag, args.status, 63)) break;
+            tc_fence_after();
+            const uint32_t d = tmem + acc * GT_TILE_N;
+            for (int s = 0; s < j.steps; ++s, ++it) {
+                const int slot = it % NS;
+                if (!pair_wait(smem_u32(full + slot), (it / NS) & 1, abort_flag, args.status, 64)) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+                const uint32_t a_addr = smem_u32(smem + slot * GT_STAGE), b_addr = a_addr + GT_A_BYTES;
+                // a step of 16 contraction values: 32 bytes along a K-major row, 16 rows of 128 bytes MN-major
+                const uint64_t ad = MODE == K3_GROUP_MM ? smem_desc_sw128(a_addr) : smem_desc_mn_sw128(a_addr, GT_A_BYTES / 2);
+                const uint64_t bd = W ? smem_desc_mn_sw128(b_addr, GT_A_BYTES / 2) : smem_desc_sw128(b_addr);
+                constexpr int a_step = MODE == K3_GROUP_MM ? 2 : 128, b_step = W ? 128 : 2;
+                const int kk_n = s == j.steps - 1 ? (j.last + 15) >> 4 : GT_BK / 16;
+                for (int kk = 0; kk < kk_n; ++kk)
+                    tc_mma_f16_pair(d, ad + a_step * kk, bd + b_step * kk, idesc, (s > 0 || kk > 0) ? 1u : 0u);
+                tc_commit_pair(smem_u32(empty + slot));
+            }
+            if (!ok) break;
+            tc_commit_pair(smem_u32(tfull + acc));
+            ++tc;
+        }
+        // every issued MMA completes before TMEM is released
+        tc_commit_pair(smem_u32(drain));
+        mbar_wait(smem_u32(drain), 0, 0xFFFFFFFFu);
+    } else if (W && warp == 2) {
+        // ------------------------------------------------------------ tails of the groups (each CTA its half)
+        uint32_t it = 0, tails = 0;
+        for (int job = first; job < jobs; job += stride) {
+            const GroupJob j = group_job<MODE>(args, s_off, s_tile, mb, cb, job);
+            it += j.steps;
+            if (j.steps == 0 || !(j.last & 15)) continue;
+            const int slot = (it - 1) % NS;
+            if (!pair_wait(smem_u32(tail + tails % NS), (tails / NS) & 1, abort_flag, args.status, 65)) break;
+            ++tails;
+            // rows last .. last rounded up to 16 of the four 64 x 64 boxes: a row is 128 bytes, whatever the swizzle
+            const int pad = 16 - (j.last & 15);
+            uint8_t *st = smem + slot * GT_STAGE;
+            for (int i = lane; i < pad * 32; i += 32) {
+                const int box = i / (pad * 8), q = i % (pad * 8);
+                *reinterpret_cast<uint4 *>(st + box * (GT_A_BYTES / 2) + (j.last + q / 8) * 128 + (q % 8) * 16) =
+                    make_uint4(0, 0, 0, 0);
+            }
+            asm volatile("fence.proxy.async;" ::: "memory");
+            __syncwarp();
+            if (lane == 0) mbar_arrive_cluster(cluster_addr(smem_u32(full + slot), 0));
+        }
+    } else if (warp >= 4) {
+        // ------------------------------------------------------------ epilogue (each CTA its 128 rows)
+        const int q = warp & 3, half = (warp - 4) >> 2;                  // TMEM lanes 32q .. 32q + 31
+        uint32_t tc = 0;
+        O *out = static_cast<O *>(args.out);
+        uint8_t *box = smem + SM::OFF_OUT + (warp - 4) * 2 * 4096;
+        uint32_t boxes = 0;
+        for (int job = first; job < jobs; job += stride) {
+            const GroupJob j = group_job<MODE>(args, s_off, s_tile, mb, cb, job);
+            const int m0 = j.m0 + 128 * (int)rank + 32 * q;
+            const bool none = W && j.steps == 0;                         // an expert without rows: zeros
+            if (none && args.accumulate) continue;
+            const int acc = (int)(tc & 1);
+            const uint32_t tbase = tmem + ((uint32_t)(32 * q) << 16) + acc * GT_TILE_N;
+            if (!none) {
+                if (!pair_wait(smem_u32(tfull + acc), (tc >> 1) & 1, abort_flag, args.status, 66)) break;
+                tc_fence_after();
+                ++tc;
+            }
+            if (W) {
+                constexpr int CW = 128 / (int)sizeof(O);                 // columns of a 128-byte box row
+                for (int c = half * 128; c < half * 128 + 128; c += CW) {
+                    if (m0 >= args.M || j.c0 + c >= args.Nc) continue;   // wholly outside
+                    uint8_t *b = box + (boxes & 1) * 4096;
+                    ++boxes;
+                    if (lane == 0) bulk_wait_read<1>();                  // this box's previous store has read it
+                    __syncwarp();
+#pragma unroll
+                    for (int h = 0; h < CW; h += 16) {
+                        uint32_t v[16] = {};
+                        if (!none) {
+                            tmem_ld16(tbase + c + h, v);
+                            tc_wait_ld();
+                        }
+                        // 16-byte pieces at the 128-byte swizzle's place: piece p of row r at p ^ (r % 8)
+#pragma unroll
+                        for (int p = 0; p < 16 * (int)sizeof(O) / 16; ++p) {
+                            uint4 w;
+                            if (sizeof(O) == 4) {
+                                w = make_uint4(v[4 * p], v[4 * p + 1], v[4 * p + 2], v[4 * p + 3]);
+                            } else {
+                                O o[8];
+#pragma unroll
+                                for (int i = 0; i < 8; ++i) o[i] = from_f32<O>(__uint_as_float(v[(8 * p + i) & 15]));
+                                w = *reinterpret_cast<uint4 *>(o);
+                            }
+                            const int piece = h * (int)sizeof(O) / 16 + p;
+                            *reinterpret_cast<uint4 *>(b + lane * 128 + ((piece ^ (lane & 7)) << 4)) = w;
+                        }
+                    }
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) {
+                        if (args.accumulate) tma_add_3d(&maps.out, smem_u32(b), j.c0 + c, m0, j.e);
+                        else tma_store_3d(&maps.out, smem_u32(b), j.c0 + c, m0, j.e);
+                        bulk_commit();
+                    }
+                }
+            } else {
+                const int m = m0 + lane;
+                for (int c = 16 * half; c < j.n; c += 32) {
+                    uint32_t v[16];
+                    tmem_ld16(tbase + c, v);
+                    tc_wait_ld();
+                    if (m < args.M) {
+                        O *o = out + (int64_t)(j.c0 + c) * args.ldo + m;
+#pragma unroll
+                        for (int i = 0; i < 16; ++i)
+                            if (c + i < j.n) o[i * args.ldo] = from_f32<O>(__uint_as_float(v[i]));
+                    }
+                }
+            }
+            if (!none) {
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive_cluster(cluster_addr(smem_u32(tempty + acc), 0));
+            }
+        }
+        if (W && lane == 0) bulk_wait<0>();
+    }
+    tc_fence_before();
+    __syncthreads();
+    // the issuer's last commit arrives in both CTAs: the other one waits for it too before it may exit
+    if (rank == 1 && threadIdx.x == 32) mbar_wait(smem_u32(drain), 0, 0xFFFFFFFFu);
+    cluster_sync();                                      // no arrival or MMA of the pair is outstanding past this
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc_pair(tmem, 512);
+    }
+}
+
+// ------------------------------------------------------------------ host
+typedef PFN_cuTensorMapEncodeTiled_v12000 EncodeFn;
+
+static EncodeFn encode_fn()
+{
+    static EncodeFn fn = nullptr;
+    if (!fn) {
+        void *p = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) == cudaSuccess &&
+            q == cudaDriverEntryPointSuccess)
+            fn = (EncodeFn)p;
+    }
+    return fn;
+}
+
+// Tiled map over `n2` matrices of [rows, cols] (n2 = 0: two dimensions), 128-byte swizzle.
+static bool encode(CUtensorMap *m, int type, const void *base, int64_t cols, int64_t rows, int64_t n2, int64_t ld,
+                   int64_t stride2, int box_cols, int box_rows)
+{
+    EncodeFn fn = encode_fn();
+    if (!fn) return false;
+    const int es = k3_type_bytes(type);
+    const CUtensorMapDataType dt = type == K3MOE_TYPE_F32    ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
+                                   : type == K3MOE_TYPE_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
+                                                             : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
+    cuuint64_t dims[3] = {(cuuint64_t)cols, (cuuint64_t)rows, (cuuint64_t)(n2 > 0 ? n2 : 1)};
+    cuuint64_t strides[2] = {(cuuint64_t)(ld * es), (cuuint64_t)(stride2 * es)};
+    cuuint32_t box[3] = {(cuuint32_t)box_cols, (cuuint32_t)box_rows, 1};
+    cuuint32_t one[3] = {1, 1, 1};
+    return fn(m, dt, n2 > 0 ? 3 : 2, const_cast<void *>(base), dims, strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
+              CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) ==
+           CUDA_SUCCESS;
+}
+
+template <int MODE, class O>
+static int launch_tc(const GroupMaps &maps, const GroupTcArgs &a, int64_t max_jobs, cudaStream_t st)
+{
+    using SM = GroupSmem<MODE>;
+    auto kern = group_tc_kernel<MODE, O>;
+    static unsigned long long attr_set = 0;
+    if (!k3_smem_attr(kern, SM::BYTES, attr_set)) return K3MOE_ERR_CUDA;
+    const int sms = k3_num_sms();
+    if (sms < 2) return K3MOE_ERR_CUDA;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim = {2, 1, 1};
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(2 * (unsigned)std::min<int64_t>(max_jobs, sms / 2));
+    cfg.blockDim = GT_THREADS;
+    cfg.dynamicSmemBytes = SM::BYTES;
+    cfg.stream = st;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    cudaLaunchKernelEx(&cfg, kern, maps, a);
+    k3_note_launch();
+    return cudaGetLastError() == cudaSuccess ? K3MOE_OK : K3MOE_ERR_CUDA;
+}
+
+template <int MODE>
+static int launch_typed(const GroupMaps &maps, const GroupTcArgs &a, int out_type, int64_t max_jobs, cudaStream_t st)
+{
+    if (out_type == K3MOE_TYPE_F32) return launch_tc<MODE, float>(maps, a, max_jobs, st);
+    if (out_type == K3MOE_TYPE_BF16) return launch_tc<MODE, __nv_bfloat16>(maps, a, max_jobs, st);
+    return launch_tc<MODE, __half>(maps, a, max_jobs, st);
+}
+
+}  // namespace k3
+
+using namespace k3;
+
+bool k3_group_tc_fits(int mode, const K3Group &g)
+{
+    if (mode == K3_GROUP_GRAD_W)
+        return g.rows > 0 && k3_rows16(g.a, g.lda, g.dtype) && k3_rows16(g.b, g.ldb, g.dtype) &&
+               k3_rows16(g.out, g.ldo, g.out_dtype) && (g.E == 1 || (g.stride_o * k3_type_bytes(g.out_dtype)) % 16 == 0);
+    return k3_rows16(g.a, g.lda, g.dtype) && k3_rows16(g.b, g.ldb, g.dtype) && (g.E == 1 || (g.stride_b * 2) % 16 == 0);
+}
+
+int k3_group_tc(int mode, const K3Group &g, cudaStream_t st)
+{
+    GroupMaps maps;
+    GroupTcArgs a = {};
+    a.offsets = g.offsets;
+    a.E = g.E;
+    a.rows = g.rows;
+    a.bf16 = g.dtype == K3MOE_TYPE_BF16;
+    a.accumulate = g.accumulate;
+    a.out = g.out;
+    a.ldo = g.ldo;
+    a.status = g.status;
+    bool ok = true;
+    if (mode == K3_GROUP_GRAD_W) {
+        a.M = g.n_out;
+        a.Nc = g.n_in;
+        a.expert_coord = 1;
+        const int64_t so = g.E > 1 ? g.stride_o : (int64_t)g.n_out * g.ldo;
+        ok = encode(&maps.a, g.dtype, g.a, g.n_out, g.rows, 0, g.lda, 0, 64, 64) &&
+             encode(&maps.b[0], g.dtype, g.b, g.n_in, g.rows, 0, g.ldb, 0, 64, 64) &&
+             encode(&maps.out, g.out_dtype, g.out, g.n_in, g.n_out, g.E, g.ldo, so, 128 / k3_type_bytes(g.out_dtype), 32);
+        for (int i = 1; i < 5; ++i) maps.b[i] = maps.b[0];
+        if (!ok) return K3MOE_ERR_CUDA;
+        const int64_t jobs = (int64_t)g.E * ((a.M + GT_TILE_M - 1) / GT_TILE_M) * ((a.Nc + GT_TILE_N - 1) / GT_TILE_N);
+        if (jobs >= (1LL << 31)) return K3MOE_ERR_SHAPE;
+        return launch_typed<K3_GROUP_GRAD_W>(maps, a, g.out_dtype, jobs, st);
+    }
+    const bool mm = mode == K3_GROUP_MM;
+    a.M = mm ? g.n_out : g.n_in;
+    a.K = mm ? g.n_in : g.n_out;
+    // one weight for all experts: a single matrix at coordinate 0
+    a.expert_coord = g.E > 1 && g.stride_b > 0;
+    const int64_t nw = a.expert_coord ? g.E : 1, sw = a.expert_coord ? g.stride_b : (int64_t)g.n_out * g.ldb;
+    ok = encode(&maps.a, g.dtype, g.b, g.n_in, g.n_out, nw, g.ldb, sw, 64, mm ? 128 : 64);
+    for (int i = 0; i < 5; ++i) ok = ok && encode(&maps.b[i], g.dtype, g.a, a.K, g.rows, 0, g.lda, 0, 64, 128 >> i);
+    maps.out = maps.a;
+    if (!ok) return K3MOE_ERR_CUDA;
+    // at most one partly filled tile an expert with rows
+    const int64_t jobs = ((int64_t)g.rows / GT_TILE_N + std::min(g.E, g.rows)) * ((a.M + GT_TILE_M - 1) / GT_TILE_M);
+    if (jobs >= (1LL << 31)) return K3MOE_ERR_SHAPE;
+    return mm ? launch_typed<K3_GROUP_MM>(maps, a, g.out_dtype, jobs, st)
+              : launch_typed<K3_GROUP_GRAD_X>(maps, a, g.out_dtype, jobs, st);
+}
