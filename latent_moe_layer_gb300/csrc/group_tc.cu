@@ -224,6 +224,8 @@ __global__ void __launch_bounds__(GT_THREADS, 1) group_tc_kernel(const __grid_co
                     ok = false;
                     break;
                 }
+                // a tail was written by threads of either CTA, not by the copy engine
+                if (W && s == j.steps - 1 && (j.last & 15)) asm volatile("fence.acq_rel.cluster;\n\tfence.proxy.async;" ::: "memory");
                 tc_fence_after();
                 const uint32_t a_addr = smem_u32(smem + slot * GT_STAGE), b_addr = a_addr + GT_A_BYTES;
                 // a step of 16 contraction values: 32 bytes along a K-major row, 16 rows of 128 bytes MN-major
