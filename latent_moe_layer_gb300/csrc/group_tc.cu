@@ -154,95 +154,107 @@ __global__ void __launch_bounds__(GT_THREADS, 1) group_tc_kernel(const __grid_co
     tc_fence_after();
     const uint32_t tmem = *tmem_holder;
 
-    if (warp == 0 && lane == 0) {
+    // The producer and issuer warps run their loops as whole warps, one elected lane doing the work.
+    if (warp == 0) {
         // ------------------------------------------------------------ TMA producer (each CTA its half)
-        prefetch_tmap(&maps.a);
-        for (int i = 0; i < (W ? 1 : 5); ++i) prefetch_tmap(&maps.b[i]);
-        uint32_t it = 0, tails = 0;
+        const bool one = elect_one();
+        if (one) {
+            prefetch_tmap(&maps.a);
+            for (int i = 0; i < (W ? 1 : 5); ++i) prefetch_tmap(&maps.b[i]);
+        }
+        const uint32_t full0 = cluster_addr(smem_u32(full), 0);
+        RingPos<NS> p, t;                                // stages; tails
+        uint32_t issued = 0;
         bool ok = true;
         for (int job = first; job < jobs && ok; job += stride) {
             const GroupJob j = group_job<MODE>(args, s_off, s_tile, mb, cb, job);
             const int half = W ? 128 : ((j.n + 15) & ~15) / 2;           // this CTA's share of B's rows
             const int m = j.m0 + 128 * (int)rank, e = args.expert_coord * j.e;
+            const int c = j.c0 + half * (int)rank, r0 = W ? s_off[j.e] : 0;
             const uint32_t bytes = GT_A_BYTES + half * 128;
-            for (int s = 0; s < j.steps; ++s, ++it) {
-                const int slot = it % NS;
-                if (!pair_wait(smem_u32(empty + slot), ((it / NS) & 1) ^ 1, abort_flag, args.status, 61)) {
+            for (int s = 0; s < j.steps; ++s, ++issued, p.next()) {
+                if (!pair_wait(smem_u32(empty + p.slot), p.phase ^ 1, abort_flag, args.status, 61)) {
                     ok = false;
                     break;
                 }
-                const uint32_t a_dst = smem_u32(smem + slot * GT_STAGE), b_dst = a_dst + GT_A_BYTES;
-                uint32_t bar = cluster_addr(smem_u32(full + slot), 0);
-                if (W && s == j.steps - 1 && (j.last & 15)) {
-                    // the tail warp zeroes the foreign rows before it arrives for this CTA
-                    bar = smem_u32(tail + tails % NS);
-                    ++tails;
-                    mbar_expect_tx(bar, bytes);
-                } else {
-                    mbar_expect_tx_cluster(bar, bytes);
-                }
+                const uint32_t a_dst = smem_u32(smem) + p.slot * GT_STAGE, b_dst = a_dst + GT_A_BYTES;
+                uint32_t bar = full0 + p.slot * 8;
+                const bool tailed = W && s == j.steps - 1 && (j.last & 15);
+                if (tailed) bar = smem_u32(tail + t.slot);
                 const int k = s * GT_BK;
-                if (MODE == K3_GROUP_MM) {
-                    tma_load_3d_pair(a_dst, &maps.a, bar, k, m, e);
-                } else if (MODE == K3_GROUP_GRAD_X) {
-                    tma_load_3d_pair(a_dst, &maps.a, bar, m, k, e);
-                    tma_load_3d_pair(a_dst + GT_A_BYTES / 2, &maps.a, bar, m + 64, k, e);
+                if (one) {
+                    // the tail warp zeroes a tail's foreign rows before it arrives for this CTA
+                    if (tailed) mbar_expect_tx(bar, bytes);
+                    else mbar_expect_tx_cluster(bar, bytes);
+                    if (MODE == K3_GROUP_MM) {
+                        tma_load_3d_pair(a_dst, &maps.a, bar, k, m, e);
+                    } else if (MODE == K3_GROUP_GRAD_X) {
+                        tma_load_3d_pair(a_dst, &maps.a, bar, m, k, e);
+                        tma_load_3d_pair(a_dst + GT_A_BYTES / 2, &maps.a, bar, m + 64, k, e);
+                    }
+                    if (!W) {
+                        load_rows(maps.b, b_dst, bar, k, c, half);
+                    } else {
+                        tma_load_2d_pair(a_dst, &maps.a, bar, m, r0 + k);
+                        tma_load_2d_pair(a_dst + GT_A_BYTES / 2, &maps.a, bar, m + 64, r0 + k);
+                        tma_load_2d_pair(b_dst, &maps.b[0], bar, c, r0 + k);
+                        tma_load_2d_pair(b_dst + GT_A_BYTES / 2, &maps.b[0], bar, c + 64, r0 + k);
+                    }
                 }
-                if (!W) {
-                    load_rows(maps.b, b_dst, bar, k, j.c0 + half * (int)rank, half);
-                } else {
-                    const int r = s_off[j.e] + k, c = j.c0 + 128 * (int)rank;
-                    tma_load_2d_pair(a_dst, &maps.a, bar, m, r);
-                    tma_load_2d_pair(a_dst + GT_A_BYTES / 2, &maps.a, bar, m + 64, r);
-                    tma_load_2d_pair(b_dst, &maps.b[0], bar, c, r);
-                    tma_load_2d_pair(b_dst + GT_A_BYTES / 2, &maps.b[0], bar, c + 64, r);
-                }
+                __syncwarp();
+                if (tailed) t.next();
             }
         }
-        // the pair's last releases of this CTA's slots land before it may exit
-        const uint32_t n = it < (uint32_t)NS ? it : (uint32_t)NS;
-        for (uint32_t q = 0; ok && q < n; ++q) {
-            const uint32_t i2 = it - 1 - q;
-            ok = pair_wait(smem_u32(empty + i2 % NS), (i2 / NS) & 1, abort_flag, args.status, 62);
+        // the last releases of this CTA's slots land before it may exit: a slot's next use would wait for them
+        for (uint32_t q = 0; ok && q < min(issued, (uint32_t)NS); ++q, p.next()) {
+            if (issued < (uint32_t)NS && q == 0) p.slot = 0, p.phase = 1;
+            ok = pair_wait(smem_u32(empty + p.slot), p.phase ^ 1, abort_flag, args.status, 62);
         }
-    } else if (warp == 1 && lane == 0 && rank == 0) {
+    } else if (warp == 1 && rank == 0) {
         // ------------------------------------------------------------ MMA issuer (even CTA, for both)
         const uint32_t major = (MODE == K3_GROUP_MM ? 0 : IDESC_A_MN) | (W ? IDESC_B_MN : 0);
-        uint32_t it = 0, tc = 0;
+        // a step of 16 contraction values: 32 bytes along a K-major row, 16 rows of 128 bytes MN-major
+        constexpr int a_step = MODE == K3_GROUP_MM ? 2 : 128, b_step = W ? 128 : 2;
+        const uint32_t a0 = smem_u32(smem);
+        const uint64_t ad0 = MODE == K3_GROUP_MM ? smem_desc_sw128(a0) : smem_desc_mn_sw128(a0, GT_A_BYTES / 2);
+        const uint64_t bd0 = W ? smem_desc_mn_sw128(a0 + GT_A_BYTES, GT_A_BYTES / 2) : smem_desc_sw128(a0 + GT_A_BYTES);
+        const bool one = elect_one();
+        RingPos<NS> p;
+        RingPos<2> acc;
         bool ok = true;
         for (int job = first; job < jobs && ok; job += stride) {
             const GroupJob j = group_job<MODE>(args, s_off, s_tile, mb, cb, job);
             if (W && j.steps == 0) continue;
             const uint32_t idesc = idesc_f16(GT_TILE_M, (j.n + 15) & ~15, args.bf16) | major;
-            const int acc = (int)(tc & 1);
-            if (!pair_wait(smem_u32(tempty + acc), ((tc >> 1) & 1) ^ 1, abort_flag, args.status, 63)) break;
+            if (!pair_wait(smem_u32(tempty + acc.slot), acc.phase ^ 1, abort_flag, args.status, 63)) break;
             tc_fence_after();
-            const uint32_t d = tmem + acc * GT_TILE_N;
-            for (int s = 0; s < j.steps; ++s, ++it) {
-                const int slot = it % NS;
-                if (!pair_wait(smem_u32(full + slot), (it / NS) & 1, abort_flag, args.status, 64)) {
+            const uint32_t d = tmem + acc.slot * GT_TILE_N;
+            for (int s = 0; s < j.steps; ++s, p.next()) {
+                if (!pair_wait(smem_u32(full + p.slot), p.phase, abort_flag, args.status, 64)) {
                     ok = false;
                     break;
                 }
+                const bool end = s == j.steps - 1;
                 // a tail was written by threads of either CTA, not by the copy engine
-                if (W && s == j.steps - 1 && (j.last & 15)) asm volatile("fence.acq_rel.cluster;\n\tfence.proxy.async;" ::: "memory");
+                if (W && end && (j.last & 15)) asm volatile("fence.acq_rel.cluster;\n\tfence.proxy.async;" ::: "memory");
                 tc_fence_after();
-                const uint32_t a_addr = smem_u32(smem + slot * GT_STAGE), b_addr = a_addr + GT_A_BYTES;
-                // a step of 16 contraction values: 32 bytes along a K-major row, 16 rows of 128 bytes MN-major
-                const uint64_t ad = MODE == K3_GROUP_MM ? smem_desc_sw128(a_addr) : smem_desc_mn_sw128(a_addr, GT_A_BYTES / 2);
-                const uint64_t bd = W ? smem_desc_mn_sw128(b_addr, GT_A_BYTES / 2) : smem_desc_sw128(b_addr);
-                constexpr int a_step = MODE == K3_GROUP_MM ? 2 : 128, b_step = W ? 128 : 2;
-                const int kk_n = s == j.steps - 1 ? (j.last + 15) >> 4 : GT_BK / 16;
-                for (int kk = 0; kk < kk_n; ++kk)
-                    tc_mma_f16_pair(d, ad + a_step * kk, bd + b_step * kk, idesc, (s > 0 || kk > 0) ? 1u : 0u);
-                tc_commit_pair(smem_u32(empty + slot));
+                const uint64_t ad = ad0 + p.slot * (GT_STAGE / 16), bd = bd0 + p.slot * (GT_STAGE / 16);
+                const int kk_n = end ? (j.last + 15) >> 4 : GT_BK / 16;
+                if (one) {
+#pragma unroll
+                    for (int kk = 0; kk < GT_BK / 16; ++kk)
+                        if (kk < kk_n)
+                            tc_mma_f16_pair(d, ad + a_step * kk, bd + b_step * kk, idesc, (s > 0 || kk > 0) ? 1u : 0u);
+                    tc_commit_pair(smem_u32(empty + p.slot));
+                    if (end) tc_commit_pair(smem_u32(tfull + acc.slot));
+                }
+                __syncwarp();
             }
-            if (!ok) break;
-            tc_commit_pair(smem_u32(tfull + acc));
-            ++tc;
+            acc.next();
         }
         // every issued MMA completes before TMEM is released
-        tc_commit_pair(smem_u32(drain));
+        if (one) tc_commit_pair(smem_u32(drain));
+        __syncwarp();
         mbar_wait(smem_u32(drain), 0, 0xFFFFFFFFu);
     } else if (W && warp == 2) {
         // ------------------------------------------------------------ tails of the groups (each CTA its half)

@@ -6,6 +6,28 @@
 
 namespace k3 {
 
+// One lane of a converged warp (the same at every call): single-thread instructions under it keep the
+// warp's control flow uniform.
+__device__ __forceinline__ bool elect_one()
+{
+    uint32_t r;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+    return r != 0;
+}
+
+// Slot and phase parity of a ring's next use.
+template <int NS>
+struct RingPos {
+    uint32_t slot = 0, phase = 0;
+    __device__ __forceinline__ void next()
+    {
+        if (++slot == NS) {
+            slot = 0;
+            phase ^= 1;
+        }
+    }
+};
+
 // Address of the same shared-memory offset in CTA `rank` of the cluster (shared::cluster window).
 __device__ __forceinline__ uint32_t cluster_addr(uint32_t saddr, uint32_t rank)
 {
