@@ -5,15 +5,6 @@
 
 namespace k3 {
 
-// Largest multiple-of-`round` split of n rows into the fewest tiles of at most `tile` rows: 300 rows
-// at tile 256 are two tiles of 160, not 256 + 44, so that both run at about the same rate.
-__device__ __forceinline__ int group_tile_width(int n, int tile, int round)
-{
-    const int t = (n + tile - 1) / tile;
-    if (t <= 1) return tile;
-    return min(tile, ((n + t - 1) / t + round - 1) / round * round);
-}
-
 // All threads of the CTA (a multiple of 32): s_off[0 .. E] = the offsets, s_tile[0 .. E] = exclusive
 // prefix of each expert's tiles of at most `tile` rows (none for an empty expert).  Returns false,
 // after recording K3MOE_ERR_RANGE, when the offsets decrease or leave [0, rows].  s_tmp: 34 ints.

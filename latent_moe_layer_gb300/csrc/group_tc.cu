@@ -24,13 +24,21 @@ namespace k3 {
 
 constexpr int GT_BK = 64, GT_TILE_M = 256, GT_TILE_N = 256;
 constexpr int GT_A_BYTES = 128 * GT_BK * 2, GT_STAGE = 2 * GT_A_BYTES;
-constexpr int GT_EPI_WARPS = 8, GT_THREADS = 128 + 32 * GT_EPI_WARPS;   // TMA, MMA, tail, idle, epilogue
+// grad_w: stages of one accumulation in TMEM (512 rows).  The tensor core truncates each sum it adds to
+// (1.2e-9 of the result a row: 3.8e-5 after 32,768 rows), so longer contractions are summed in registers
+// (error 5e-7 at any length).
+constexpr int GT_CHUNK = 8;
+// mm, grad_x: bytes of activation rows whose tiles pass under one block of weights before the next block
+constexpr int64_t GT_L2_ROWS = 32 << 20;
 
 template <int MODE>
 struct GroupSmem {
     static constexpr int NS = MODE == K3_GROUP_GRAD_W ? 5 : 6;
-    static constexpr int OFF_OUT = NS * GT_STAGE;                       // grad_w: two 4 KB output boxes a warp
-    static constexpr int OUT_BYTES = MODE == K3_GROUP_GRAD_W ? GT_EPI_WARPS * 2 * 4096 : 0;
+    // grad_w's epilogue keeps 64 sums a thread and writes every value in fp32: four warps a TMEM quarter
+    static constexpr int EPI_WARPS = MODE == K3_GROUP_GRAD_W ? 16 : 8;
+    static constexpr int THREADS = 96 + 32 * EPI_WARPS;                 // TMA, MMA, tails, epilogue
+    static constexpr int OFF_OUT = NS * GT_STAGE;                       // grad_w: a 4 KB output box a warp
+    static constexpr int OUT_BYTES = MODE == K3_GROUP_GRAD_W ? EPI_WARPS * 4096 : 0;
     static constexpr int OFF_BAR = OFF_OUT + OUT_BYTES;
     static constexpr int N_BAR = 3 * NS + 5;                            // full, empty, tail; tfull, tempty x 2; drain
     static constexpr int OFF_INT = OFF_BAR + N_BAR * 8 + 8;
@@ -50,6 +58,7 @@ struct GroupTcArgs {
     const int32_t *offsets;
     int E, rows, M, Nc;      // M: the tile-row extent; Nc: grad_w's column extent (n_in)
     int K;                   // contraction of mm and grad_x
+    int l2_tiles;            // row tiles of GT_L2_ROWS bytes
     int expert_coord;        // 0: one weight for all experts
     int bf16, accumulate;
     void *out;
@@ -58,38 +67,78 @@ struct GroupTcArgs {
 };
 
 struct GroupJob {
-    int e, m0, c0, n, steps, last;   // first row and column of the tile; columns; stages; contraction values of the last stage
+    int m0, c0, n, steps, last;      // first row and column of the tile; columns; stages; contraction values of the last stage
 };
 
+// A CTA pair's walk over the tiles: job indexes first, first + stride, ...  An expert's tiles are
+// consecutive, so that what they share stays in L2.
 template <int MODE>
-__device__ __forceinline__ GroupJob group_job(const GroupTcArgs &a, const int *s_off, const int *s_tile, int mb, int cb,
-                                              int job)
-{
-    GroupJob j;
-    if (MODE == K3_GROUP_GRAD_W) {
-        // expert by expert, so that its rows of dy and x stay in L2
-        j.e = job / (mb * cb);
-        const int w = job - j.e * mb * cb;
-        j.m0 = (w / cb) * GT_TILE_M;
-        j.c0 = (w % cb) * GT_TILE_N;
-        j.n = GT_TILE_N;
-        const int k = s_off[j.e + 1] - s_off[j.e];
-        j.steps = (k + GT_BK - 1) / GT_BK;
-        j.last = k - (j.steps - 1) * GT_BK;
-    } else {
-        // an expert's row tiles next to each other on the same block of weights
-        j.e = group_find(s_tile, a.E, job / mb);
-        const int w = job - s_tile[j.e] * mb, t = s_tile[j.e + 1] - s_tile[j.e];
-        const int rows = s_off[j.e + 1] - s_off[j.e], width = group_tile_width(rows, GT_TILE_N, 16);
-        j.m0 = (w / t) * GT_TILE_M;
-        const int first = (w % t) * width;
-        j.c0 = s_off[j.e] + first;
-        j.n = min(width, rows - first);
-        j.steps = (a.K + GT_BK - 1) / GT_BK;
-        j.last = a.K - (j.steps - 1) * GT_BK;
+struct GroupWalk {
+    const GroupTcArgs &a;
+    const int *s_off, *s_tile;
+    const int mb, cb, jobs, stride;
+    int job, e = -1, begin = 0, end = 0, off0 = 0, rows = 0;     // the current expert, its job range and rows
+
+    __device__ __forceinline__ GroupWalk(const GroupTcArgs &a_, const int *so, const int *st, int mb_, int cb_, int jobs_)
+        : a(a_), s_off(so), s_tile(st), mb(mb_), cb(cb_), jobs(jobs_), stride((int)ncluster_x()), job((int)cluster_id_x())
+    {
+        enter();
     }
-    return j;
-}
+    __device__ __forceinline__ bool valid() const { return job < jobs; }
+    __device__ __forceinline__ void next()
+    {
+        job += stride;
+        enter();
+    }
+    __device__ __forceinline__ void enter()
+    {
+        if (job < end || job >= jobs) return;
+        if (MODE == K3_GROUP_GRAD_W) {
+            e = job / (mb * cb);
+            begin = e * mb * cb;
+            end = begin + mb * cb;
+        } else {
+            // the next expert as a rule, a search where experts are smaller than the stride
+            if (e + 1 < a.E && job < s_tile[e + 2] * mb) ++e;
+            else e = group_find(s_tile, a.E, job / mb);
+            begin = s_tile[e] * mb;
+            end = s_tile[e + 1] * mb;
+        }
+        off0 = s_off[e];
+        rows = s_off[e + 1] - off0;
+    }
+    __device__ __forceinline__ GroupJob get() const
+    {
+        GroupJob j;
+        int w = job - begin;
+        if (MODE == K3_GROUP_GRAD_W) {
+            j.m0 = (w / cb) * GT_TILE_M;
+            j.c0 = (w % cb) * GT_TILE_N;
+            j.n = GT_TILE_N;
+            j.steps = (rows + GT_BK - 1) / GT_BK;
+            j.last = rows - (j.steps - 1) * GT_BK;
+        } else {
+            // row tiles (in groups that fit the L2) next to each other on the same block of weights
+            int t = s_tile[e + 1] - s_tile[e], first = 0;
+            const int all = t;
+            if (t > a.l2_tiles) {
+                const int g = w / (a.l2_tiles * mb);
+                first = g * a.l2_tiles;
+                w -= first * mb;
+                t = min(a.l2_tiles, t - first);
+            }
+            j.m0 = (w / t) * GT_TILE_M;
+            const int i = first + w % t;
+            // an expert's tiles differ by at most 16 rows: 585 rows are 208 + 192 + 185, not 256 + 256 + 73
+            const int units = (rows + 15) >> 4, u = units / all, more = units - u * all;
+            j.c0 = off0 + 16 * (i * u + min(i, more));
+            j.n = min(16 * (u + (i < more)), off0 + rows - j.c0);
+            j.steps = (a.K + GT_BK - 1) / GT_BK;
+            j.last = a.K - (j.steps - 1) * GT_BK;
+        }
+        return j;
+    }
+};
 
 // `rows` (a multiple of 8, at most 128) rows of B from row `row`: boxes of 128 .. 8 rows, largest first.
 __device__ __forceinline__ void load_rows(const CUtensorMap *maps, uint32_t dst, uint32_t bar, int k, int row, int rows)
@@ -106,7 +155,7 @@ __device__ __forceinline__ void load_rows(const CUtensorMap *maps, uint32_t dst,
 }
 
 template <int MODE, class O>
-__global__ void __launch_bounds__(GT_THREADS, 1) group_tc_kernel(const __grid_constant__ GroupMaps maps,
+__global__ void __launch_bounds__(GroupSmem<MODE>::THREADS, 1) group_tc_kernel(const __grid_constant__ GroupMaps maps,
                                                                  const GroupTcArgs args)
 {
     griddep_enter();
@@ -125,13 +174,12 @@ __global__ void __launch_bounds__(GT_THREADS, 1) group_tc_kernel(const __grid_co
     const uint32_t rank = cluster_ctarank();
 
     // every CTA reads the same offsets, so all agree on a refusal
-    if (W ? !group_offsets_ok<GT_THREADS>(args.offsets, args.E, args.rows, args.status)
-          : !group_tiles<GT_THREADS>(args.offsets, args.E, args.rows, GT_TILE_N, s_int, s_tile,
+    if (W ? !group_offsets_ok<SM::THREADS>(args.offsets, args.E, args.rows, args.status)
+          : !group_tiles<SM::THREADS>(args.offsets, args.E, args.rows, GT_TILE_N, s_int, s_tile,
                                      s_tile + K3MOE_TRAIN_MAX_EXPERTS + 1, args.status))
         return;
     const int mb = (args.M + GT_TILE_M - 1) / GT_TILE_M, cb = W ? (args.Nc + GT_TILE_N - 1) / GT_TILE_N : 1;
     const int jobs = W ? args.E * mb * cb : s_tile[args.E] * mb;
-    const int first = (int)cluster_id_x(), stride = (int)ncluster_x();
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < NS; ++i) {
@@ -141,7 +189,7 @@ __global__ void __launch_bounds__(GT_THREADS, 1) group_tc_kernel(const __grid_co
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(smem_u32(tfull + i), 1);
-            mbar_init(smem_u32(tempty + i), 2 * GT_EPI_WARPS);
+            mbar_init(smem_u32(tempty + i), 2 * SM::EPI_WARPS);
         }
         mbar_init(smem_u32(drain), 1);
         *abort_flag = 0;
@@ -166,11 +214,11 @@ __global__ void __launch_bounds__(GT_THREADS, 1) group_tc_kernel(const __grid_co
         RingPos<NS> p, t;                                // stages; tails
         uint32_t issued = 0;
         bool ok = true;
-        for (int job = first; job < jobs && ok; job += stride) {
-            const GroupJob j = group_job<MODE>(args, s_off, s_tile, mb, cb, job);
+        for (GroupWalk<MODE> walk(args, s_off, s_tile, mb, cb, jobs); walk.valid() && ok; walk.next()) {
+            const GroupJob j = walk.get();
             const int half = W ? 128 : ((j.n + 15) & ~15) / 2;           // this CTA's share of B's rows
-            const int m = j.m0 + 128 * (int)rank, e = args.expert_coord * j.e;
-            const int c = j.c0 + half * (int)rank, r0 = W ? s_off[j.e] : 0;
+            const int m = j.m0 + 128 * (int)rank, e = args.expert_coord * walk.e;
+            const int c = j.c0 + half * (int)rank, r0 = walk.off0;
             const uint32_t bytes = GT_A_BYTES + half * 128;
             for (int s = 0; s < j.steps; ++s, ++issued, p.next()) {
                 if (!pair_wait(smem_u32(empty + p.slot), p.phase ^ 1, abort_flag, args.status, 61)) {
@@ -222,35 +270,35 @@ __global__ void __launch_bounds__(GT_THREADS, 1) group_tc_kernel(const __grid_co
         RingPos<NS> p;
         RingPos<2> acc;
         bool ok = true;
-        for (int job = first; job < jobs && ok; job += stride) {
-            const GroupJob j = group_job<MODE>(args, s_off, s_tile, mb, cb, job);
-            if (W && j.steps == 0) continue;
+        for (GroupWalk<MODE> walk(args, s_off, s_tile, mb, cb, jobs); walk.valid() && ok; walk.next()) {
+            const GroupJob j = walk.get();
             const uint32_t idesc = idesc_f16(GT_TILE_M, (j.n + 15) & ~15, args.bf16) | major;
-            if (!pair_wait(smem_u32(tempty + acc.slot), acc.phase ^ 1, abort_flag, args.status, 63)) break;
-            tc_fence_after();
-            const uint32_t d = tmem + acc.slot * GT_TILE_N;
             for (int s = 0; s < j.steps; ++s, p.next()) {
-                if (!pair_wait(smem_u32(full + p.slot), p.phase, abort_flag, args.status, 64)) {
-                    ok = false;
-                    break;
+                const bool begin = s == 0 || (W && s % GT_CHUNK == 0), last = s == j.steps - 1;
+                const bool end = last || (W && (s + 1) % GT_CHUNK == 0);
+                if (begin) {
+                    ok = pair_wait(smem_u32(tempty + acc.slot), acc.phase ^ 1, abort_flag, args.status, 63);
+                    tc_fence_after();
                 }
-                const bool end = s == j.steps - 1;
+                ok = ok && pair_wait(smem_u32(full + p.slot), p.phase, abort_flag, args.status, 64);
+                if (!ok) break;
                 // a tail was written by threads of either CTA, not by the copy engine
-                if (W && end && (j.last & 15)) asm volatile("fence.acq_rel.cluster;\n\tfence.proxy.async;" ::: "memory");
+                if (W && last && (j.last & 15)) mbar_try_wait_cluster(smem_u32(full + p.slot), p.phase);
                 tc_fence_after();
+                const uint32_t d = tmem + acc.slot * GT_TILE_N;
                 const uint64_t ad = ad0 + p.slot * (GT_STAGE / 16), bd = bd0 + p.slot * (GT_STAGE / 16);
-                const int kk_n = end ? (j.last + 15) >> 4 : GT_BK / 16;
+                const int kk_n = last ? (j.last + 15) >> 4 : GT_BK / 16;
                 if (one) {
 #pragma unroll
                     for (int kk = 0; kk < GT_BK / 16; ++kk)
                         if (kk < kk_n)
-                            tc_mma_f16_pair(d, ad + a_step * kk, bd + b_step * kk, idesc, (s > 0 || kk > 0) ? 1u : 0u);
+                            tc_mma_f16_pair(d, ad + a_step * kk, bd + b_step * kk, idesc, (!begin || kk > 0) ? 1u : 0u);
                     tc_commit_pair(smem_u32(empty + p.slot));
                     if (end) tc_commit_pair(smem_u32(tfull + acc.slot));
                 }
                 __syncwarp();
+                if (end) acc.next();
             }
-            acc.next();
         }
         // every issued MMA completes before TMEM is released
         if (one) tc_commit_pair(smem_u32(drain));
@@ -258,89 +306,111 @@ __global__ void __launch_bounds__(GT_THREADS, 1) group_tc_kernel(const __grid_co
         mbar_wait(smem_u32(drain), 0, 0xFFFFFFFFu);
     } else if (W && warp == 2) {
         // ------------------------------------------------------------ tails of the groups (each CTA its half)
-        uint32_t it = 0, tails = 0;
-        for (int job = first; job < jobs; job += stride) {
-            const GroupJob j = group_job<MODE>(args, s_off, s_tile, mb, cb, job);
+        RingPos<NS> t;
+        uint32_t it = 0;
+        for (GroupWalk<MODE> walk(args, s_off, s_tile, mb, cb, jobs); walk.valid(); walk.next()) {
+            const GroupJob j = walk.get();
             it += j.steps;
             if (j.steps == 0 || !(j.last & 15)) continue;
             const int slot = (it - 1) % NS;
-            if (!pair_wait(smem_u32(tail + tails % NS), (tails / NS) & 1, abort_flag, args.status, 65)) break;
-            ++tails;
-            // rows last .. last rounded up to 16 of the four 64 x 64 boxes: a row is 128 bytes, whatever the swizzle
-            const int pad = 16 - (j.last & 15);
-            uint8_t *st = smem + slot * GT_STAGE;
-            for (int i = lane; i < pad * 32; i += 32) {
-                const int box = i / (pad * 8), q = i % (pad * 8);
-                *reinterpret_cast<uint4 *>(st + box * (GT_A_BYTES / 2) + (j.last + q / 8) * 128 + (q % 8) * 16) =
-                    make_uint4(0, 0, 0, 0);
-            }
-            asm volatile("fence.proxy.async;" ::: "memory");
+            if (!pair_wait(smem_u32(tail + t.slot), t.phase, abort_flag, args.status, 65)) break;
+            t.next();
+            // rows last .. last rounded up to 16 of the four 64 x 64 boxes, eight lanes a row: a row is 128
+            // bytes, whatever the swizzle
+            uint8_t *st = smem + slot * GT_STAGE + (lane >> 3) * (GT_A_BYTES / 2) + (lane & 7) * 16;
+            for (int r = j.last; r & 15; ++r) *reinterpret_cast<uint4 *>(st + r * 128) = make_uint4(0, 0, 0, 0);
+            fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) mbar_arrive_cluster(cluster_addr(smem_u32(full + slot), 0));
         }
-    } else if (warp >= 4) {
+    } else if (warp >= 3) {
         // ------------------------------------------------------------ epilogue (each CTA its 128 rows)
-        const int q = warp & 3, half = (warp - 4) >> 2;                  // TMEM lanes 32q .. 32q + 31
-        uint32_t tc = 0;
+        constexpr int PARTS = SM::EPI_WARPS / 4, COLS = GT_TILE_N / PARTS;
+        const int q = warp & 3, part = (warp - 3) >> 2;                  // TMEM lanes 32q .. 32q + 31
+        const uint32_t tbase = tmem + ((uint32_t)(32 * q) << 16);
+        const uint32_t tempty0 = cluster_addr(smem_u32(tempty), 0);
+        RingPos<2> acc;
         O *out = static_cast<O *>(args.out);
-        uint8_t *box = smem + SM::OFF_OUT + (warp - 4) * 2 * 4096;
-        uint32_t boxes = 0;
-        for (int job = first; job < jobs; job += stride) {
-            const GroupJob j = group_job<MODE>(args, s_off, s_tile, mb, cb, job);
+        uint8_t *box = smem + SM::OFF_OUT + (warp - 3) * 4096;
+        bool ok = true;
+        for (GroupWalk<MODE> walk(args, s_off, s_tile, mb, cb, jobs); walk.valid() && ok; walk.next()) {
+            const GroupJob j = walk.get();
             const int m0 = j.m0 + 128 * (int)rank + 32 * q;
-            const bool none = W && j.steps == 0;                         // an expert without rows: zeros
-            if (none && args.accumulate) continue;
-            const int acc = (int)(tc & 1);
-            const uint32_t tbase = tmem + ((uint32_t)(32 * q) << 16) + acc * GT_TILE_N;
-            if (!none) {
-                if (!pair_wait(smem_u32(tfull + acc), (tc >> 1) & 1, abort_flag, args.status, 66)) break;
-                tc_fence_after();
-                ++tc;
-            }
             if (W) {
                 constexpr int CW = 128 / (int)sizeof(O);                 // columns of a 128-byte box row
-                for (int c = half * 128; c < half * 128 + 128; c += CW) {
-                    if (m0 >= args.M || j.c0 + c >= args.Nc) continue;   // wholly outside
-                    uint8_t *b = box + (boxes & 1) * 4096;
-                    ++boxes;
-                    if (lane == 0) bulk_wait_read<1>();                  // this box's previous store has read it
-                    __syncwarp();
+                const int chunks = (j.steps + GT_CHUNK - 1) / GT_CHUNK;
+                if (chunks == 0 && args.accumulate) continue;            // an expert without rows: nothing, or zeros
+                float sum[COLS];
+                for (int ch = 0; ch < chunks; ++ch) {
+                    ok = pair_wait(smem_u32(tfull + acc.slot), acc.phase, abort_flag, args.status, 66);
+                    if (!ok) break;
+                    tc_fence_after();
+                    if (chunks == 1) break;                              // stored from TMEM below
 #pragma unroll
-                    for (int h = 0; h < CW; h += 16) {
-                        uint32_t v[16] = {};
-                        if (!none) {
-                            tmem_ld16(tbase + c + h, v);
-                            tc_wait_ld();
-                        }
-                        // 16-byte pieces at the 128-byte swizzle's place: piece p of row r at p ^ (r % 8)
+                    for (int g = 0; g < COLS / 8; ++g) {
+                        uint32_t v[8];
+                        tmem_ld8(tbase + acc.slot * GT_TILE_N + part * COLS + 8 * g, v);
+                        tc_wait_ld();
 #pragma unroll
-                        for (int p = 0; p < 16 * (int)sizeof(O) / 16; ++p) {
-                            uint4 w;
-                            if (sizeof(O) == 4) {
-                                w = make_uint4(v[4 * p], v[4 * p + 1], v[4 * p + 2], v[4 * p + 3]);
-                            } else {
-                                O o[8];
-#pragma unroll
-                                for (int i = 0; i < 8; ++i) o[i] = from_f32<O>(__uint_as_float(v[(8 * p + i) & 15]));
-                                w = *reinterpret_cast<uint4 *>(o);
-                            }
-                            const int piece = h * (int)sizeof(O) / 16 + p;
-                            *reinterpret_cast<uint4 *>(b + lane * 128 + ((piece ^ (lane & 7)) << 4)) = w;
-                        }
+                        for (int i = 0; i < 8; ++i)
+                            sum[8 * g + i] = (ch ? sum[8 * g + i] : 0.f) + __uint_as_float(v[i]);
                     }
-                    fence_proxy_async_smem();
+                    tc_fence_before();
                     __syncwarp();
-                    if (lane == 0) {
-                        if (args.accumulate) tma_add_3d(&maps.out, smem_u32(b), j.c0 + c, m0, j.e);
-                        else tma_store_3d(&maps.out, smem_u32(b), j.c0 + c, m0, j.e);
-                        bulk_commit();
+                    if (lane == 0) mbar_arrive_cluster(tempty0 + acc.slot * 8);
+                    acc.next();
+                }
+                if (!ok) break;
+#pragma unroll
+                for (int g0 = 0; g0 < COLS; g0 += CW) {
+                    const int c = part * COLS + g0;
+                    if (m0 < args.M && j.c0 + c < args.Nc) {             // else wholly outside
+                        if (lane == 0) bulk_wait_read<0>();              // the box's previous store has read it
+                        __syncwarp();
+#pragma unroll
+                        for (int h = 0; h < CW; h += 16) {
+                            uint32_t v[16] = {};
+                            if (chunks == 1) {
+                                tmem_ld16(tbase + acc.slot * GT_TILE_N + c + h, v);
+                                tc_wait_ld();
+                            } else if (chunks > 1) {
+#pragma unroll
+                                for (int i = 0; i < 16; ++i) v[i] = __float_as_uint(sum[g0 + h + i]);
+                            }
+                            // 16-byte pieces at the 128-byte swizzle's place: piece p of row r at p ^ (r % 8)
+#pragma unroll
+                            for (int p = 0; p < (int)sizeof(O); ++p) {
+                                uint4 w;
+                                if (sizeof(O) == 4) {
+                                    w = make_uint4(v[(4 * p) & 15], v[(4 * p + 1) & 15], v[(4 * p + 2) & 15], v[(4 * p + 3) & 15]);
+                                } else {
+                                    O o[8];
+#pragma unroll
+                                    for (int i = 0; i < 8; ++i) o[i] = from_f32<O>(__uint_as_float(v[(8 * p + i) & 15]));
+                                    w = *reinterpret_cast<uint4 *>(o);
+                                }
+                                const int piece = h * (int)sizeof(O) / 16 + p;
+                                *reinterpret_cast<uint4 *>(box + lane * 128 + ((piece ^ (lane & 7)) << 4)) = w;
+                            }
+                        }
+                        fence_proxy_async_smem();
+                        __syncwarp();
+                        if (lane == 0) {
+                            if (args.accumulate) tma_add_3d(&maps.out, smem_u32(box), j.c0 + c, m0, walk.e);
+                            else tma_store_3d(&maps.out, smem_u32(box), j.c0 + c, m0, walk.e);
+                            bulk_commit();
+                        }
                     }
                 }
+                if (chunks != 1) continue;
             } else {
+                ok = pair_wait(smem_u32(tfull + acc.slot), acc.phase, abort_flag, args.status, 66);
+                if (!ok) break;
+                tc_fence_after();
                 const int m = m0 + lane;
-                for (int c = 16 * half; c < j.n; c += 32) {
+                for (int c = 16 * part; c < j.n; c += 16 * PARTS) {
                     uint32_t v[16];
-                    tmem_ld16(tbase + c, v);
+                    tmem_ld16(tbase + acc.slot * GT_TILE_N + c, v);
                     tc_wait_ld();
                     if (m < args.M) {
                         O *o = out + (int64_t)(j.c0 + c) * args.ldo + m;
@@ -350,11 +420,10 @@ __global__ void __launch_bounds__(GT_THREADS, 1) group_tc_kernel(const __grid_co
                     }
                 }
             }
-            if (!none) {
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive_cluster(cluster_addr(smem_u32(tempty + acc), 0));
-            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_cluster(tempty0 + acc.slot * 8);
+            acc.next();
         }
         if (W && lane == 0) bulk_wait<0>();
     }
@@ -420,7 +489,7 @@ static int launch_tc(const GroupMaps &maps, const GroupTcArgs &a, int64_t max_jo
     attr[1].val.clusterDim = {2, 1, 1};
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(2 * (unsigned)std::min<int64_t>(max_jobs, sms / 2));
-    cfg.blockDim = GT_THREADS;
+    cfg.blockDim = SM::THREADS;
     cfg.dynamicSmemBytes = SM::BYTES;
     cfg.stream = st;
     cfg.attrs = attr;
@@ -482,6 +551,7 @@ int k3_group_tc(int mode, const K3Group &g, cudaStream_t st)
     a.K = mm ? g.n_in : g.n_out;
     // one weight for all experts: a single matrix at coordinate 0
     a.expert_coord = g.E > 1 && g.stride_b > 0;
+    a.l2_tiles = (int)std::max<int64_t>(1, GT_L2_ROWS / ((int64_t)GT_TILE_N * a.K * 2));
     const int64_t nw = a.expert_coord ? g.E : 1, sw = a.expert_coord ? g.stride_b : (int64_t)g.n_out * g.ldb;
     ok = encode(&maps.a, g.dtype, g.b, g.n_in, g.n_out, nw, g.ldb, sw, 64, mm ? 128 : 64);
     for (int i = 0; i < 5; ++i) ok = ok && encode(&maps.b[i], g.dtype, g.a, a.K, g.rows, 0, g.lda, 0, 64, 128 >> i);
