@@ -6,7 +6,8 @@
 namespace k3 {
 
 struct DropArgs {
-    uint32_t key0, key1, off0, off1;      // seed, offset
+    uint32_t key[10][2];                  // the rounds' keys: seed + round x the generator's two increments
+    uint32_t off0, off1;                  // offset
     uint32_t threshold;                   // keep where the word is at least this: floor(p 2^32)
     float scale;                          // 1 / (1 - p)
 };
@@ -14,16 +15,14 @@ struct DropArgs {
 // Philox4x32-10 (Salmon, Moraes, Dror and Shaw 2011): ten rounds of two 32 x 32 -> 64-bit products.
 __device__ __forceinline__ uint4 philox(uint64_t block, const DropArgs &a)
 {
-    uint32_t x0 = (uint32_t)block, x1 = (uint32_t)(block >> 32), x2 = a.off0, x3 = a.off1, k0 = a.key0, k1 = a.key1;
+    uint32_t x0 = (uint32_t)block, x1 = (uint32_t)(block >> 32), x2 = a.off0, x3 = a.off1;
 #pragma unroll
     for (int r = 0; r < 10; ++r) {
         const uint64_t p = (uint64_t)x0 * 0xD2511F53u, q = (uint64_t)x2 * 0xCD9E8D57u;
-        x0 = (uint32_t)(q >> 32) ^ x1 ^ k0;
+        x0 = (uint32_t)(q >> 32) ^ x1 ^ a.key[r][0];
         x1 = (uint32_t)q;
-        x2 = (uint32_t)(p >> 32) ^ x3 ^ k1;
+        x2 = (uint32_t)(p >> 32) ^ x3 ^ a.key[r][1];
         x3 = (uint32_t)p;
-        k0 += 0x9E3779B9u;
-        k1 += 0xBB67AE85u;
     }
     return make_uint4(x0, x1, x2, x3);
 }
@@ -87,7 +86,23 @@ __global__ void __launch_bounds__(256) dropout_kernel(const T *x, const T *res, 
 }
 
 // ------------------------------------------------------------------ gated unit
-__device__ __forceinline__ float sigmoid(float g) { return 1.0f / (1.0f + __expf(-g)); }
+// Results are rounded to 16 bits, so hardware exponential and reciprocal (a few 2^-22) suffice; an
+// infinite exponential gives the exact limits 0 and 1.
+__device__ __forceinline__ float sigmoid(float g) { return __fdividef(1.0f, 1.0f + __expf(-g)); }
+
+// tanh x within 3e-7, relative also near 0: Lambert's continued fraction x / (1 + x^2 / (3 + x^2 / (5 + x^2 / (7 +
+// x^2 / 9)))) as one quotient up to |x| = 1 (off by 6e-8 there), (e^2x - 1) / (e^2x + 1) beyond.
+__device__ __forceinline__ float tanh_quotient(float x)
+{
+    const float x2 = x * x;
+    float num = x * fmaf(x2, x2 + 105.0f, 945.0f), den = fmaf(x2, fmaf(15.0f, x2, 420.0f), 945.0f);
+    if (fabsf(x) > 1.0f) {
+        const float e = __expf(2.0f * fminf(fmaxf(x, -10.0f), 10.0f));      // tanh 10 is 1 in fp32
+        num = e - 1.0f;
+        den = e + 1.0f;
+    }
+    return x != x ? x : __fdividef(num, den);
+}
 
 // a(g, u) and its derivatives: SiLU a = g s u, or the soft-limited a = s f h with f = beta tanh(g /
 // beta), h = linear_beta tanh(u / linear_beta), s = sigmoid(g).
@@ -96,7 +111,7 @@ __device__ __forceinline__ float glu_value(float g, float u, const K3Act &c)
 {
     const float s = sigmoid(g);
     if (ACT == K3MOE_ACT_SILU) return g * s * u;
-    return s * (c.beta * tanhf(g * c.inv_beta)) * (c.linear_beta * tanhf(u * c.inv_linear_beta));
+    return s * (c.beta * tanh_quotient(g * c.inv_beta)) * (c.linear_beta * tanh_quotient(u * c.inv_linear_beta));
 }
 
 template <int ACT>
@@ -107,7 +122,7 @@ __device__ __forceinline__ void glu_slopes(float g, float u, const K3Act &c, flo
         dg = u * (s + g * s * (1.0f - s));
         du = g * s;
     } else {
-        const float tg = tanhf(g * c.inv_beta), tu = tanhf(u * c.inv_linear_beta);
+        const float tg = tanh_quotient(g * c.inv_beta), tu = tanh_quotient(u * c.inv_linear_beta);
         const float f = c.beta * tg, h = c.linear_beta * tu;
         dg = h * (s * (1.0f - s) * f + s * (1.0f - tg * tg));
         du = s * f * (1.0f - tu * tu);
@@ -174,8 +189,14 @@ using namespace k3;
 static bool drop_args(double p, uint64_t seed, uint64_t offset, DropArgs &a)
 {
     if (!(p >= 0.0 && p < 1.0)) return false;
-    a = {(uint32_t)seed, (uint32_t)(seed >> 32), (uint32_t)offset, (uint32_t)(offset >> 32), (uint32_t)(p * 4294967296.0),
-         (float)(1.0 / (1.0 - p))};
+    for (uint32_t r = 0; r < 10; ++r) {
+        a.key[r][0] = (uint32_t)seed + r * 0x9E3779B9u;
+        a.key[r][1] = (uint32_t)(seed >> 32) + r * 0xBB67AE85u;
+    }
+    a.off0 = (uint32_t)offset;
+    a.off1 = (uint32_t)(offset >> 32);
+    a.threshold = (uint32_t)(p * 4294967296.0);
+    a.scale = (float)(1.0 / (1.0 - p));
     return true;
 }
 

@@ -159,6 +159,8 @@ __global__ void __launch_bounds__(256) rows_gather_kernel(const T *__restrict__ 
 }
 
 // ------------------------------------------------------------------ combine
+// A warp per token and 32 V columns, so that nothing but memory keeps a warp waiting: the lanes hold the
+// token's rows and weights, and only rows that exist are loaded, eight in flight, summed in k order.
 template <class T, int V>
 __global__ void __launch_bounds__(256) rows_combine_kernel(const T *__restrict__ y, int64_t ldy, int n_rows,
                                                            const int32_t *__restrict__ pos,
@@ -166,31 +168,45 @@ __global__ void __launch_bounds__(256) rows_combine_kernel(const T *__restrict__
                                                            T *__restrict__ z, int64_t ldz, int *status)
 {
     griddep_enter();
-    for (int t = blockIdx.x; t < T_; t += gridDim.x) {
-        const int32_t *row = pos + (int64_t)t * K;
-        const float *wt = wts ? wts + (int64_t)t * K : nullptr;
-        for (int i = blockIdx.y * blockDim.x + threadIdx.x; i < nv; i += gridDim.y * blockDim.x) {
-            float acc[V] = {};
-            for (int kb = 0; kb < K; kb += 8) {               // eight rows' loads in flight, summed in k order
+    const int lane = threadIdx.x & 31, chunks = (nv + 31) / 32;
+    const int64_t work = (int64_t)T_ * chunks, step = (int64_t)gridDim.x * 8;
+    for (int64_t u = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5); u < work; u += step) {
+        const int t = (int)(u / chunks), i = (int)(u - (int64_t)t * chunks) * 32 + lane;
+        const bool in = i < nv;
+        float acc[V] = {};
+        for (int kb = 0; kb < K; kb += 32) {
+            int row = -1;
+            float w = 0.f;
+            if (kb + lane < K) {
+                row = __ldg(pos + (int64_t)t * K + kb + lane);
+                w = wts ? __ldg(wts + (int64_t)t * K + kb + lane) : 1.0f;
+                if (row >= n_rows) {
+                    set_status(status, K3MOE_ERR_RANGE, row);
+                    row = -1;
+                }
+            }
+            uint32_t live = __ballot_sync(0xffffffffu, row >= 0);
+            while (live) {
                 Vec<T, V> v[8];
-                int r[8];
+                float f[8];
+                const int n = __popc(live);
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
-                    r[j] = kb + j < K ? __ldg(row + kb + j) : -1;
-                    if (r[j] >= n_rows) {
-                        if (i == 0) set_status(status, K3MOE_ERR_RANGE, r[j]);
-                        r[j] = -1;
-                    }
-                    if (r[j] >= 0) v[j] = *reinterpret_cast<const Vec<T, V> *>(y + r[j] * ldy + (int64_t)i * V);
+                    if (j >= n) break;
+                    const int k = __ffs(live) - 1;
+                    live &= live - 1;
+                    const int r = __shfl_sync(0xffffffffu, row, k);
+                    f[j] = __shfl_sync(0xffffffffu, w, k);
+                    if (in) v[j] = *reinterpret_cast<const Vec<T, V> *>(y + r * ldy + (int64_t)i * V);
                 }
 #pragma unroll
                 for (int j = 0; j < 8; ++j)
-                    if (r[j] >= 0) {
-                        const float w = wt ? __ldg(wt + kb + j) : 1.0f;
+                    if (j < n && in)
 #pragma unroll
-                        for (int q = 0; q < V; ++q) acc[q] = fmaf(w, to_f32(v[j].v[q]), acc[q]);
-                    }
+                        for (int q = 0; q < V; ++q) acc[q] = fmaf(f[j], to_f32(v[j].v[q]), acc[q]);
             }
+        }
+        if (in) {
             Vec<T, V> o;
 #pragma unroll
             for (int q = 0; q < V; ++q) o.v[q] = from_f32<T>(acc[q]);
@@ -377,9 +393,10 @@ extern "C" int k3moe_rows_combine(const void *y, int64_t ldy, int n_rows, const 
     with_types(dtype, vec, [&](auto t, auto v) {
         using Ty = decltype(t);
         constexpr int V = decltype(v)::value;
-        const int nv = D / V, th = row_threads(nv);
-        k3_launch(rows_combine_kernel<Ty, V>, dim3(T, std::min(65535, (nv + th - 1) / th)), th, 0, st, (const Ty *)y,
-                  ldy, n_rows, pos, weights, T, K, nv, (Ty *)z, ldz, status);
+        const int nv = D / V;
+        const int64_t warps = (int64_t)T * ((nv + 31) / 32);
+        k3_launch(rows_combine_kernel<Ty, V>, (unsigned)std::min<int64_t>((warps + 7) / 8, 1 << 20), 256, 0, st,
+                  (const Ty *)y, ldy, n_rows, pos, weights, T, K, nv, (Ty *)z, ldz, status);
     });
     k3_note_launch();
     return cudaGetLastError() == cudaSuccess ? K3MOE_OK : K3MOE_ERR_CUDA;
