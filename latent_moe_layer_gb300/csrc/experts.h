@@ -24,6 +24,17 @@ template <> __device__ __forceinline__ float from_f32<float>(float v) { return v
 template <> __device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(float v) { return __float2bfloat16_rn(v); }
 template <> __device__ __forceinline__ __half from_f32<__half>(float v) { return __float2half_rn(v); }
 
+// Two values rounded together (one conversion instruction for the 16-bit types).
+__device__ __forceinline__ void store2(float *o, float a, float b) { o[0] = a, o[1] = b; }
+__device__ __forceinline__ void store2(__nv_bfloat16 *o, float a, float b)
+{
+    *reinterpret_cast<__nv_bfloat162 *>(o) = __floats2bfloat162_rn(a, b);
+}
+__device__ __forceinline__ void store2(__half *o, float a, float b)
+{
+    *reinterpret_cast<__half2 *>(o) = __floats2half2_rn(a, b);
+}
+
 // V consecutive elements as one aligned access (V sizeof(T) = 2 to 32 bytes).
 template <class T, int V>
 struct alignas(V * sizeof(T) > 16 ? 16 : V * sizeof(T)) Vec {

@@ -5,20 +5,33 @@
 
 namespace k3 {
 
+constexpr uint32_t PHILOX_M0 = 0xD2511F53u, PHILOX_M1 = 0xCD9E8D57u, PHILOX_W0 = 0x9E3779B9u, PHILOX_W1 = 0xBB67AE85u;
+
 struct DropArgs {
     uint32_t key[10][2];                  // the rounds' keys: seed + round x the generator's two increments
-    uint32_t off0, off1;                  // offset
+    uint32_t first[3];                    // what round 1 makes of the offset: hi(off0 M1) ^ key, lo(off0 M1), off1 ^ key
+    uint64_t second;                      // M0 x first[0]: round 2's product where the element's high word is 0
     uint32_t threshold;                   // keep where the word is at least this: floor(p 2^32)
     float scale;                          // 1 / (1 - p)
 };
 
-// Philox4x32-10 (Salmon, Moraes, Dror and Shaw 2011): ten rounds of two 32 x 32 -> 64-bit products.
-__device__ __forceinline__ uint4 philox(uint64_t block, const DropArgs &a)
+// Philox4x32-10 (Salmon, Moraes, Dror and Shaw 2011): ten rounds of two 32 x 32 -> 64-bit products.  Counter
+// (block, offset), key seed.  The products are what it costs (4 cycles each of the integer multiplier a
+// warp), so those of rounds 1 and 2 that do not depend on the element come with the arguments; `p` is the
+// first round's other product, (low word of block) x M0.
+__device__ __forceinline__ uint4 philox(uint64_t p, uint32_t block_hi, const DropArgs &a)
 {
-    uint32_t x0 = (uint32_t)block, x1 = (uint32_t)(block >> 32), x2 = a.off0, x3 = a.off1;
+    uint32_t x2 = (uint32_t)(p >> 32) ^ a.first[2], x3 = (uint32_t)p, x0, x1;
+    p = a.second;
+    if (block_hi) p = (uint64_t)(a.first[0] ^ block_hi) * PHILOX_M0;       // elements past 2^34
+    uint64_t q = (uint64_t)x2 * PHILOX_M1;
+    x0 = (uint32_t)(q >> 32) ^ a.first[1] ^ a.key[1][0];
+    x1 = (uint32_t)q;
+    x2 = (uint32_t)(p >> 32) ^ x3 ^ a.key[1][1];
+    x3 = (uint32_t)p;
 #pragma unroll
-    for (int r = 0; r < 10; ++r) {
-        const uint64_t p = (uint64_t)x0 * 0xD2511F53u, q = (uint64_t)x2 * 0xCD9E8D57u;
+    for (int r = 2; r < 10; ++r) {
+        p = (uint64_t)x0 * PHILOX_M0, q = (uint64_t)x2 * PHILOX_M1;
         x0 = (uint32_t)(q >> 32) ^ x1 ^ a.key[r][0];
         x1 = (uint32_t)q;
         x2 = (uint32_t)(p >> 32) ^ x3 ^ a.key[r][1];
@@ -27,159 +40,292 @@ __device__ __forceinline__ uint4 philox(uint64_t block, const DropArgs &a)
     return make_uint4(x0, x1, x2, x3);
 }
 
-// factor[j] = scale where element i0 + j is kept, else 0; i0 a multiple of 4 when V is.
-template <int V, bool DROP>
-__device__ __forceinline__ void drop_factors(uint64_t i0, const DropArgs &a, float (&f)[V])
+// word[j] = the random word of element i0 + j; i0 a multiple of V when V is 4 or 8.
+template <int V>
+__device__ __forceinline__ void drop_words(uint64_t i0, const DropArgs &a, uint32_t (&w)[V])
 {
-    if (!DROP) {
-#pragma unroll
-        for (int j = 0; j < V; ++j) f[j] = 1.0f;
-    } else if (V % 4 == 0) {
+    const uint64_t block = i0 >> 2, p = (uint64_t)(uint32_t)block * PHILOX_M0;
+    const uint32_t hi = (uint32_t)(block >> 32);
+    if (V % 4 == 0) {
 #pragma unroll
         for (int j = 0; j < V; j += 4) {
-            const uint4 r = philox((i0 + j) >> 2, a);
-            f[j] = r.x >= a.threshold ? a.scale : 0.f;
-            f[j + 1] = r.y >= a.threshold ? a.scale : 0.f;
-            f[j + 2] = r.z >= a.threshold ? a.scale : 0.f;
-            f[j + 3] = r.w >= a.threshold ? a.scale : 0.f;
+            const uint4 r = philox(p + (uint64_t)(j / 4) * PHILOX_M0, hi, a);      // block is even when V is 8
+            w[j] = r.x, w[(j + 1) % V] = r.y, w[(j + 2) % V] = r.z, w[(j + 3) % V] = r.w;
         }
     } else {
+        static_assert(V % 4 == 0 || V == 1, "whole blocks or one element");
+        const uint4 r = philox(p, hi, a);
+        const uint32_t q = (uint32_t)i0 & 3;
+        w[0] = q == 0 ? r.x : q == 1 ? r.y : q == 2 ? r.z : r.w;
+    }
+}
+
+// v where the element is kept, else 0 (whatever v holds)
+template <bool DROP>
+__device__ __forceinline__ float kept(float v, uint32_t word, const DropArgs &a)
+{
+    return !DROP || word >= a.threshold ? v : 0.f;
+}
+
+// ------------------------------------------------------------------ pipelined pieces
+// The generator costs 160 cycles of the integer multiplier per warp and 8 elements, about what HBM takes
+// for their bytes, and warps that load, then compute, spend the sum of the two.  So each thread copies its
+// next PIPE - 1 pieces of 16 bytes an input into shared memory ahead (cp.async; its own slots, so nothing
+// is synchronised), which holds 100 KB and more in flight an SM without registers.
+constexpr int PIPE = 4, PIPE_THREADS = 256;
+
+__device__ __forceinline__ void cp_async16(void *dst, const void *src)
+{
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"((uint32_t)__cvta_generic_to_shared(dst)), "l"(src)
+                 : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+
+// Runs work(i, values) over this thread's pieces i0, i0 + step, ... < total; addr gives the inputs' addresses of
+// the next piece, in order.  Pieces of 16 bytes go through the ring, single elements are read directly.
+template <class T, int V, int NIN, class Addr, class Work>
+__device__ __forceinline__ void for_pieces(int64_t i0, int64_t step, int64_t total, Addr addr, Work work)
+{
+    if constexpr (V * sizeof(T) == 16) {
+        __shared__ uint4 ring[PIPE][NIN][PIPE_THREADS];
+        const int tid = threadIdx.x;
+        int64_t ahead = i0;
+        auto fetch = [&](int slot) {
+            if (ahead < total) {
+                const T *p[NIN];
+                addr(p);
 #pragma unroll
-        for (int j = 0; j < V; ++j) {
-            const uint4 r = philox((i0 + j) >> 2, a);
-            const uint32_t q = (uint32_t)(i0 + j) & 3;
-            f[j] = (q == 0 ? r.x : q == 1 ? r.y : q == 2 ? r.z : r.w) >= a.threshold ? a.scale : 0.f;
+                for (int j = 0; j < NIN; ++j)
+                    cp_async16(&ring[slot][j][tid], p[j]);
+            }
+            cp_async_commit();
+            ahead += step;
+        };
+#pragma unroll
+        for (int s = 0; s < PIPE - 1; ++s) fetch(s);
+        int slot = 0;
+        for (int64_t i = i0; i < total; i += step) {
+            fetch((slot + PIPE - 1) % PIPE);
+            cp_async_wait<PIPE - 1>();
+            Vec<T, V> in[NIN];
+#pragma unroll
+            for (int j = 0; j < NIN; ++j) in[j] = *reinterpret_cast<const Vec<T, V> *>(&ring[slot][j][tid]);
+            work(i, in);
+            slot = (slot + 1) % PIPE;
+        }
+    } else {
+        for (int64_t i = i0; i < total; i += step) {
+            const T *p[NIN];
+            addr(p);
+            Vec<T, V> in[NIN];
+#pragma unroll
+            for (int j = 0; j < NIN; ++j)
+                in[j] = *reinterpret_cast<const Vec<T, V> *>(p[j]);
+            work(i, in);
         }
     }
 }
 
 // ------------------------------------------------------------------ dropout with residual
-template <class T, int V, bool DROP>
-__global__ void __launch_bounds__(256) dropout_kernel(const T *x, const T *res, int64_t n, const DropArgs a, T *out)
+template <class T, int V, bool DROP, bool RES>
+__global__ void __launch_bounds__(PIPE_THREADS) dropout_kernel(const T *x, const T *res, int64_t n, const DropArgs a,
+                                                               T *out)
 {
     griddep_enter();
-    const int64_t step = (int64_t)gridDim.x * blockDim.x;
-    for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < (n + V - 1) / V; i += step) {
-        const int64_t i0 = i * V;
-        float f[V];
-        drop_factors<V, DROP>((uint64_t)i0, a, f);
-        if (i0 + V <= n) {
-            const Vec<T, V> v = *reinterpret_cast<const Vec<T, V> *>(x + i0);
-            Vec<T, V> r = {}, o;
-            if (res) r = *reinterpret_cast<const Vec<T, V> *>(res + i0);
+    const int64_t step = (int64_t)gridDim.x * PIPE_THREADS, i0 = (int64_t)blockIdx.x * PIPE_THREADS + threadIdx.x;
+    const int64_t whole = n / V;
+    int64_t at = i0 * V;
+    for_pieces<T, V, 1 + RES>(
+        i0, step, whole,
+        [&](const T *(&p)[1 + RES]) {
+            p[0] = x + at;
+            if (RES) p[RES] = res + at;
+            at += step * V;
+        },
+        [&](int64_t i, const Vec<T, V>(&in)[1 + RES]) {
+            uint32_t w[V] = {};
+            if (DROP) drop_words<V>((uint64_t)i * V, a, w);
+            Vec<T, V> o;
+            float d[V];
 #pragma unroll
             for (int j = 0; j < V; ++j) {
-                // a dropped element contributes 0 whatever it holds
-                const float d = !DROP || f[j] != 0.f ? to_f32(v.v[j]) * f[j] : 0.f;
-                o.v[j] = from_f32<T>(res ? d + to_f32(r.v[j]) : d);
+                d[j] = kept<DROP>(to_f32(in[0].v[j]) * a.scale, w[j], a);
+                if (RES) d[j] += to_f32(in[RES].v[j]);
+                if (j % 2) store2(o.v + j - 1, d[j - 1], d[j]);
+                else if (V == 1) o.v[0] = from_f32<T>(d[0]);
             }
-            *reinterpret_cast<Vec<T, V> *>(out + i0) = o;
-        } else {
-#pragma unroll
-            for (int j = 0; j < V; ++j)
-                if (i0 + j < n) {
-                    const float d = !DROP || f[j] != 0.f ? to_f32(x[i0 + j]) * f[j] : 0.f;
-                    out[i0 + j] = from_f32<T>(res ? d + to_f32(res[i0 + j]) : d);
-                }
-        }
+            *reinterpret_cast<Vec<T, V> *>(out + i * V) = o;
+        });
+    // the elements after the last whole piece, one a thread
+    const int64_t i = whole * V + i0;
+    if (i < n) {
+        uint32_t w[1] = {};
+        if (DROP) drop_words<1>((uint64_t)i, a, w);
+        const float d = kept<DROP>(to_f32(x[i]) * a.scale, w[0], a);
+        out[i] = from_f32<T>(RES ? d + to_f32(res[i]) : d);
     }
 }
 
 // ------------------------------------------------------------------ gated unit
-// Results are rounded to 16 bits, so hardware exponential and reciprocal (a few 2^-22) suffice; an
-// infinite exponential gives the exact limits 0 and 1.
-__device__ __forceinline__ float sigmoid(float g) { return __fdividef(1.0f, 1.0f + __expf(-g)); }
+// Results are rounded to 16 bits, so the hardware exponential and reciprocal (2^-22 relative, subnormals
+// flushed) suffice; an infinite exponential gives the exact limits 0 and 1.
+__device__ __forceinline__ float rcp_fast(float x)
+{
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ float exp_fast(float x)
+{
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x * 1.4426950408889634f));
+    return y;
+}
+__device__ __forceinline__ float sigmoid(float g) { return rcp_fast(1.0f + exp_fast(-g)); }
 
-// tanh x within 3e-7, relative also near 0: Lambert's continued fraction x / (1 + x^2 / (3 + x^2 / (5 + x^2 / (7 +
-// x^2 / 9)))) as one quotient up to |x| = 1 (off by 6e-8 there), (e^2x - 1) / (e^2x + 1) beyond.
-__device__ __forceinline__ float tanh_quotient(float x)
+// tanh x = num / den for |x| <= 1 within 3e-7, relative also near 0: Lambert's continued fraction
+// x / (1 + x^2 / (3 + x^2 / (5 + x^2 / (7 + x^2 / 9)))) as one quotient (itself off by 6e-8 at 1); 945 <= den <= 1380.
+__device__ __forceinline__ void tanh_quotient(float x, float &num, float &den)
 {
     const float x2 = x * x;
-    float num = x * fmaf(x2, x2 + 105.0f, 945.0f), den = fmaf(x2, fmaf(15.0f, x2, 420.0f), 945.0f);
-    if (fabsf(x) > 1.0f) {
-        const float e = __expf(2.0f * fminf(fmaxf(x, -10.0f), 10.0f));      // tanh 10 is 1 in fp32
-        num = e - 1.0f;
-        den = e + 1.0f;
-    }
-    return x != x ? x : __fdividef(num, den);
+    num = x * fmaf(x2, x2 + 105.0f, 945.0f);
+    den = fmaf(x2, fmaf(15.0f, x2, 420.0f), 945.0f);
+}
+// any x: beyond 1 (e^2x - 1) / (e^2x + 1), with tanh 10 = 1 in fp32
+__device__ __forceinline__ float tanh_any(float x)
+{
+    float num, den;
+    tanh_quotient(x, num, den);
+    const float e = exp_fast(2.0f * fminf(fmaxf(x, -10.0f), 10.0f));
+    const float big = (e - 1.0f) * rcp_fast(e + 1.0f);
+    return fabsf(x) <= 1.0f ? num * rcp_fast(den) : x != x ? x : big;
 }
 
-// a(g, u) and its derivatives: SiLU a = g s u, or the soft-limited a = s f h with f = beta tanh(g /
-// beta), h = linear_beta tanh(u / linear_beta), s = sigmoid(g).
-template <int ACT>
-__device__ __forceinline__ float glu_value(float g, float u, const K3Act &c)
+// The unit a = s f(g) h(u), s = sigmoid(g): SiLU f = g, h = u; SiTU f = beta tanh(g / beta), h = linear_beta
+// tanh(u / linear_beta).  GRAD: (da/dg, da/du) instead of a.  SMALL: all tanh arguments are within [-1, 1],
+// so that the sigmoid and both tanh share one reciprocal (exp(-g) is held below e^60, where the sigmoid is 0
+// for every 16-bit result, to keep the common denominator finite).
+template <int ACT, bool GRAD, bool SMALL>
+__device__ __forceinline__ void glu_one(float g, float u, const K3Act &c, float &o0, float &o1)
 {
-    const float s = sigmoid(g);
-    if (ACT == K3MOE_ACT_SILU) return g * s * u;
-    return s * (c.beta * tanh_quotient(g * c.inv_beta)) * (c.linear_beta * tanh_quotient(u * c.inv_linear_beta));
-}
-
-template <int ACT>
-__device__ __forceinline__ void glu_slopes(float g, float u, const K3Act &c, float &dg, float &du)
-{
-    const float s = sigmoid(g);
     if (ACT == K3MOE_ACT_SILU) {
-        dg = u * (s + g * s * (1.0f - s));
-        du = g * s;
+        const float s = sigmoid(g), f = g * s;
+        o0 = GRAD ? u * fmaf(f, 1.0f - s, s) : f * u;
+        o1 = f;
+        return;
+    }
+    const float xg = g * c.inv_beta, xu = u * c.inv_linear_beta;
+    float s, tg, tu;
+    if (SMALL) {
+        float ng, dg, nu, du;
+        tanh_quotient(xg, ng, dg);
+        tanh_quotient(xu, nu, du);
+        const float ds = 1.0f + exp_fast(fminf(-g, 60.0f)), dgu = dg * du, r = rcp_fast(ds * dgu);
+        if (!GRAD) {
+            o0 = (c.beta * c.linear_beta) * (ng * nu) * r;
+            return;
+        }
+        const float rs = r * ds;
+        s = r * dgu;
+        tg = ng * (rs * du);
+        tu = nu * (rs * dg);
     } else {
-        const float tg = tanh_quotient(g * c.inv_beta), tu = tanh_quotient(u * c.inv_linear_beta);
-        const float f = c.beta * tg, h = c.linear_beta * tu;
-        dg = h * (s * (1.0f - s) * f + s * (1.0f - tg * tg));
-        du = s * f * (1.0f - tu * tu);
+        s = sigmoid(g);
+        tg = tanh_any(xg);
+        tu = tanh_any(xu);
+    }
+    const float f = c.beta * tg, h = c.linear_beta * tu, sf = s * f;
+    if (GRAD) {
+        o0 = h * s * fmaf(f, 1.0f - s, fmaf(-tg, tg, 1.0f));
+        o1 = sf * fmaf(-tu, tu, 1.0f);
+    } else {
+        o0 = sf * h;
+    }
+}
+
+// Whether all |v| <= limit (no NaN): packed maxima for the 16-bit types.
+template <class T, int V>
+__device__ __forceinline__ bool all_within(const Vec<T, V> &v, float limit)
+{
+    if constexpr (V == 8) {
+        using T2 = std::conditional_t<std::is_same<T, __half>::value, __half2, __nv_bfloat162>;
+        const T2 *p = reinterpret_cast<const T2 *>(v.v);
+        const T2 m = __hmax2_nan(__hmax2_nan(__habs2(p[0]), __habs2(p[1])), __hmax2_nan(__habs2(p[2]), __habs2(p[3])));
+        const T *e = reinterpret_cast<const T *>(&m);
+        return to_f32(e[0]) <= limit && to_f32(e[1]) <= limit;
+    } else {
+        return fabsf(to_f32(v.v[0])) <= limit;
+    }
+}
+
+// V outputs from loaded inputs g, u (and the output's gradient).
+template <class T, int V, int ACT, bool DROP, bool GRAD, bool SMALL>
+__device__ __forceinline__ void glu_piece(const Vec<T, V> (&in)[2 + GRAD], const uint32_t (&w)[V], const K3Act &act,
+                                          const DropArgs &a, Vec<T, V> &o0, Vec<T, V> &o1)
+{
+    float r0[V], r1[V];
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+        float v0, v1;
+        glu_one<ACT, GRAD, SMALL>(to_f32(in[0].v[j]), to_f32(in[1].v[j]), act, v0, v1);
+        const float t = GRAD ? to_f32(in[1 + GRAD].v[j]) * a.scale : a.scale;
+        r0[j] = kept<DROP>(DROP || GRAD ? t * v0 : v0, w[j], a);
+        if (GRAD) r1[j] = kept<DROP>(t * v1, w[j], a);
+        if (j % 2) {
+            store2(o0.v + j - 1, r0[j - 1], r0[j]);
+            if (GRAD) store2(o1.v + j - 1, r1[j - 1], r1[j]);
+        } else if (V == 1) {
+            o0.v[0] = from_f32<T>(r0[0]);
+            if (GRAD) o1.v[0] = from_f32<T>(r1[0]);
+        }
     }
 }
 
 // Pieces of V elements over the [rows, width] matrix; piece i is row i / nv, column (i % nv) V.
 template <class T, int V, int ACT, bool DROP, bool GRAD>
-__global__ void __launch_bounds__(256) glu_kernel(const T *da, int64_t ldda, const T *gu, int64_t ldgu, int rows,
-                                                  int width, const K3Act act, const DropArgs a, T *out, int64_t ldo)
+__global__ void __launch_bounds__(PIPE_THREADS, GRAD ? 4 : 5) glu_kernel(const T *da, int64_t ldda, const T *gu, int64_t ldgu,
+                                                                         int rows, int width, const K3Act act,
+                                                                         const DropArgs a, T *out, int64_t ldo)
 {
     griddep_enter();
     const int nv = width / V;
-    const int64_t total = (int64_t)rows * nv, step = (int64_t)gridDim.x * blockDim.x;
-    int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
-    int64_t row = i / nv;
-    int col = (int)(i - row * nv);
-    const int64_t row_step = step / nv;
+    const int64_t total = (int64_t)rows * nv, step = (int64_t)gridDim.x * PIPE_THREADS;
+    const int64_t i0 = (int64_t)blockIdx.x * PIPE_THREADS + threadIdx.x, row_step = step / nv;
     const int col_step = (int)(step - row_step * nv);
-    for (; i < total; i += step) {
-        const T *src = gu + row * ldgu + (int64_t)col * V;
-        const Vec<T, V> g = *reinterpret_cast<const Vec<T, V> *>(src);
-        const Vec<T, V> u = *reinterpret_cast<const Vec<T, V> *>(src + width);
-        Vec<T, V> d = {};
-        if (GRAD) d = *reinterpret_cast<const Vec<T, V> *>(da + row * ldda + (int64_t)col * V);
-        float f[V];
-        drop_factors<V, DROP>((uint64_t)i * V, a, f);
-        T *dst = out + row * ldo + (int64_t)col * V;
-        if (GRAD) {
-            Vec<T, V> og, ou;
-#pragma unroll
-            for (int j = 0; j < V; ++j) {
-                float sg, su;
-                glu_slopes<ACT>(to_f32(g.v[j]), to_f32(u.v[j]), act, sg, su);
-                const float t = to_f32(d.v[j]) * f[j];
-                const bool kept = !DROP || f[j] != 0.f;       // a dropped element contributes 0 whatever it holds
-                og.v[j] = from_f32<T>(kept ? t * sg : 0.f);
-                ou.v[j] = from_f32<T>(kept ? t * su : 0.f);
-            }
-            *reinterpret_cast<Vec<T, V> *>(dst) = og;
-            *reinterpret_cast<Vec<T, V> *>(dst + width) = ou;
-        } else {
-            Vec<T, V> o;
-#pragma unroll
-            for (int j = 0; j < V; ++j) {
-                const float v = glu_value<ACT>(to_f32(g.v[j]), to_f32(u.v[j]), act) * f[j];
-                o.v[j] = from_f32<T>(!DROP || f[j] != 0.f ? v : 0.f);
-            }
-            *reinterpret_cast<Vec<T, V> *>(dst) = o;
+    int64_t row = i0 / nv, out_row = row;                // of the piece being fetched; of the one being computed
+    int col = (int)(i0 - row * nv), out_col = col;
+    auto advance = [&](int64_t &r, int &c) {
+        r += row_step;
+        c += col_step;
+        if (c >= nv) {
+            c -= nv;
+            ++r;
         }
-        row += row_step;
-        col += col_step;
-        if (col >= nv) {
-            col -= nv;
-            ++row;
-        }
-    }
+    };
+    for_pieces<T, V, 2 + GRAD>(
+        i0, step, total,
+        [&](const T *(&p)[2 + GRAD]) {
+            p[0] = gu + row * ldgu + (int64_t)col * V;
+            p[1] = p[0] + width;
+            if (GRAD) p[1 + GRAD] = da + row * ldda + (int64_t)col * V;
+            advance(row, col);
+        },
+        [&](int64_t i, const Vec<T, V>(&in)[2 + GRAD]) {
+            uint32_t w[V] = {};
+            if (DROP) drop_words<V>((uint64_t)i * V, a, w);
+            Vec<T, V> o0, o1;
+            // one branch a piece: tanh arguments beyond 1 (or NaN) are rare
+            const bool small = ACT == K3MOE_ACT_SILU ||
+                               (all_within<T, V>(in[0], act.beta) && all_within<T, V>(in[1], act.linear_beta));
+            if (small) glu_piece<T, V, ACT, DROP, GRAD, true>(in, w, act, a, o0, o1);
+            else glu_piece<T, V, ACT, DROP, GRAD, false>(in, w, act, a, o0, o1);
+            T *dst = out + out_row * ldo + (int64_t)out_col * V;
+            *reinterpret_cast<Vec<T, V> *>(dst) = o0;
+            if (GRAD) *reinterpret_cast<Vec<T, V> *>(dst + width) = o1;
+            advance(out_row, out_col);
+        });
 }
 
 }  // namespace k3
@@ -190,11 +336,14 @@ static bool drop_args(double p, uint64_t seed, uint64_t offset, DropArgs &a)
 {
     if (!(p >= 0.0 && p < 1.0)) return false;
     for (uint32_t r = 0; r < 10; ++r) {
-        a.key[r][0] = (uint32_t)seed + r * 0x9E3779B9u;
-        a.key[r][1] = (uint32_t)(seed >> 32) + r * 0xBB67AE85u;
+        a.key[r][0] = (uint32_t)seed + r * PHILOX_W0;
+        a.key[r][1] = (uint32_t)(seed >> 32) + r * PHILOX_W1;
     }
-    a.off0 = (uint32_t)offset;
-    a.off1 = (uint32_t)(offset >> 32);
+    const uint64_t q = (uint64_t)(uint32_t)offset * PHILOX_M1;
+    a.first[0] = (uint32_t)(q >> 32) ^ a.key[0][0];
+    a.first[1] = (uint32_t)q;
+    a.first[2] = (uint32_t)(offset >> 32) ^ a.key[0][1];
+    a.second = (uint64_t)a.first[0] * PHILOX_M0;
     a.threshold = (uint32_t)(p * 4294967296.0);
     a.scale = (float)(1.0 / (1.0 - p));
     return true;
@@ -207,10 +356,17 @@ static void with_bool(bool b, F f)
     else f(std::false_type());
 }
 
-// enough CTAs of 256 threads for `pieces`, at most eight a multiprocessor (the loops stride the rest)
-static int elementwise_grid(int64_t pieces, int sms)
+// CTAs for `pieces`: as many as are resident at once (the loops stride the rest), since a
+// second, partly filled round of CTAs costs as much as a full one.  `fit` is the kernel's own memory.
+template <class F>
+static unsigned resident_grid(F kern, int64_t pieces, int sms, int &fit)
 {
-    return (int)std::min<int64_t>((pieces + 255) / 256, (int64_t)8 * sms);
+    int n = fit;
+    if (!n) {
+        if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kern, PIPE_THREADS, 0) != cudaSuccess || n < 1) n = 1;
+        fit = n;
+    }
+    return (unsigned)std::min<int64_t>((pieces + PIPE_THREADS - 1) / PIPE_THREADS, (int64_t)n * sms);
 }
 
 template <class T, int V>
@@ -218,8 +374,12 @@ static void launch_dropout(const void *x, const void *res, int64_t n, const Drop
                            cudaStream_t st)
 {
     with_bool(a.threshold != 0, [&](auto drop) {
-        k3_launch(dropout_kernel<T, V, decltype(drop)::value>, elementwise_grid((n + V - 1) / V, sms), 256, 0, st,
-                  (const T *)x, (const T *)res, n, a, (T *)out);
+        with_bool(res != nullptr, [&](auto with_res) {
+            auto kern = dropout_kernel<T, V, decltype(drop)::value, decltype(with_res)::value>;
+            static int fit = 0;
+            k3_launch(kern, resident_grid(kern, (n + V - 1) / V, sms, fit), PIPE_THREADS, 0, st, (const T *)x,
+                      (const T *)res, n, a, (T *)out);
+        });
     });
 }
 
@@ -256,8 +416,10 @@ static void launch_glu(const void *da, int64_t ldda, const void *gu, int64_t ldg
     with_bool(a.threshold != 0, [&](auto drop) {
         with_bool(act.kind == K3MOE_ACT_SITU, [&](auto situ) {
             constexpr int ACT = decltype(situ)::value ? K3MOE_ACT_SITU : K3MOE_ACT_SILU;
-            k3_launch(glu_kernel<T, V, ACT, decltype(drop)::value, GRAD>,
-                      elementwise_grid((int64_t)rows * (width / V), sms), 256, 0, st, (const T *)da, ldda,
+            auto kern = glu_kernel<T, V, ACT, decltype(drop)::value, GRAD>;
+            static int fit = 0;
+            k3_launch(kern, resident_grid(kern, (int64_t)rows * (width / V), sms, fit), PIPE_THREADS, 0, st, (const T *)da,
+                      ldda,
                       (const T *)gu, ldgu, rows, width, act, a, (T *)out, ldo);
         });
     });
