@@ -68,11 +68,12 @@ __device__ __forceinline__ float kept(float v, uint32_t word, const DropArgs &a)
 }
 
 // ------------------------------------------------------------------ pipelined pieces
-// The generator costs 160 cycles of the integer multiplier per warp and 8 elements, about what HBM takes
-// for their bytes, and warps that load, then compute, spend the sum of the two.  So each thread copies its
-// next PIPE - 1 pieces of 16 bytes an input into shared memory ahead (cp.async; its own slots, so nothing
-// is synchronised), which holds 100 KB and more in flight an SM without registers.
-constexpr int PIPE = 4, PIPE_THREADS = 256;
+// With the generator a 16-bit piece costs about as much computing as HBM takes for its bytes, and warps that
+// load, then compute, spend the sum of the two.  So there (RING) each thread copies its next piece of 16 bytes
+// an input into shared memory ahead (cp.async; its own slots, so nothing is synchronised), which costs no
+// registers: 58.7 M bf16 elements 72 -> 58 us.  Without the generator, and for fp32, direct loads are 3-5 %
+// faster (its computing hides behind the bytes).
+constexpr int PIPE = 2, PIPE_THREADS = 256;
 
 __device__ __forceinline__ void cp_async16(void *dst, const void *src)
 {
@@ -84,11 +85,12 @@ template <int N>
 __device__ __forceinline__ void cp_async_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
 
 // Runs work(i, values) over this thread's pieces i0, i0 + step, ... < total; addr gives the inputs' addresses of
-// the next piece, in order.  Pieces of 16 bytes go through the ring, single elements are read directly.
-template <class T, int V, int NIN, class Addr, class Work>
+// the next piece, in order.
+template <class T, int V, int NIN, bool RING, class Addr, class Work>
 __device__ __forceinline__ void for_pieces(int64_t i0, int64_t step, int64_t total, Addr addr, Work work)
 {
-    if constexpr (V * sizeof(T) == 16) {
+    if constexpr (RING) {
+        static_assert(V * sizeof(T) == 16, "16-byte pieces");
         __shared__ uint4 ring[PIPE][NIN][PIPE_THREADS];
         const int tid = threadIdx.x;
         int64_t ahead = i0;
@@ -137,7 +139,7 @@ __global__ void __launch_bounds__(PIPE_THREADS) dropout_kernel(const T *x, const
     const int64_t step = (int64_t)gridDim.x * PIPE_THREADS, i0 = (int64_t)blockIdx.x * PIPE_THREADS + threadIdx.x;
     const int64_t whole = n / V;
     int64_t at = i0 * V;
-    for_pieces<T, V, 1 + RES>(
+    for_pieces<T, V, 1 + RES, DROP && V == 8>(
         i0, step, whole,
         [&](const T *(&p)[1 + RES]) {
             p[0] = x + at;
@@ -177,71 +179,108 @@ __device__ __forceinline__ float rcp_fast(float x)
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
-__device__ __forceinline__ float exp_fast(float x)
+// Two fp32 values in one register pair; sums and products of both in one instruction.
+struct F2 {
+    float x, y;
+};
+__device__ __forceinline__ F2 f2(float v) { return {v, v}; }
+__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c)
 {
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x * 1.4426950408889634f));
-    return y;
+    F2 d;
+    asm("{\n\t.reg .b64 a, b, c, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tmov.b64 c, {%6, %7};\n\t"
+        "fma.rn.f32x2 d, a, b, c;\n\tmov.b64 {%0, %1}, d;\n\t}"
+        : "=f"(d.x), "=f"(d.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+    return d;
 }
-__device__ __forceinline__ float sigmoid(float g) { return rcp_fast(1.0f + exp_fast(-g)); }
+__device__ __forceinline__ F2 mul2(F2 a, F2 b)
+{
+    F2 d;
+    asm("{\n\t.reg .b64 a, b, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tmul.rn.f32x2 d, a, b;\n\t"
+        "mov.b64 {%0, %1}, d;\n\t}"
+        : "=f"(d.x), "=f"(d.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return d;
+}
+__device__ __forceinline__ F2 rcp2(F2 a) { return {rcp_fast(a.x), rcp_fast(a.y)}; }
+// 1 + exp(-v)
+__device__ __forceinline__ F2 one_plus_exp_neg(F2 v)
+{
+    const F2 t = mul2(v, f2(-1.4426950408889634f));
+    float a, b;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(a) : "f"(t.x));
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(b) : "f"(t.y));
+    return fma2({a, b}, f2(1.0f), f2(1.0f));
+}
 
-// tanh x = num / den for |x| <= 1 within 3e-7, relative also near 0: Lambert's continued fraction
-// x / (1 + x^2 / (3 + x^2 / (5 + x^2 / (7 + x^2 / 9)))) as one quotient (itself off by 6e-8 at 1); 945 <= den <= 1380.
-__device__ __forceinline__ void tanh_quotient(float x, float &num, float &den)
+// limit tanh(v / limit) = v num / den for |v| <= limit within 3e-7, relative also near 0, with x = (v / limit)^2:
+// Lambert's continued fraction t / (1 + t^2 / (3 + t^2 / (5 + t^2 / (7 + t^2 / 9)))) as one quotient (itself off
+// by 6e-8 at 1); 1 <= den <= 1.46.
+__device__ __forceinline__ void tanh_quotient(F2 x, F2 &num, F2 &den)
 {
-    const float x2 = x * x;
-    num = x * fmaf(x2, x2 + 105.0f, 945.0f);
-    den = fmaf(x2, fmaf(15.0f, x2, 420.0f), 945.0f);
+    num = fma2(x, fma2(x, f2(1.0f / 945.0f), f2(105.0f / 945.0f)), f2(1.0f));
+    den = fma2(x, fma2(x, f2(15.0f / 945.0f), f2(420.0f / 945.0f)), f2(1.0f));
 }
-// any x: beyond 1 (e^2x - 1) / (e^2x + 1), with tanh 10 = 1 in fp32
+// tanh of any x: beyond 1 (e^2x - 1) / (e^2x + 1), with tanh 10 = 1 in fp32
 __device__ __forceinline__ float tanh_any(float x)
 {
-    float num, den;
-    tanh_quotient(x, num, den);
-    const float e = exp_fast(2.0f * fminf(fmaxf(x, -10.0f), 10.0f));
+    F2 num, den;
+    tanh_quotient(f2(x * x), num, den);
+    float e;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(2.8853900817779268f * fminf(fmaxf(x, -10.0f), 10.0f)));
     const float big = (e - 1.0f) * rcp_fast(e + 1.0f);
-    return fabsf(x) <= 1.0f ? num * rcp_fast(den) : x != x ? x : big;
+    return fabsf(x) <= 1.0f ? x * num.x * rcp_fast(den.x) : x != x ? x : big;
 }
 
-// The unit a = s f(g) h(u), s = sigmoid(g): SiLU f = g, h = u; SiTU f = beta tanh(g / beta), h = linear_beta
-// tanh(u / linear_beta).  GRAD: (da/dg, da/du) instead of a.  SMALL: all tanh arguments are within [-1, 1],
-// so that the sigmoid and both tanh share one reciprocal (exp(-g) is held below e^60, where the sigmoid is 0
-// for every 16-bit result, to keep the common denominator finite).
+// The unit a = s f(g) h(u), s = sigmoid(g), of two elements: SiLU f = g, h = u; SiTU f = beta tanh(g / beta),
+// h = linear_beta tanh(u / linear_beta).  GRAD: (da/dg, da/du) instead of a.  SMALL: all tanh arguments are
+// within [-1, 1] and |g| <= 60, so that the sigmoid and both tanh share one reciprocal of a finite product.
 template <int ACT, bool GRAD, bool SMALL>
-__device__ __forceinline__ void glu_one(float g, float u, const K3Act &c, float &o0, float &o1)
+__device__ __forceinline__ void glu_two(F2 g, F2 u, const K3Act &c, F2 &o0, F2 &o1)
 {
+    const F2 ds = one_plus_exp_neg(g), one = f2(1.0f);
     if (ACT == K3MOE_ACT_SILU) {
-        const float s = sigmoid(g), f = g * s;
-        o0 = GRAD ? u * fmaf(f, 1.0f - s, s) : f * u;
+        const F2 s = rcp2(ds), f = mul2(g, s);
+        o0 = GRAD ? mul2(u, fma2(f, fma2(s, f2(-1.0f), one), s)) : mul2(f, u);
         o1 = f;
         return;
     }
-    const float xg = g * c.inv_beta, xu = u * c.inv_linear_beta;
-    float s, tg, tu;
+    F2 s, f, h, tg2, tu2;                                // tg2, tu2: the tanh squared
     if (SMALL) {
-        float ng, dg, nu, du;
+        const F2 xg = mul2(mul2(g, g), f2(c.inv_beta * c.inv_beta));
+        const F2 xu = mul2(mul2(u, u), f2(c.inv_linear_beta * c.inv_linear_beta));
+        F2 ng, dg, nu, du;
         tanh_quotient(xg, ng, dg);
         tanh_quotient(xu, nu, du);
-        const float ds = 1.0f + exp_fast(fminf(-g, 60.0f)), dgu = dg * du, r = rcp_fast(ds * dgu);
+        ng = mul2(ng, g);
+        nu = mul2(nu, u);
+        const F2 dgu = mul2(dg, du), r = rcp2(mul2(ds, dgu));
         if (!GRAD) {
-            o0 = (c.beta * c.linear_beta) * (ng * nu) * r;
+            o0 = mul2(mul2(ng, nu), r);
             return;
         }
-        const float rs = r * ds;
-        s = r * dgu;
-        tg = ng * (rs * du);
-        tu = nu * (rs * dg);
+        const F2 rs = mul2(r, ds);
+        s = mul2(r, dgu);
+        f = mul2(ng, mul2(rs, du));
+        h = mul2(nu, mul2(rs, dg));
+        tg2 = mul2(mul2(f, f), f2(c.inv_beta * c.inv_beta));
+        tu2 = mul2(mul2(h, h), f2(c.inv_linear_beta * c.inv_linear_beta));
     } else {
-        s = sigmoid(g);
-        tg = tanh_any(xg);
-        tu = tanh_any(xu);
+        const F2 tg = {tanh_any(g.x * c.inv_beta), tanh_any(g.y * c.inv_beta)};
+        const F2 tu = {tanh_any(u.x * c.inv_linear_beta), tanh_any(u.y * c.inv_linear_beta)};
+        s = rcp2(ds);
+        f = mul2(tg, f2(c.beta));
+        h = mul2(tu, f2(c.linear_beta));
+        tg2 = mul2(tg, tg);
+        tu2 = mul2(tu, tu);
     }
-    const float f = c.beta * tg, h = c.linear_beta * tu, sf = s * f;
+    const F2 sf = mul2(s, f), neg = f2(-1.0f);
     if (GRAD) {
-        o0 = h * s * fmaf(f, 1.0f - s, fmaf(-tg, tg, 1.0f));
-        o1 = sf * fmaf(-tu, tu, 1.0f);
+        // da/dg = h s (f (1 - s) + 1 - tg^2), da/du = s f (1 - tu^2)
+        o0 = mul2(mul2(h, s), fma2(tg2, neg, fma2(sf, neg, fma2(f, one, one))));
+        o1 = mul2(sf, fma2(tu2, neg, one));
     } else {
-        o0 = sf * h;
+        o0 = mul2(sf, h);
     }
 }
 
@@ -265,27 +304,31 @@ template <class T, int V, int ACT, bool DROP, bool GRAD, bool SMALL>
 __device__ __forceinline__ void glu_piece(const Vec<T, V> (&in)[2 + GRAD], const uint32_t (&w)[V], const K3Act &act,
                                           const DropArgs &a, Vec<T, V> &o0, Vec<T, V> &o1)
 {
-    float r0[V], r1[V];
+    const F2 scale = f2(a.scale);
 #pragma unroll
-    for (int j = 0; j < V; ++j) {
-        float v0, v1;
-        glu_one<ACT, GRAD, SMALL>(to_f32(in[0].v[j]), to_f32(in[1].v[j]), act, v0, v1);
-        const float t = GRAD ? to_f32(in[1 + GRAD].v[j]) * a.scale : a.scale;
-        r0[j] = kept<DROP>(DROP || GRAD ? t * v0 : v0, w[j], a);
-        if (GRAD) r1[j] = kept<DROP>(t * v1, w[j], a);
-        if (j % 2) {
-            store2(o0.v + j - 1, r0[j - 1], r0[j]);
-            if (GRAD) store2(o1.v + j - 1, r1[j - 1], r1[j]);
-        } else if (V == 1) {
-            o0.v[0] = from_f32<T>(r0[0]);
-            if (GRAD) o1.v[0] = from_f32<T>(r1[0]);
+    for (int j = 0; j < V; j += 2) {
+        const int k = V == 1 ? 0 : j + 1;                // a single element is its own partner
+        F2 v0, v1;
+        glu_two<ACT, GRAD, SMALL>({to_f32(in[0].v[j]), to_f32(in[0].v[k])}, {to_f32(in[1].v[j]), to_f32(in[1].v[k])}, act,
+                                  v0, v1);
+        const F2 t = GRAD ? mul2({to_f32(in[1 + GRAD].v[j]), to_f32(in[1 + GRAD].v[k])}, scale) : scale;
+        if (DROP || GRAD) v0 = mul2(v0, t);
+        if (GRAD) v1 = mul2(v1, t);
+        v0 = {kept<DROP>(v0.x, w[j], a), kept<DROP>(v0.y, w[k], a)};
+        if (GRAD) v1 = {kept<DROP>(v1.x, w[j], a), kept<DROP>(v1.y, w[k], a)};
+        if (V == 1) {
+            o0.v[0] = from_f32<T>(v0.x);
+            if (GRAD) o1.v[0] = from_f32<T>(v1.x);
+        } else {
+            store2(o0.v + j, v0.x, v0.y);
+            if (GRAD) store2(o1.v + j, v1.x, v1.y);
         }
     }
 }
 
 // Pieces of V elements over the [rows, width] matrix; piece i is row i / nv, column (i % nv) V.
 template <class T, int V, int ACT, bool DROP, bool GRAD>
-__global__ void __launch_bounds__(PIPE_THREADS, GRAD ? 4 : 5) glu_kernel(const T *da, int64_t ldda, const T *gu, int64_t ldgu,
+__global__ void __launch_bounds__(PIPE_THREADS, GRAD ? 3 : 4) glu_kernel(const T *da, int64_t ldda, const T *gu, int64_t ldgu,
                                                                          int rows, int width, const K3Act act,
                                                                          const DropArgs a, T *out, int64_t ldo)
 {
@@ -304,7 +347,7 @@ __global__ void __launch_bounds__(PIPE_THREADS, GRAD ? 4 : 5) glu_kernel(const T
             ++r;
         }
     };
-    for_pieces<T, V, 2 + GRAD>(
+    for_pieces<T, V, 2 + GRAD, DROP && V == 8>(
         i0, step, total,
         [&](const T *(&p)[2 + GRAD]) {
             p[0] = gu + row * ldgu + (int64_t)col * V;
@@ -318,7 +361,7 @@ __global__ void __launch_bounds__(PIPE_THREADS, GRAD ? 4 : 5) glu_kernel(const T
             Vec<T, V> o0, o1;
             // one branch a piece: tanh arguments beyond 1 (or NaN) are rare
             const bool small = ACT == K3MOE_ACT_SILU ||
-                               (all_within<T, V>(in[0], act.beta) && all_within<T, V>(in[1], act.linear_beta));
+                               (all_within<T, V>(in[0], fminf(act.beta, 60.0f)) && all_within<T, V>(in[1], act.linear_beta));
             if (small) glu_piece<T, V, ACT, DROP, GRAD, true>(in, w, act, a, o0, o1);
             else glu_piece<T, V, ACT, DROP, GRAD, false>(in, w, act, a, o0, o1);
             T *dst = out + out_row * ldo + (int64_t)out_col * V;
