@@ -159,24 +159,25 @@ __global__ void __launch_bounds__(256) rows_gather_kernel(const T *__restrict__ 
 }
 
 // ------------------------------------------------------------------ combine
-// A warp per token and 32 V columns, so that nothing but memory keeps a warp waiting: the lanes hold the
-// token's rows and weights, and only rows that exist are loaded, eight in flight, summed in k order.
+// `split` warps per token, each with every split-th piece of 32 V columns, so that nothing but memory keeps a
+// warp waiting: its lanes hold the token's rows and weights (32 at a time), and only rows that exist are
+// loaded, eight in flight, summed in k order.
 template <class T, int V>
 __global__ void __launch_bounds__(256) rows_combine_kernel(const T *__restrict__ y, int64_t ldy, int n_rows,
                                                            const int32_t *__restrict__ pos,
                                                            const float *__restrict__ wts, int T_, int K, int nv,
-                                                           T *__restrict__ z, int64_t ldz, int *status)
+                                                           int split, T *__restrict__ z, int64_t ldz, int *status)
 {
     griddep_enter();
-    const int lane = threadIdx.x & 31, chunks = (nv + 31) / 32;
-    const int64_t work = (int64_t)T_ * chunks, step = (int64_t)gridDim.x * 8;
+    const int lane = threadIdx.x & 31;
+    const int64_t work = (int64_t)T_ * split, step = (int64_t)gridDim.x * 8;
     for (int64_t u = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5); u < work; u += step) {
-        const int t = (int)(u / chunks), i = (int)(u - (int64_t)t * chunks) * 32 + lane;
-        const bool in = i < nv;
-        float acc[V] = {};
-        for (int kb = 0; kb < K; kb += 32) {
-            int row = -1;
-            float w = 0.f;
+        const int t = (int)(u / split), first = (int)(u - (int64_t)t * split);
+        int row = -1;
+        float w = 0.f;
+        auto table = [&](int kb) {
+            row = -1;
+            w = 0.f;
             if (kb + lane < K) {
                 row = __ldg(pos + (int64_t)t * K + kb + lane);
                 w = wts ? __ldg(wts + (int64_t)t * K + kb + lane) : 1.0f;
@@ -185,41 +186,66 @@ __global__ void __launch_bounds__(256) rows_combine_kernel(const T *__restrict__
                     row = -1;
                 }
             }
-            uint32_t live = __ballot_sync(0xffffffffu, row >= 0);
-            while (live) {
-                Vec<T, V> v[8];
-                float f[8];
-                const int n = __popc(live);
+        };
+        table(0);
+        for (int i = first * 32 + lane; i - lane < nv; i += split * 32) {
+            const bool in = i < nv;
+            float acc[V] = {};
+            for (int kb = 0; kb < K; kb += 32) {
+                if (K > 32) table(kb);
+                uint32_t live = __ballot_sync(0xffffffffu, row >= 0);
+                while (live) {
+                    Vec<T, V> v[8];
+                    float f[8];
+                    const int n = __popc(live);
 #pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    if (j >= n) break;
-                    const int k = __ffs(live) - 1;
-                    live &= live - 1;
-                    const int r = __shfl_sync(0xffffffffu, row, k);
-                    f[j] = __shfl_sync(0xffffffffu, w, k);
-                    if (in) v[j] = *reinterpret_cast<const Vec<T, V> *>(y + r * ldy + (int64_t)i * V);
+                    for (int j = 0; j < 8; ++j) {
+                        const int k = max(__ffs(live) - 1, 0);
+                        live &= live - 1;
+                        const int r = __shfl_sync(0xffffffffu, row, k);
+                        f[j] = __shfl_sync(0xffffffffu, w, k);
+                        if (in && j < n) v[j] = *reinterpret_cast<const Vec<T, V> *>(y + r * ldy + (int64_t)i * V);
+                    }
+#pragma unroll
+                    for (int j = 0; j < 8; ++j)
+                        if (j < n && in)
+#pragma unroll
+                            for (int q = 0; q < V; ++q) acc[q] = fmaf(f[j], to_f32(v[j].v[q]), acc[q]);
                 }
-#pragma unroll
-                for (int j = 0; j < 8; ++j)
-                    if (j < n && in)
-#pragma unroll
-                        for (int q = 0; q < V; ++q) acc[q] = fmaf(f[j], to_f32(v[j].v[q]), acc[q]);
             }
-        }
-        if (in) {
-            Vec<T, V> o;
+            if (in) {
+                Vec<T, V> o;
 #pragma unroll
-            for (int q = 0; q < V; ++q) o.v[q] = from_f32<T>(acc[q]);
-            *reinterpret_cast<Vec<T, V> *>(z + t * ldz + (int64_t)i * V) = o;
+                for (int q = 0; q < V; ++q) o.v[q] = from_f32<T>(acc[q]);
+                *reinterpret_cast<Vec<T, V> *>(z + t * ldz + (int64_t)i * V) = o;
+            }
         }
     }
 }
 
 // ------------------------------------------------------------------ combine's gradient
-// CTA per token: dz's row once per eight pairs, the pair's y row read and its dy row written (in that
-// order by the same thread, so dy may be y), dot products summed per thread, warp and CTA in fixed order.
+// Sums of eight values over the warp in nine shuffles: each of the first three steps halves the values a
+// lane still holds.  Lane l ends with value l / 4 in v[0].
+__device__ __forceinline__ void warp_sum8(float (&v)[8], int lane)
+{
+#pragma unroll
+    for (int n = 4, d = 16; n > 0; n >>= 1, d >>= 1) {
+        const bool up = lane & d;
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            if (j < n) {
+                const float give = up ? v[j] : v[j + n], keep = up ? v[j + n] : v[j];
+                v[j] = keep + __shfl_xor_sync(0xffffffffu, give, d);
+            }
+    }
+    v[0] += __shfl_xor_sync(0xffffffffu, v[0], 2);
+    v[0] += __shfl_xor_sync(0xffffffffu, v[0], 1);
+}
+
+// CTA per token and eight pairs (or all its pairs, eight at a time): dz's row, the pairs' y rows read and their dy rows written (in that order
+// by the same thread, so dy may be y), dot products summed per thread, warp and CTA in fixed order.
 template <class T, int V>
-__global__ void __launch_bounds__(256) rows_combine_grad_kernel(const T *__restrict__ dz, int64_t lddz, const T *y,
+__global__ void __launch_bounds__(256, 3) rows_combine_grad_kernel(const T *__restrict__ dz, int64_t lddz, const T *y,
                                                                 int64_t ldy, int n_rows,
                                                                 const int32_t *__restrict__ pos,
                                                                 const float *__restrict__ wts, int T_, int K, int nv,
@@ -230,7 +256,7 @@ __global__ void __launch_bounds__(256) rows_combine_grad_kernel(const T *__restr
     __shared__ float part[8][8];
     const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, nw = blockDim.x >> 5;
     for (int t = blockIdx.x; t < T_; t += gridDim.x) {
-        for (int kb = 0; kb < K; kb += 8) {
+        for (int kb = 8 * blockIdx.y; kb < K; kb += 8 * gridDim.y) {
             int r[8];
             float wt[8], acc[8] = {};
 #pragma unroll
@@ -262,12 +288,8 @@ __global__ void __launch_bounds__(256) rows_combine_grad_kernel(const T *__restr
                         *reinterpret_cast<Vec<T, V> *>(dy + r[j] * lddy + (int64_t)i * V) = o;
                     }
             }
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-#pragma unroll
-                for (int d = 16; d > 0; d >>= 1) acc[j] += __shfl_xor_sync(0xffffffffu, acc[j], d);
-                if (lane == 0) part[w][j] = acc[j];
-            }
+            warp_sum8(acc, lane);
+            if ((lane & 3) == 0) part[w][lane >> 2] = acc[0];
             __syncthreads();
             if (threadIdx.x < 8 && kb + threadIdx.x < K) {
                 float s = 0.f;
@@ -394,9 +416,10 @@ extern "C" int k3moe_rows_combine(const void *y, int64_t ldy, int n_rows, const 
         using Ty = decltype(t);
         constexpr int V = decltype(v)::value;
         const int nv = D / V;
-        const int64_t warps = (int64_t)T * ((nv + 31) / 32);
-        k3_launch(rows_combine_kernel<Ty, V>, (unsigned)std::min<int64_t>((warps + 7) / 8, 1 << 20), 256, 0, st,
-                  (const Ty *)y, ldy, n_rows, pos, weights, T, K, nv, (Ty *)z, ldz, status);
+        // about four rounds of the 32 or so warps an SM holds (4096 tokens: 95 us, with one round 103)
+        const int pieces = (nv + 31) / 32, split = (int)std::min<int64_t>(pieces, (128LL * sms + T - 1) / T);
+        k3_launch(rows_combine_kernel<Ty, V>, (unsigned)std::min<int64_t>(((int64_t)T * split + 7) / 8, 1 << 20), 256, 0,
+                  st, (const Ty *)y, ldy, n_rows, pos, weights, T, K, nv, split, (Ty *)z, ldz, status);
     });
     k3_note_launch();
     return cudaGetLastError() == cudaSuccess ? K3MOE_OK : K3MOE_ERR_CUDA;
@@ -420,8 +443,10 @@ extern "C" int k3moe_rows_combine_grad(const void *dz, int64_t lddz, const void 
     with_types(dtype, vec, [&](auto t, auto v) {
         using Ty = decltype(t);
         constexpr int V = decltype(v)::value;
-        const int nv = D / V;
-        k3_launch(rows_combine_grad_kernel<Ty, V>, T, row_threads(nv), 0, st, (const Ty *)dz, lddz, (const Ty *)y, ldy,
+        // few tokens: a CTA for every eight pairs (16 tokens 7.0 -> 4.0 us); many: one for all of a token's
+        // (4096 tokens 167 us against 180; three CTAs an SM by registers, 154 us, against 177 with two)
+        const int nv = D / V, ky = T < 4 * k3_num_sms() ? std::min(65535, (K + 7) / 8) : 1;
+        k3_launch(rows_combine_grad_kernel<Ty, V>, dim3(T, ky), row_threads(nv), 0, st, (const Ty *)dz, lddz, (const Ty *)y, ldy,
                   n_rows, pos, weights, T, K, nv, (Ty *)dy, lddy, dweights, status);
     });
     k3_note_launch();
