@@ -24,21 +24,51 @@ template <> __device__ __forceinline__ float from_f32<float>(float v) { return v
 template <> __device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(float v) { return __float2bfloat16_rn(v); }
 template <> __device__ __forceinline__ __half from_f32<__half>(float v) { return __float2half_rn(v); }
 
-// Two values rounded together (one conversion instruction for the 16-bit types).
-__device__ __forceinline__ void store2(float *o, float a, float b) { o[0] = a, o[1] = b; }
-__device__ __forceinline__ void store2(__nv_bfloat16 *o, float a, float b)
+// Two values of a 16-bit type in a register, low half first.
+template <class T> __device__ __forceinline__ float2 unpack2(uint32_t w);
+template <> __device__ __forceinline__ float2 unpack2<__nv_bfloat16>(uint32_t w)
 {
-    *reinterpret_cast<__nv_bfloat162 *>(o) = __floats2bfloat162_rn(a, b);
+    return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
 }
-__device__ __forceinline__ void store2(__half *o, float a, float b)
+template <> __device__ __forceinline__ float2 unpack2<__half>(uint32_t w)
 {
-    *reinterpret_cast<__half2 *>(o) = __floats2half2_rn(a, b);
+    return __half22float2(*reinterpret_cast<const __half2 *>(&w));
+}
+template <class T> __device__ __forceinline__ uint32_t pack2(float a, float b);      // rounded to nearest even
+template <> __device__ __forceinline__ uint32_t pack2<__nv_bfloat16>(float a, float b)
+{
+    const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
+    return *reinterpret_cast<const uint32_t *>(&v);
+}
+template <> __device__ __forceinline__ uint32_t pack2<__half>(float a, float b)
+{
+    const __half2 v = __floats2half2_rn(a, b);
+    return *reinterpret_cast<const uint32_t *>(&v);
 }
 
-// V consecutive elements as one aligned access (V sizeof(T) = 2 to 32 bytes).
+// A piece of memory of V elements: 16 bytes kept as words until they are used (16-bit values held one to a
+// register cost the bf16 kernels up to 40 registers), or one element.
 template <class T, int V>
-struct alignas(V * sizeof(T) > 16 ? 16 : V * sizeof(T)) Vec {
-    T v[V];
+struct alignas(16) Vec {
+    static_assert(V * sizeof(T) == 16, "16 bytes, or one element");
+    uint32_t w[4];
+    // elements j and j + 1, j even
+    __device__ __forceinline__ float2 get2(int j) const
+    {
+        if constexpr (sizeof(T) == 4) return make_float2(__uint_as_float(w[j]), __uint_as_float(w[j + 1]));
+        else return unpack2<T>(w[j / 2]);
+    }
+    __device__ __forceinline__ void set2(int j, float a, float b)
+    {
+        if constexpr (sizeof(T) == 4) w[j] = __float_as_uint(a), w[j + 1] = __float_as_uint(b);
+        else w[j / 2] = pack2<T>(a, b);
+    }
+};
+template <class T>
+struct Vec<T, 1> {
+    T v;
+    __device__ __forceinline__ float2 get2(int) const { return make_float2(to_f32(v), 0.f); }
+    __device__ __forceinline__ void set2(int, float a, float) { v = from_f32<T>(a); }
 };
 
 }  // namespace k3

@@ -150,13 +150,15 @@ __global__ void __launch_bounds__(PIPE_THREADS) dropout_kernel(const T *x, const
             uint32_t w[V] = {};
             if (DROP) drop_words<V>((uint64_t)i * V, a, w);
             Vec<T, V> o;
-            float d[V];
 #pragma unroll
-            for (int j = 0; j < V; ++j) {
-                d[j] = kept<DROP>(to_f32(in[0].v[j]) * a.scale, w[j], a);
-                if (RES) d[j] += to_f32(in[RES].v[j]);
-                if (j % 2) store2(o.v + j - 1, d[j - 1], d[j]);
-                else if (V == 1) o.v[0] = from_f32<T>(d[0]);
+            for (int j = 0; j < V; j += 2) {
+                float2 d = in[0].get2(j);
+                d = {kept<DROP>(d.x * a.scale, w[j], a), kept<DROP>(d.y * a.scale, w[V == 1 ? 0 : j + 1], a)};
+                if (RES) {
+                    const float2 r = in[RES].get2(j);
+                    d = {d.x + r.x, d.y + r.y};
+                }
+                o.set2(j, d.x, d.y);
             }
             *reinterpret_cast<Vec<T, V> *>(out + i * V) = o;
         });
@@ -290,12 +292,12 @@ __device__ __forceinline__ bool all_within(const Vec<T, V> &v, float limit)
 {
     if constexpr (V == 8) {
         using T2 = std::conditional_t<std::is_same<T, __half>::value, __half2, __nv_bfloat162>;
-        const T2 *p = reinterpret_cast<const T2 *>(v.v);
+        const T2 *p = reinterpret_cast<const T2 *>(v.w);
         const T2 m = __hmax2_nan(__hmax2_nan(__habs2(p[0]), __habs2(p[1])), __hmax2_nan(__habs2(p[2]), __habs2(p[3])));
-        const T *e = reinterpret_cast<const T *>(&m);
-        return to_f32(e[0]) <= limit && to_f32(e[1]) <= limit;
+        const float2 e = unpack2<T>(*reinterpret_cast<const uint32_t *>(&m));
+        return e.x <= limit && e.y <= limit;
     } else {
-        return fabsf(to_f32(v.v[0])) <= limit;
+        return fabsf(v.get2(0).x) <= limit;
     }
 }
 
@@ -307,22 +309,18 @@ __device__ __forceinline__ void glu_piece(const Vec<T, V> (&in)[2 + GRAD], const
     const F2 scale = f2(a.scale);
 #pragma unroll
     for (int j = 0; j < V; j += 2) {
-        const int k = V == 1 ? 0 : j + 1;                // a single element is its own partner
-        F2 v0, v1;
-        glu_two<ACT, GRAD, SMALL>({to_f32(in[0].v[j]), to_f32(in[0].v[k])}, {to_f32(in[1].v[j]), to_f32(in[1].v[k])}, act,
-                                  v0, v1);
-        const F2 t = GRAD ? mul2({to_f32(in[1 + GRAD].v[j]), to_f32(in[1 + GRAD].v[k])}, scale) : scale;
+        const int k = V == 1 ? 0 : j + 1;
+        const float2 g = in[0].get2(j), u = in[1].get2(j);
+        F2 v0, v1, t = scale;
+        glu_two<ACT, GRAD, SMALL>({g.x, g.y}, {u.x, u.y}, act, v0, v1);
+        if (GRAD) {
+            const float2 d = in[1 + GRAD].get2(j);
+            t = mul2({d.x, d.y}, scale);
+        }
         if (DROP || GRAD) v0 = mul2(v0, t);
         if (GRAD) v1 = mul2(v1, t);
-        v0 = {kept<DROP>(v0.x, w[j], a), kept<DROP>(v0.y, w[k], a)};
-        if (GRAD) v1 = {kept<DROP>(v1.x, w[j], a), kept<DROP>(v1.y, w[k], a)};
-        if (V == 1) {
-            o0.v[0] = from_f32<T>(v0.x);
-            if (GRAD) o1.v[0] = from_f32<T>(v1.x);
-        } else {
-            store2(o0.v + j, v0.x, v0.y);
-            if (GRAD) store2(o1.v + j, v1.x, v1.y);
-        }
+        o0.set2(j, kept<DROP>(v0.x, w[j], a), kept<DROP>(v0.y, w[k], a));
+        if (GRAD) o1.set2(j, kept<DROP>(v1.x, w[j], a), kept<DROP>(v1.y, w[k], a));
     }
 }
 

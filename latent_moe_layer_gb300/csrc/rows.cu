@@ -163,7 +163,7 @@ __global__ void __launch_bounds__(256) rows_gather_kernel(const T *__restrict__ 
 // warp waiting: its lanes hold the token's rows and weights (32 at a time), and only rows that exist are
 // loaded, eight in flight, summed in k order.
 template <class T, int V>
-__global__ void __launch_bounds__(256) rows_combine_kernel(const T *__restrict__ y, int64_t ldy, int n_rows,
+__global__ void __launch_bounds__(256, 4) rows_combine_kernel(const T *__restrict__ y, int64_t ldy, int n_rows,
                                                            const int32_t *__restrict__ pos,
                                                            const float *__restrict__ wts, int T_, int K, int nv,
                                                            int split, T *__restrict__ z, int64_t ldz, int *status)
@@ -190,7 +190,7 @@ __global__ void __launch_bounds__(256) rows_combine_kernel(const T *__restrict__
         table(0);
         for (int i = first * 32 + lane; i - lane < nv; i += split * 32) {
             const bool in = i < nv;
-            float acc[V] = {};
+            float acc[V + (V == 1)] = {};
             for (int kb = 0; kb < K; kb += 32) {
                 if (K > 32) table(kb);
                 uint32_t live = __ballot_sync(0xffffffffu, row >= 0);
@@ -210,13 +210,17 @@ __global__ void __launch_bounds__(256) rows_combine_kernel(const T *__restrict__
                     for (int j = 0; j < 8; ++j)
                         if (j < n && in)
 #pragma unroll
-                            for (int q = 0; q < V; ++q) acc[q] = fmaf(f[j], to_f32(v[j].v[q]), acc[q]);
+                            for (int q = 0; q < V; q += 2) {
+                                const float2 d = v[j].get2(q);
+                                acc[q] = fmaf(f[j], d.x, acc[q]);
+                                if (V > 1) acc[q + 1] = fmaf(f[j], d.y, acc[q + 1]);
+                            }
                 }
             }
             if (in) {
                 Vec<T, V> o;
 #pragma unroll
-                for (int q = 0; q < V; ++q) o.v[q] = from_f32<T>(acc[q]);
+                for (int q = 0; q < V; q += 2) o.set2(q, acc[q], acc[q + 1]);
                 *reinterpret_cast<Vec<T, V> *>(z + t * ldz + (int64_t)i * V) = o;
             }
         }
@@ -280,10 +284,10 @@ __global__ void __launch_bounds__(256, 3) rows_combine_grad_kernel(const T *__re
                     if (r[j] >= 0) {
                         Vec<T, V> o;
 #pragma unroll
-                        for (int q = 0; q < V; ++q) {
-                            const float f = to_f32(d.v[q]);
-                            acc[j] = fmaf(f, to_f32(v[j].v[q]), acc[j]);
-                            o.v[q] = from_f32<T>(wt[j] * f);
+                        for (int q = 0; q < V; q += 2) {
+                            const float2 f = d.get2(q), g = v[j].get2(q);
+                            acc[j] = fmaf(f.y, g.y, fmaf(f.x, g.x, acc[j]));
+                            o.set2(q, wt[j] * f.x, wt[j] * f.y);
                         }
                         *reinterpret_cast<Vec<T, V> *>(dy + r[j] * lddy + (int64_t)i * V) = o;
                     }
