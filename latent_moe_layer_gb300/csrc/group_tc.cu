@@ -62,7 +62,7 @@ struct GroupTcArgs {
     int expert_coord;        // 0: one weight for all experts
     int bf16, accumulate;
     void *out;
-    int64_t ldo;
+    int64_t ldo, stride_o;
     int *status;
 };
 
@@ -154,11 +154,11 @@ __device__ __forceinline__ void load_rows(const CUtensorMap *maps, uint32_t dst,
     }
 }
 
-template <int MODE, class O>
+// CUT: grad_w's rows end inside 16 bytes (a variant of its own for the registers it costs).
+template <int MODE, class O, bool CUT>
 __global__ void __launch_bounds__(GroupSmem<MODE>::THREADS, 1) group_tc_kernel(const __grid_constant__ GroupMaps maps,
                                                                  const GroupTcArgs args)
 {
-    griddep_enter();
     using SM = GroupSmem<MODE>;
     constexpr int NS = SM::NS;
     constexpr bool W = MODE == K3_GROUP_GRAD_W;
@@ -172,14 +172,6 @@ __global__ void __launch_bounds__(GroupSmem<MODE>::THREADS, 1) group_tc_kernel(c
     const int *s_off = W ? args.offsets : s_int;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t rank = cluster_ctarank();
-
-    // every CTA reads the same offsets, so all agree on a refusal
-    if (W ? !group_offsets_ok<SM::THREADS>(args.offsets, args.E, args.rows, args.status)
-          : !group_tiles<SM::THREADS>(args.offsets, args.E, args.rows, GT_TILE_N, s_int, s_tile,
-                                     s_tile + K3MOE_TRAIN_MAX_EXPERTS + 1, args.status))
-        return;
-    const int mb = (args.M + GT_TILE_M - 1) / GT_TILE_M, cb = W ? (args.Nc + GT_TILE_N - 1) / GT_TILE_N : 1;
-    const int jobs = W ? args.E * mb * cb : s_tile[args.E] * mb;
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < NS; ++i) {
@@ -195,10 +187,21 @@ __global__ void __launch_bounds__(GroupSmem<MODE>::THREADS, 1) group_tc_kernel(c
         *abort_flag = 0;
         mbar_fence_init();
     }
-    if (warp == 1) tmem_alloc_pair(smem_u32(tmem_holder), 512);
-    tc_fence_before();
-    __syncthreads();
+    if (warp == 0 && lane < (W ? 2 : 6)) prefetch_tmap(lane == 0 ? &maps.a : &maps.b[lane - 1]);
     cluster_sync();                                      // barriers of both CTAs before any remote arrival
+
+    // all of the above may run while the previous kernel of the stream finishes; tensor memory may not
+    // be taken before, as that kernel may still have to
+    griddep_enter();
+    if (warp == 1) tmem_alloc_pair(smem_u32(tmem_holder), 512);
+    tc_fence_before();                                   // the CTA-wide barriers below publish the address
+    const bool offsets_ok = W ? group_offsets_ok<SM::THREADS>(args.offsets, args.E, args.rows, args.status)
+                              : group_tiles<SM::THREADS>(args.offsets, args.E, args.rows, GT_TILE_N, s_int, s_tile,
+                                                         s_tile + K3MOE_TRAIN_MAX_EXPERTS + 1, args.status);
+    const int mb = (args.M + GT_TILE_M - 1) / GT_TILE_M, cb = W ? (args.Nc + GT_TILE_N - 1) / GT_TILE_N : 1;
+    // every CTA reads the same offsets, so all agree on a refusal
+    const int jobs = !offsets_ok ? 0 : W ? args.E * mb * cb : s_tile[args.E] * mb;
+
     tc_fence_after();
     const uint32_t tmem = *tmem_holder;
 
@@ -206,10 +209,6 @@ __global__ void __launch_bounds__(GroupSmem<MODE>::THREADS, 1) group_tc_kernel(c
     if (warp == 0) {
         // ------------------------------------------------------------ TMA producer (each CTA its half)
         const bool one = elect_one();
-        if (one) {
-            prefetch_tmap(&maps.a);
-            for (int i = 0; i < (W ? 1 : 5); ++i) prefetch_tmap(&maps.b[i]);
-        }
         const uint32_t full0 = cluster_addr(smem_u32(full), 0);
         RingPos<NS> p, t;                                // stages; tails
         uint32_t issued = 0;
@@ -364,8 +363,11 @@ __global__ void __launch_bounds__(GroupSmem<MODE>::THREADS, 1) group_tc_kernel(c
 #pragma unroll
                 for (int g0 = 0; g0 < COLS; g0 += CW) {
                     const int c = part * COLS + g0;
+                    // a box that crosses the last column of rows that end inside 16 bytes: the copy engine
+                    // would write those 16 bytes whole, so its values are stored one by one
+                    const bool cut = CUT && j.c0 + c + CW > args.Nc;
                     if (m0 < args.M && j.c0 + c < args.Nc) {             // else wholly outside
-                        if (lane == 0) bulk_wait_read<0>();              // the box's previous store has read it
+                        if (!cut && lane == 0) bulk_wait_read<0>();              // the box's previous store has read it
                         __syncwarp();
 #pragma unroll
                         for (int h = 0; h < CW; h += 16) {
@@ -376,6 +378,14 @@ __global__ void __launch_bounds__(GroupSmem<MODE>::THREADS, 1) group_tc_kernel(c
                             } else if (chunks > 1) {
 #pragma unroll
                                 for (int i = 0; i < 16; ++i) v[i] = __float_as_uint(sum[g0 + h + i]);
+                            }
+                            if (cut) {
+                                O *o = out + walk.e * args.stride_o + (int64_t)(m0 + lane) * args.ldo + j.c0 + c + h;
+#pragma unroll
+                                for (int i = 0; i < 16; ++i)
+                                    if (m0 + lane < args.M && j.c0 + c + h + i < args.Nc)
+                                        o[i] = from_f32<O>(__uint_as_float(v[i]) + (args.accumulate ? to_f32(o[i]) : 0.f));
+                                continue;
                             }
                             // 16-byte pieces at the 128-byte swizzle's place: piece p of row r at p ^ (r % 8)
 #pragma unroll
@@ -395,7 +405,7 @@ __global__ void __launch_bounds__(GroupSmem<MODE>::THREADS, 1) group_tc_kernel(c
                         }
                         fence_proxy_async_smem();
                         __syncwarp();
-                        if (lane == 0) {
+                        if (!cut && lane == 0) {
                             if (args.accumulate) tma_add_3d(&maps.out, smem_u32(box), j.c0 + c, m0, walk.e);
                             else tma_store_3d(&maps.out, smem_u32(box), j.c0 + c, m0, walk.e);
                             bulk_commit();
@@ -473,11 +483,13 @@ static bool encode(CUtensorMap *m, int type, const void *base, int64_t cols, int
            CUDA_SUCCESS;
 }
 
-template <int MODE, class O>
+template <int MODE, class O, bool CUT = false>
 static int launch_tc(const GroupMaps &maps, const GroupTcArgs &a, int64_t max_jobs, cudaStream_t st)
 {
     using SM = GroupSmem<MODE>;
-    auto kern = group_tc_kernel<MODE, O>;
+    if constexpr (MODE == K3_GROUP_GRAD_W && !CUT)
+        if (a.Nc * sizeof(O) % 16) return launch_tc<MODE, O, true>(maps, a, max_jobs, st);
+    auto kern = group_tc_kernel<MODE, O, CUT>;
     static unsigned long long attr_set = 0;
     if (!k3_smem_attr(kern, SM::BYTES, attr_set)) return K3MOE_ERR_CUDA;
     const int sms = k3_num_sms();
@@ -530,6 +542,7 @@ int k3_group_tc(int mode, const K3Group &g, cudaStream_t st)
     a.accumulate = g.accumulate;
     a.out = g.out;
     a.ldo = g.ldo;
+    a.stride_o = g.stride_o;
     a.status = g.status;
     bool ok = true;
     if (mode == K3_GROUP_GRAD_W) {

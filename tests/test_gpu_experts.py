@@ -84,7 +84,7 @@ def _routing(T, K, E, drop, seed):
 
 @TYPES
 @pytest.mark.parametrize("T,K,D,drop", [(1, 1, 8, 0.0), (16, 16, 3584, 0.0), (5, 3, 7, 0.3), (300, 9, 200, 0.5),
-                                        (33, 32, 2056, 0.1), (4, 2, 5000, 0.0), (0, 4, 64, 0.0)])
+                                        (33, 32, 2056, 0.1), (4, 2, 5000, 0.0), (0, 4, 64, 0.0), (3, 40, 72, 0.2)])
 def test_gather_combine_and_gradient(T, K, D, drop, dt):
     gen = _gen(T + K + D)
     E = 40
@@ -259,6 +259,73 @@ def test_group_strides(dt):
             assert not got[:, :lead].any() and not got[:, lead + width:].any()
         assert torch.allclose(dw[:, :N, lead:lead + K], want[2], rtol=1e-4, atol=1e-3)
         assert not dw[:, N:].any() and not dw[..., :lead].any() and not dw[..., lead + K:].any()
+
+
+@TYPES
+def test_group_products_of_odd_widths_in_16_byte_rows(dt):
+    # the tensor-core path where a row's last piece is cut: widths 70 and 90 in rows of 80 and 96
+    sizes, K, N = [37, 0, 300, 5], 70, 90
+    off_d, off, x, dy, w = _group_inputs(sizes, K, N, dt)
+    pad = lambda t, n: torch.nn.functional.pad(t, (0, n - t.shape[-1]), value=float("nan"))[..., :t.shape[-1]]  # noqa: E731
+    x, dy, w = pad(x, 80), pad(dy, 96), pad(w, 80)
+    _check_group(off_d, off, x, dy, w)
+    dw = torch.full((4, N, 80), 5.0, device="cuda")
+    ex.group_mm_grad_w(dy, x, off_d, out=dw[..., :K])
+    assert (dw[..., K:] == 5).all()
+    dn, xn, rows = _np(dy), _np(x), np.diff(off)[:, None, None]
+    want, mag = ox.group_mm_grad_w(dn, xn, off), ox.group_mm_grad_w(np.abs(dn), np.abs(xn), off)
+    _close(dw[..., :K], want, (rows + 2) * 2.0 ** -23 * mag)
+    ex.group_mm_grad_w(dy, x, off_d, out=dw[..., :K], accumulate=True)
+    assert (dw[..., K:] == 5).all()
+    _close(dw[..., :K], 2 * want, 2 * (rows + 3) * 2.0 ** -23 * mag)
+
+
+def test_grad_w_of_long_groups_keeps_fp32_precision():
+    # sums of 512-row parts in fp32: a rounding (2^-24) per part and the parts' own truncation (n 2^-23 / 16 of
+    # a running sum at most); against the norm of the result 2e-6 covers both at any length
+    off_d, off, x, dy, w = _group_inputs([20011, 3, 0, 1025], 128, 256, BF)
+    dw = ex.group_mm_grad_w(dy, x, off_d).double()
+    for e, (a, b) in enumerate(zip(off[:-1], off[1:])):
+        want = dy[a:b].double().T @ x[a:b].double()
+        assert torch.linalg.norm(dw[e] - want) <= 2e-6 * torch.linalg.norm(want)
+
+
+def test_many_experts():
+    rng = np.random.default_rng(0)
+    sizes = (rng.integers(0, 4, 1024) * (rng.random(1024) < 0.5)).tolist()
+    _check_group(*_group_inputs(sizes, 64, 72, BF))
+
+
+def test_element_offsets_past_31_bits():
+    # 700,000 rows of 3584: element offsets up to 2.5e9
+    rows, D = 700_000, 3584
+    y = torch.empty(rows, D, dtype=BF, device="cuda")
+    gen = _gen(9)
+    last = _rand(gen, 60, D)
+    y[-60:] = last
+    pos = torch.tensor([[rows - 1, rows - 60], [rows - 30, -1]], dtype=torch.int32, device="cuda")
+    mix = torch.tensor([[0.5, 2.0], [1.0, 3.0]], device="cuda")
+    assert torch.equal(ex.combine_rows(y, pos, mix),
+                       torch.stack([last[59].float() * 0.5 + last[0].float() * 2, last[30].float()]).to(BF))
+    x = _rand(gen, 2, D)
+    dy, dmix = ex.combine_rows_grad(x, y, pos, mix, out=torch.empty_like(y))
+    assert torch.equal(dy[rows - 30], x[1]) and torch.equal(dy[rows - 1], (x[0].float() * 0.5).to(BF))
+    del dy
+    ex.gather_rows(x, pos, out=y)
+    assert torch.equal(y[-1], x[0]) and torch.equal(y[-60], x[0]) and torch.equal(y[-30], x[1])
+    w = _rand(gen, 2, 64, D, scale=D ** -0.5)
+    off = torch.tensor([rows - 50, rows - 31, rows], dtype=torch.int32, device="cuda")
+    got = ex.group_mm(y, w, off)
+    want = torch.cat([y[-50:-31].double() @ w[0].double().T, y[-31:].double() @ w[1].double().T])
+    assert ((got[-50:].double() - want).abs() <= HALF[BF] * want.abs() + 1e-4).all()
+    dx = ex.group_mm_grad_x(got, w, off)
+    want = torch.cat([got[-50:-31].double() @ w[0].double(), got[-31:].double() @ w[1].double()])
+    assert ((dx[-50:].double() - want).abs() <= HALF[BF] * want.abs() + 1e-4).all()
+    dw = ex.group_mm_grad_w(got, y, off)
+    want = got[-31:].double().T @ y[-31:].double()
+    assert ((dw[1].double() - want).abs() <= 33 * 2.0 ** -23 * (got[-31:].double().abs().T @ y[-31:].double().abs())).all()
+    del y, dx
+    torch.cuda.empty_cache()
 
 
 def test_one_weight_for_all_groups():
