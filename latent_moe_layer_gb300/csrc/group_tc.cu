@@ -49,8 +49,8 @@ struct GroupSmem {
 };
 
 struct GroupMaps {
-    CUtensorMap a;           // mm: box 64 x 128 rows; grad_x, grad_w: box 64 x 64
-    CUtensorMap b[5];        // mm, grad_x: boxes of 128, 64, 32, 16, 8 rows; grad_w: b[0], box 64 x 64
+    CUtensorMap a;           // mm: box 64 x 128 rows; grad_x, grad_w: box 64 x 64, or two of them (wide)
+    CUtensorMap b[5];        // mm, grad_x: boxes of 128, 64, 32, 16, 8 rows; grad_w: b[0] as a
     CUtensorMap out;         // grad_w
 };
 
@@ -60,6 +60,7 @@ struct GroupTcArgs {
     int K;                   // contraction of mm and grad_x
     int l2_tiles;            // row tiles of GT_L2_ROWS bytes
     int expert_coord;        // 0: one weight for all experts
+    int wide_a, wide_b;      // MN-major operands whose width is a multiple of 64: both 64 x 64 boxes in one copy
     int bf16, accumulate;
     void *out;
     int64_t ldo, stride_o;
@@ -236,16 +237,28 @@ __global__ void __launch_bounds__(GroupSmem<MODE>::THREADS, 1) group_tc_kernel(c
                     if (MODE == K3_GROUP_MM) {
                         tma_load_3d_pair(a_dst, &maps.a, bar, k, m, e);
                     } else if (MODE == K3_GROUP_GRAD_X) {
-                        tma_load_3d_pair(a_dst, &maps.a, bar, m, k, e);
-                        tma_load_3d_pair(a_dst + GT_A_BYTES / 2, &maps.a, bar, m + 64, k, e);
+                        if (args.wide_a) {
+                            tma_load_4d_pair(a_dst, &maps.a, bar, 0, k, m / 64, e);
+                        } else {
+                            tma_load_3d_pair(a_dst, &maps.a, bar, m, k, e);
+                            tma_load_3d_pair(a_dst + GT_A_BYTES / 2, &maps.a, bar, m + 64, k, e);
+                        }
                     }
                     if (!W) {
                         load_rows(maps.b, b_dst, bar, k, c, half);
                     } else {
-                        tma_load_2d_pair(a_dst, &maps.a, bar, m, r0 + k);
-                        tma_load_2d_pair(a_dst + GT_A_BYTES / 2, &maps.a, bar, m + 64, r0 + k);
-                        tma_load_2d_pair(b_dst, &maps.b[0], bar, c, r0 + k);
-                        tma_load_2d_pair(b_dst + GT_A_BYTES / 2, &maps.b[0], bar, c + 64, r0 + k);
+                        if (args.wide_a) {
+                            tma_load_3d_pair(a_dst, &maps.a, bar, 0, r0 + k, m / 64);
+                        } else {
+                            tma_load_2d_pair(a_dst, &maps.a, bar, m, r0 + k);
+                            tma_load_2d_pair(a_dst + GT_A_BYTES / 2, &maps.a, bar, m + 64, r0 + k);
+                        }
+                        if (args.wide_b) {
+                            tma_load_3d_pair(b_dst, &maps.b[0], bar, 0, r0 + k, c / 64);
+                        } else {
+                            tma_load_2d_pair(b_dst, &maps.b[0], bar, c, r0 + k);
+                            tma_load_2d_pair(b_dst + GT_A_BYTES / 2, &maps.b[0], bar, c + 64, r0 + k);
+                        }
                     }
                 }
                 __syncwarp();
@@ -464,9 +477,8 @@ static EncodeFn encode_fn()
     return fn;
 }
 
-// Tiled map over `n2` matrices of [rows, cols] (n2 = 0: two dimensions), 128-byte swizzle.
-static bool encode(CUtensorMap *m, int type, const void *base, int64_t cols, int64_t rows, int64_t n2, int64_t ld,
-                   int64_t stride2, int box_cols, int box_rows)
+static bool encode(CUtensorMap *m, int type, const void *base, int nd, const int64_t (&dim)[4], const int64_t (&stride)[3],
+                   const int (&box)[4])
 {
     EncodeFn fn = encode_fn();
     if (!fn) return false;
@@ -474,13 +486,32 @@ static bool encode(CUtensorMap *m, int type, const void *base, int64_t cols, int
     const CUtensorMapDataType dt = type == K3MOE_TYPE_F32    ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
                                    : type == K3MOE_TYPE_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
                                                              : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
-    cuuint64_t dims[3] = {(cuuint64_t)cols, (cuuint64_t)rows, (cuuint64_t)(n2 > 0 ? n2 : 1)};
-    cuuint64_t strides[2] = {(cuuint64_t)(ld * es), (cuuint64_t)(stride2 * es)};
-    cuuint32_t box[3] = {(cuuint32_t)box_cols, (cuuint32_t)box_rows, 1};
-    cuuint32_t one[3] = {1, 1, 1};
-    return fn(m, dt, n2 > 0 ? 3 : 2, const_cast<void *>(base), dims, strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
-              CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) ==
-           CUDA_SUCCESS;
+    cuuint64_t d[4], st[3];
+    cuuint32_t b[4], one[4] = {1, 1, 1, 1};
+    for (int i = 0; i < nd; ++i) {
+        d[i] = (cuuint64_t)dim[i];
+        b[i] = (cuuint32_t)box[i];
+        if (i + 1 < nd) st[i] = (cuuint64_t)(stride[i] * es);
+    }
+    return fn(m, dt, nd, const_cast<void *>(base), d, st, b, one, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// Map over `n2` matrices of [rows, cols] (n2 = 0: two dimensions), 128-byte swizzle, 128-byte box rows.
+static bool encode_rows(CUtensorMap *m, int type, const void *base, int64_t cols, int64_t rows, int64_t n2, int64_t ld,
+                        int64_t stride2, int box_rows)
+{
+    return encode(m, type, base, n2 > 0 ? 3 : 2, {cols, rows, n2, 1}, {ld, stride2, 0},
+                  {128 / k3_type_bytes(type), box_rows, 1, 1});
+}
+
+// The same matrices of 16-bit elements as [n2][cols / 64][rows][64], where that is whole: a box of two blocks is
+// what an MN-major operand of 128 columns wants in one copy (grad_w of 57,344 rows over 28 experts: 1.53 ms, 1.56 with
+// two copies an operand).
+static bool encode_wide(CUtensorMap *m, int type, const void *base, int64_t cols, int64_t rows, int64_t n2, int64_t ld,
+                        int64_t stride2)
+{
+    return encode(m, type, base, n2 > 0 ? 4 : 3, {64, rows, cols / 64, n2}, {ld, 64, stride2}, {64, 64, 2, 1});
 }
 
 template <int MODE, class O, bool CUT = false>
@@ -550,9 +581,13 @@ int k3_group_tc(int mode, const K3Group &g, cudaStream_t st)
         a.Nc = g.n_in;
         a.expert_coord = 1;
         const int64_t so = g.E > 1 ? g.stride_o : (int64_t)g.n_out * g.ldo;
-        ok = encode(&maps.a, g.dtype, g.a, g.n_out, g.rows, 0, g.lda, 0, 64, 64) &&
-             encode(&maps.b[0], g.dtype, g.b, g.n_in, g.rows, 0, g.ldb, 0, 64, 64) &&
-             encode(&maps.out, g.out_dtype, g.out, g.n_in, g.n_out, g.E, g.ldo, so, 128 / k3_type_bytes(g.out_dtype), 32);
+        a.wide_a = g.n_out % 64 == 0;
+        a.wide_b = g.n_in % 64 == 0;
+        ok = (a.wide_a ? encode_wide(&maps.a, g.dtype, g.a, g.n_out, g.rows, 0, g.lda, 0)
+                       : encode_rows(&maps.a, g.dtype, g.a, g.n_out, g.rows, 0, g.lda, 0, 64)) &&
+             (a.wide_b ? encode_wide(&maps.b[0], g.dtype, g.b, g.n_in, g.rows, 0, g.ldb, 0)
+                       : encode_rows(&maps.b[0], g.dtype, g.b, g.n_in, g.rows, 0, g.ldb, 0, 64)) &&
+             encode_rows(&maps.out, g.out_dtype, g.out, g.n_in, g.n_out, g.E, g.ldo, so, 32);
         for (int i = 1; i < 5; ++i) maps.b[i] = maps.b[0];
         if (!ok) return K3MOE_ERR_CUDA;
         const int64_t jobs = (int64_t)g.E * ((a.M + GT_TILE_M - 1) / GT_TILE_M) * ((a.Nc + GT_TILE_N - 1) / GT_TILE_N);
@@ -566,8 +601,10 @@ int k3_group_tc(int mode, const K3Group &g, cudaStream_t st)
     a.expert_coord = g.E > 1 && g.stride_b > 0;
     a.l2_tiles = (int)std::max<int64_t>(1, GT_L2_ROWS / ((int64_t)GT_TILE_N * a.K * 2));
     const int64_t nw = a.expert_coord ? g.E : 1, sw = a.expert_coord ? g.stride_b : (int64_t)g.n_out * g.ldb;
-    ok = encode(&maps.a, g.dtype, g.b, g.n_in, g.n_out, nw, g.ldb, sw, 64, mm ? 128 : 64);
-    for (int i = 0; i < 5; ++i) ok = ok && encode(&maps.b[i], g.dtype, g.a, a.K, g.rows, 0, g.lda, 0, 64, 128 >> i);
+    a.wide_a = !mm && g.n_in % 64 == 0;
+    ok = a.wide_a ? encode_wide(&maps.a, g.dtype, g.b, g.n_in, g.n_out, nw, g.ldb, sw)
+                  : encode_rows(&maps.a, g.dtype, g.b, g.n_in, g.n_out, nw, g.ldb, sw, mm ? 128 : 64);
+    for (int i = 0; i < 5; ++i) ok = ok && encode_rows(&maps.b[i], g.dtype, g.a, a.K, g.rows, 0, g.lda, 0, 128 >> i);
     maps.out = maps.a;
     if (!ok) return K3MOE_ERR_CUDA;
     // at most one partly filled tile an expert with rows
