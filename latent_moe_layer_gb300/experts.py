@@ -48,11 +48,11 @@ def _type(t, what):
     return code
 
 
-def _out(out, n, width, dtype, dev, what="out"):
-    """`out` (checked) or a new [n, width] matrix of `dtype` -> (matrix, row stride)."""
+def _out(out, n, width, dtype, ref, what="out"):
+    """`out` (checked) or a new [n, width] matrix of `dtype` on ref's device -> (matrix, row stride)."""
     if out is None:
-        return torch.empty((n, width), dtype=dtype, device=dev), width
-    rows, _, ld = _rows(out, what, dev, width)
+        return torch.empty((n, width), dtype=dtype, device=ref.device), width     # a device number costs 2 us more
+    rows, _, ld = _rows(out, what, ref.get_device(), width)
     if rows != n or out.dtype != dtype:
         _refuse(f"{what}: {n} rows of {dtype}")
     return out, ld
@@ -126,8 +126,8 @@ def plan_rows(idx, n_experts, first_expert=0, *, s):
         if len(_ws_bytes) > 4096:
             _ws_bytes.clear()
         nb = _ws_bytes[key] = max(4, L.k3moe_rows_plan_workspace_bytes(T, K, n_experts))
-    new, i32 = torch.empty, torch.int32
-    ws, offsets = new((nb + 3) // 4, dtype=i32, device=dev), new(max(n_experts, 0) + 1, dtype=i32, device=dev)
+    new, i32, where = torch.empty, torch.int32, idx.device
+    ws, offsets = new((nb + 3) // 4, dtype=i32, device=where), new(max(n_experts, 0) + 1, dtype=i32, device=where)
     pos = torch.empty_like(idx)
     check(L.k3moe_rows_plan(idx.data_ptr(), T, K, first_expert, n_experts, offsets.data_ptr(), pos.data_ptr(),
                             ws.data_ptr(), nb, s), "plan_rows")
@@ -142,7 +142,7 @@ def gather_rows(x, pos, n_rows=None, out=None, *, s):
     T, D, ldx = _rows(x, "x", dev)
     K = _pairs(pos, "pos", dev, T)[1]
     if out is None:
-        out = torch.empty((T * K if n_rows is None else n_rows, D), dtype=x.dtype, device=dev)
+        out = torch.empty((T * K if n_rows is None else n_rows, D), dtype=x.dtype, device=x.device)
     n, _, ldo = _rows(out, "out", dev, D)
     if out.dtype != x.dtype or (n_rows is not None and n_rows > n):
         _refuse("out: x's type and at least n_rows rows")
@@ -159,7 +159,7 @@ def combine_rows(y, pos, weights=None, out=None, *, s):
     T, K = _pairs(pos, "pos", dev)
     if weights is not None:
         _table(weights, "weights", dev, torch.float32, (T, K))
-    out, ldz = _out(out, T, D, y.dtype, dev)
+    out, ldz = _out(out, T, D, y.dtype, y)
     check(lib().k3moe_rows_combine(y.data_ptr(), ldy, n, pos.data_ptr(), None if weights is None else weights.data_ptr(),
                                    T, K, D, _type(y, "y"), out.data_ptr(), ldz, _status_word(dev), s), "combine_rows")
     return out
@@ -175,7 +175,7 @@ def combine_rows_grad(dz, y, pos, weights, out=None, *, s):
     _table(weights, "weights", dev, torch.float32, (T, K))
     if dz.dtype != y.dtype:
         _refuse("dz: y's type")
-    out, lddy = _out(out, n, D, y.dtype, dev)
+    out, lddy = _out(out, n, D, y.dtype, y)
     dw = torch.empty_like(weights)
     check(lib().k3moe_rows_combine_grad(dz.data_ptr(), lddz, y.data_ptr(), ldy, n, pos.data_ptr(), weights.data_ptr(), T,
                                         K, D, _type(y, "y"), out.data_ptr(), lddy, dw.data_ptr(), _status_word(dev), s),
@@ -202,7 +202,7 @@ def _group(name, what, a, w, offsets, out, out_dtype, s, mm):
         _refuse(f"{what}: w's type")
     _table(offsets, "offsets", dev, torch.int32, (E + 1,))
     width = N if mm else K
-    out, ldo = _out(out, n, width, out_dtype or (a.dtype if out is None else out.dtype), dev)
+    out, ldo = _out(out, n, width, out_dtype or (a.dtype if out is None else out.dtype), a)
     check(getattr(lib(), name)(offsets.data_ptr(), E, n, K, N, a.data_ptr(), lda, w.data_ptr(), ldw, sw, _type(a, what),
                                out.data_ptr(), ldo, _type(out, "out"), _status_word(dev), s), name)
     return out
@@ -241,7 +241,7 @@ def group_mm_grad_w(dy, x, offsets, out=None, out_dtype=None, accumulate=False, 
     if out is None:
         if accumulate:
             _refuse("accumulate needs out")
-        out = torch.empty((E, N, K), dtype=out_dtype or torch.float32, device=dev)
+        out = torch.empty((E, N, K), dtype=out_dtype or torch.float32, device=x.device)
     Eo, No, Ko, ldo, so = _matrices(out, "out", dev)
     if (Eo, No, Ko) != (E, N, K) or (out_dtype is not None and out.dtype != out_dtype):
         _refuse("out: [E, n_out, n_in] of the type asked for")
@@ -272,7 +272,7 @@ def glu_dropout(gu, p=0.0, seed=0, offset=0, act="silu", situ_beta=4.0, situ_lin
     dev = gu.get_device()
     n, width, ldgu = _gated(gu, act, dev)
     _random(p, seed, offset)
-    out, lda = _out(out, n, width, gu.dtype, dev)
+    out, lda = _out(out, n, width, gu.dtype, gu)
     check(lib().k3moe_glu_dropout(gu.data_ptr(), ldgu, n, width, _type(gu, "gu"), _ACT[act], situ_beta,
                                   situ_linear_beta, p, seed, offset, out.data_ptr(), lda, s), "glu_dropout")
     return out
@@ -287,7 +287,7 @@ def glu_dropout_grad(da, gu, p=0.0, seed=0, offset=0, act="silu", situ_beta=4.0,
     if da.dtype != gu.dtype or na != n:
         _refuse("da: gu's rows and type")
     _random(p, seed, offset)
-    out, ldo = _out(out, n, 2 * width, gu.dtype, dev)
+    out, ldo = _out(out, n, 2 * width, gu.dtype, gu)
     check(lib().k3moe_glu_dropout_grad(da.data_ptr(), ldda, gu.data_ptr(), ldgu, n, width, _type(gu, "gu"), _ACT[act],
                                        situ_beta, situ_linear_beta, p, seed, offset, out.data_ptr(), ldo, s),
           "glu_dropout_grad")
