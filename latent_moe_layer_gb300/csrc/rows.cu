@@ -11,7 +11,8 @@ namespace k3 {
 // and its own first row of each expert, and numbers its pairs in order, PLAN_SUB at a time: each of
 // the 32 warps numbers 64 consecutive pairs against its own counters, in two rounds of 32 in which
 // lanes of the same expert find each other by match_any, and a scan over the warps' counters joins
-// them.  Order is by pair alone, no atomics decide it.
+// them.  Order is by pair alone, no atomics decide it.  Bound by latency: 16 x 16 pairs over 896 experts
+// 3.8 us (one launch), 8192 x 16 pairs 9.9 us.
 constexpr int PLAN_THREADS = 1024, PLAN_SUB = 2048, PLAN_BLOCKS = 128;
 
 __device__ __forceinline__ int plan_expert(const int32_t *idx, int64_t p, int64_t n, int first, int E)
@@ -134,6 +135,8 @@ __global__ void __launch_bounds__(PLAN_THREADS) plan_place_kernel(const int32_t 
 }
 
 // ------------------------------------------------------------------ gather
+// A CTA per token reads its row once and writes its K copies.  HBM writes bind it: 4096 x 16 rows of 3584
+// bf16 take 80 us, 6.2 TB/s.
 template <class T, int V>
 __global__ void __launch_bounds__(256) rows_gather_kernel(const T *__restrict__ x, int64_t ldx,
                                                           const int32_t *__restrict__ pos, int T_, int K, int nv,
@@ -161,7 +164,8 @@ __global__ void __launch_bounds__(256) rows_gather_kernel(const T *__restrict__ 
 // ------------------------------------------------------------------ combine
 // `split` warps per token, each with every split-th piece of 32 V columns, so that nothing but memory keeps a
 // warp waiting: its lanes hold the token's rows and weights (32 at a time), and only rows that exist are
-// loaded, eight in flight, summed in k order.
+// loaded, eight in flight, summed in k order.  Reads of 512 bytes here and there bind it: 4096 x 16 rows of
+// 3584 in 90 us, 5.5 TB/s; 16 tokens 2.8 us.
 template <class T, int V>
 __global__ void __launch_bounds__(256, 4) rows_combine_kernel(const T *__restrict__ y, int64_t ldy, int n_rows,
                                                            const int32_t *__restrict__ pos,
@@ -247,7 +251,8 @@ __device__ __forceinline__ void warp_sum8(float (&v)[8], int lane)
 }
 
 // CTA per token and eight pairs (or all its pairs, eight at a time): dz's row, the pairs' y rows read and their dy rows written (in that order
-// by the same thread, so dy may be y), dot products summed per thread, warp and CTA in fixed order.
+// by the same thread, so dy may be y), dot products summed per thread, warp and CTA in fixed order.  HBM
+// binds it: 4096 x 16 rows of 3584 bf16 in 148 us, 6.5 TB/s.
 template <class T, int V>
 __global__ void __launch_bounds__(256, 3) rows_combine_grad_kernel(const T *__restrict__ dz, int64_t lddz, const T *y,
                                                                 int64_t ldy, int n_rows,
