@@ -1,10 +1,12 @@
-"""Compile libk3moe.so (every .cu under csrc/) for sm_103a with nvcc, in-tree."""
+"""Compile libk3moe.so (every .cu under csrc/) for sm_103a with nvcc, and the Python binding of the expert
+training operators (csrc/experts_py.cpp, against the installed PyTorch) with the host compiler; in-tree."""
 from __future__ import annotations
 
 import glob
 import os
 import subprocess
 import sys
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -12,6 +14,8 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libk3moe.so")
+BINDING = os.path.join(PKG, "_experts.so")
+BINDING_SRC = os.path.join(CSRC, "experts_py.cpp")
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-I", os.path.join(ROOT, "include"),
@@ -30,7 +34,38 @@ def _stale() -> bool:
     return any(os.path.getmtime(f) > t for f in _deps())
 
 
+def _build_binding() -> None:
+    import torch
+    base = os.path.dirname(torch.__file__)
+    inc = [sysconfig.get_paths()["include"], os.path.join(base, "include"),
+           os.path.join(base, "include", "torch", "csrc", "api", "include"),
+           os.path.join(os.path.dirname(os.path.dirname(NVCC)), "include"), os.path.join(ROOT, "include")]
+    lib = os.path.join(base, "lib")
+    tmp = BINDING + f".tmp{os.getpid()}"
+    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++20", "-fPIC", "-fvisibility=hidden", "-shared",
+           *[a for i in inc for a in ("-isystem", i)], f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}", "-o", tmp,
+           BINDING_SRC, f"-L{lib}", f"-Wl,-rpath,{lib}", "-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10", "-lc10_cuda"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"the host compiler failed on {BINDING_SRC}:\n{r.stderr}")
+    os.replace(tmp, BINDING)
+
+
+def _binding_stale() -> bool:
+    return not os.path.exists(BINDING) or any(
+        os.path.getmtime(f) > os.path.getmtime(BINDING) for f in (BINDING_SRC, os.path.join(ROOT, "include", "k3moe.h")))
+
+
 def build(force: bool = False, verbose: bool = False) -> str:
+    with ThreadPoolExecutor(1) as ex:                       # beside the CUDA sources
+        binding = ex.submit(_build_binding) if force or _binding_stale() else None
+        lib = _build_library(force, verbose)
+        if binding:
+            binding.result()
+    return lib
+
+
+def _build_library(force: bool, verbose: bool) -> str:
     if not force and not _stale():
         return LIB
     os.makedirs(BUILD, exist_ok=True)

@@ -164,8 +164,8 @@ __device__ __forceinline__ void load_rows(const CUtensorMap *maps, uint32_t dst,
 
 // CUT: grad_w's rows end inside 16 bytes (a variant of its own for the registers it costs).
 template <int MODE, class O, bool CUT>
-__global__ void __launch_bounds__(GroupSmem<MODE>::THREADS, 1) group_tc_kernel(const __grid_constant__ GroupMaps maps,
-                                                                 const GroupTcArgs args)
+__global__ void __launch_bounds__(GroupSmem<MODE>::THREADS, 1)
+    group_tc_kernel(const __grid_constant__ GroupMaps maps, const GroupTcArgs args)
 {
     using SM = GroupSmem<MODE>;
     constexpr int NS = SM::NS;
@@ -277,6 +277,13 @@ __global__ void __launch_bounds__(GroupSmem<MODE>::THREADS, 1) group_tc_kernel(c
             if (issued < (uint32_t)NS && q == 0) p.slot = 0, p.phase = 1;
             ok = pair_wait(smem_u32(empty + p.slot), p.phase ^ 1, abort_flag, args.status, 62);
         }
+        if (!ok) {
+            // given up: the copies in flight land before the shared memory is given back.  The even CTA waits
+            // for the stages that both announced; what only one of them did is far past its latency in 1 ms.
+            if (rank == 0) drain_ring(full, issued, NS);
+            const uint64_t t0 = globaltimer();
+            while (globaltimer() - t0 < 1000000) __nanosleep(1000);
+        }
     } else if (warp == 1 && rank == 0) {
         // ------------------------------------------------------------ MMA issuer (even CTA, for both)
         const uint32_t major = (MODE == K3_GROUP_MM ? 0 : IDESC_A_MN) | (W ? IDESC_B_MN : 0);
@@ -387,7 +394,7 @@ __global__ void __launch_bounds__(GroupSmem<MODE>::THREADS, 1) group_tc_kernel(c
                     // would write those 16 bytes whole, so its values are stored one by one
                     const bool cut = CUT && j.c0 + c + CW > args.Nc;
                     if (m0 < args.M && j.c0 + c < args.Nc) {             // else wholly outside
-                        if (!cut && lane == 0) bulk_wait_read<0>();              // the box's previous store has read it
+                        if (!cut && lane == 0) bulk_wait_read<0>();      // the box's previous store has read it
                         __syncwarp();
 #pragma unroll
                         for (int h = 0; h < CW; h += 16) {
@@ -412,12 +419,14 @@ __global__ void __launch_bounds__(GroupSmem<MODE>::THREADS, 1) group_tc_kernel(c
                             for (int p = 0; p < (int)sizeof(O); ++p) {
                                 uint4 w;
                                 if (sizeof(O) == 4) {
-                                    w = make_uint4(v[(4 * p) & 15], v[(4 * p + 1) & 15], v[(4 * p + 2) & 15], v[(4 * p + 3) & 15]);
+                                    const uint32_t *f = v + (4 * p & 15);
+                                    w = make_uint4(f[0], f[1], f[2], f[3]);
                                 } else {
-                                    O o[8];
+                                    Vec<std::conditional_t<sizeof(O) == 4, __half, O>, 8> o;
 #pragma unroll
-                                    for (int i = 0; i < 8; ++i) o[i] = from_f32<O>(__uint_as_float(v[(8 * p + i) & 15]));
-                                    w = *reinterpret_cast<uint4 *>(o);
+                                    for (int i = 0; i < 8; i += 2)
+                                        o.set2(i, __uint_as_float(v[(8 * p + i) & 15]), __uint_as_float(v[(8 * p + i + 1) & 15]));
+                                    w = make_uint4(o.w[0], o.w[1], o.w[2], o.w[3]);
                                 }
                                 const int piece = h * (int)sizeof(O) / 16 + p;
                                 *reinterpret_cast<uint4 *>(box + lane * 128 + ((piece ^ (lane & 7)) << 4)) = w;
@@ -598,7 +607,7 @@ int k3_group_tc(int mode, const K3Group &g, cudaStream_t st)
         for (int i = 1; i < 5; ++i) maps.b[i] = maps.b[0];
         if (!ok) return K3MOE_ERR_CUDA;
         const int64_t jobs = (int64_t)g.E * ((a.M + GT_TILE_M - 1) / GT_TILE_M) * ((a.Nc + GT_TILE_N - 1) / GT_TILE_N);
-        if (jobs >= (1LL << 31)) return K3MOE_ERR_SHAPE;
+        if (jobs >= (1LL << 30)) return K3MOE_ERR_SHAPE;
         return launch_typed<K3_GROUP_GRAD_W>(maps, a, g.out_dtype, jobs, st);
     }
     const bool mm = mode == K3_GROUP_MM;
@@ -616,7 +625,7 @@ int k3_group_tc(int mode, const K3Group &g, cudaStream_t st)
     if (!ok) return K3MOE_ERR_CUDA;
     // at most one partly filled tile an expert with rows
     const int64_t jobs = ((int64_t)g.rows / GT_TILE_N + std::min(g.E, g.rows)) * ((a.M + GT_TILE_M - 1) / GT_TILE_M);
-    if (jobs >= (1LL << 31)) return K3MOE_ERR_SHAPE;
+    if (jobs >= (1LL << 30)) return K3MOE_ERR_SHAPE;
     return mm ? launch_typed<K3_GROUP_MM>(maps, a, g.out_dtype, jobs, st)
               : launch_typed<K3_GROUP_GRAD_X>(maps, a, g.out_dtype, jobs, st);
 }

@@ -250,8 +250,8 @@ __device__ __forceinline__ void warp_sum8(float (&v)[8], int lane)
     v[0] += __shfl_xor_sync(0xffffffffu, v[0], 1);
 }
 
-// CTA per token and eight pairs (or all its pairs, eight at a time): dz's row, the pairs' y rows read and their dy rows written (in that order
-// by the same thread, so dy may be y), dot products summed per thread, warp and CTA in fixed order.  HBM
+// CTA per token and eight pairs (or all its pairs, eight at a time): dz's row, the pairs' y rows read and
+// their dy rows written (in that order by the same thread, so dy may be y), dot products summed per thread, warp and CTA in fixed order.  HBM
 // binds it: 4096 x 16 rows of 3584 bf16 in 148 us, 6.5 TB/s.
 template <class T, int V>
 __global__ void __launch_bounds__(256, 3) rows_combine_grad_kernel(const T *__restrict__ dz, int64_t lddz, const T *y,
