@@ -17,8 +17,8 @@ __global__ void __launch_bounds__(GG_THREADS) group_generic_kernel(const K3Group
 {
     griddep_enter();
     __shared__ float sa[GG_K][GG_TILE + 1], sb[GG_K][GG_TILE + 1];
-    __shared__ int s_off[K3MOE_TRAIN_MAX_EXPERTS + 1], s_tile[K3MOE_TRAIN_MAX_EXPERTS + 1], s_tmp[34];
-    if (!group_tiles<GG_THREADS>(g.offsets, g.E, g.rows, GG_TILE, s_off, s_tile, s_tmp, g.status)) return;
+    __shared__ int s_off[K3MOE_TRAIN_MAX_EXPERTS + 1], s_tile[K3MOE_TRAIN_MAX_EXPERTS + 1], s_tmp[GG_THREADS / 32];
+    if (!group_tiles<GG_THREADS, GG_TILE>(g.offsets, g.E, g.rows, s_off, s_tile, s_tmp, g.status)) return;
     const T *A = static_cast<const T *>(g.a), *B = static_cast<const T *>(g.b);
     O *out = static_cast<O *>(g.out);
     const int M = MODE == K3_GROUP_GRAD_X ? g.n_in : g.n_out;            // tile rows

@@ -5,13 +5,30 @@
 
 namespace k3 {
 
-// All threads of the CTA (a multiple of 32): s_off[0 .. E] = the offsets, s_tile[0 .. E] = exclusive
-// prefix of each expert's tiles of at most `tile` rows (none for an empty expert).  Returns false,
-// after recording K3MOE_ERR_RANGE, when the offsets decrease or leave [0, rows].  s_tmp: 34 ints.
-template <int THREADS>
-__device__ __forceinline__ bool group_tiles(const int32_t *__restrict__ offsets, int E, int rows, int tile, int *s_off,
-                                            int *s_tile, int *s_tmp, int *status)
+// Rows of a tile, TILE >> i for the i < PICK with the least cost, larger first: rounds of the `pairs` workers over
+// `blocks` jobs a tile, times what a stage costs a worker (256 + rows cycles, see group_tc.cu).  Returns i.
+template <int TILE, int PICK>
+__device__ __forceinline__ int pick_tile(const int (&tiles)[PICK], int blocks, int pairs)
 {
+    int best = 0;
+    uint64_t cost = 0;
+#pragma unroll
+    for (int i = 0; i < PICK; ++i) {
+        const uint64_t c = (uint64_t)(((uint32_t)tiles[i] * blocks + pairs - 1) / (uint32_t)pairs) * (256 + (TILE >> i));
+        if (i == 0 || c < cost) best = i, cost = c;
+    }
+    return best;
+}
+
+// All threads of the CTA (a multiple of 32): s_off[0 .. E] = the offsets, s_tile[0 .. E] = exclusive
+// prefix of each expert's tiles of at most TILE rows (none for an empty expert), or of the pick of PICK
+// widths from TILE down.  Returns false, after recording K3MOE_ERR_RANGE, when the offsets decrease or leave
+// [0, rows].  s_tmp: PICK ints a warp.  The caller keeps tiles x blocks below 2^30.
+template <int THREADS, int TILE, int PICK = 1>
+__device__ __forceinline__ bool group_tiles(const int32_t *__restrict__ offsets, int E, int rows, int *s_off, int *s_tile,
+                                            int *s_tmp, int *status, int blocks = 1, int pairs = 1)
+{
+    constexpr int WARPS = THREADS / 32;
     const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
     bool bad = false;
     for (int e = tid; e <= E; e += THREADS) {
@@ -22,31 +39,45 @@ __device__ __forceinline__ bool group_tiles(const int32_t *__restrict__ offsets,
     __syncthreads();
     // thread i counts the tiles of experts [i per, (i + 1) per)
     const int per = (E + THREADS - 1) / THREADS, e0 = min(E, tid * per), e1 = min(E, e0 + per);
-    int n = 0;
+    int n[PICK] = {};
     for (int e = e0; e < e1; ++e) {
         const int c = s_off[e + 1] - s_off[e];
         bad |= c < 0;
-        n += c > 0 ? (c - 1) / tile + 1 : 0;
-    }
-    int sum = n;
 #pragma unroll
-    for (int d = 1; d < 32; d <<= 1) {
-        const int v = __shfl_up_sync(0xffffffffu, sum, d);
-        if (lane >= d) sum += v;
+        for (int i = 0; i < PICK; ++i) n[i] += (int)((uint32_t)(max(c, 0) + (TILE >> i) - 1) / (TILE >> i));
     }
-    if (lane == 31) s_tmp[w] = sum;
+#pragma unroll
+    for (int i = 0; i < PICK; ++i) {
+        const int sum = __reduce_add_sync(0xffffffffu, n[i]);
+        if (lane == 0) s_tmp[w * PICK + i] = sum;
+    }
     if (__syncthreads_or(bad)) {
         if (tid == 0) set_status(status, K3MOE_ERR_RANGE, -1);
         return false;
     }
-    int before = sum - n;
-    for (int q = 0; q < w; ++q) before += s_tmp[q];
-    for (int e = e0; e < e1; ++e) {
-        s_tile[e] = before;
-        const int c = s_off[e + 1] - s_off[e];
-        before += c > 0 ? (c - 1) / tile + 1 : 0;
+    int warp_n[PICK], all[PICK];                             // of warp `lane`; of all
+#pragma unroll
+    for (int i = 0; i < PICK; ++i) {
+        warp_n[i] = lane < WARPS ? s_tmp[lane * PICK + i] : 0;
+        all[i] = PICK > 1 ? __reduce_add_sync(0xffffffffu, warp_n[i]) : 0;
     }
-    if (e1 == E && (e0 < E || tid == 0)) s_tile[E] = before;     // the last thread with experts (E > 0)
+    const int best = PICK > 1 ? pick_tile<TILE, PICK>(all, blocks, pairs) : 0, tile = TILE >> best;
+    int mine = n[0], others = warp_n[0];
+#pragma unroll
+    for (int i = 1; i < PICK; ++i)
+        if (i == best) mine = n[i], others = warp_n[i];
+    int at = mine;                                           // exclusive prefix over the warp, after the warps before it
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+        const int v = __shfl_up_sync(0xffffffffu, at, d);
+        if (lane >= d) at += v;
+    }
+    at += __reduce_add_sync(0xffffffffu, lane < w ? others : 0) - mine;
+    for (int e = e0; e < e1; ++e) {
+        s_tile[e] = at;
+        at += (s_off[e + 1] - s_off[e] + tile - 1) / tile;
+    }
+    if (e1 == E && (e0 < E || tid == 0)) s_tile[E] = at;     // the last thread with experts (E > 0)
     __syncthreads();
     return true;
 }

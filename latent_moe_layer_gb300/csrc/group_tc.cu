@@ -30,6 +30,8 @@
 namespace k3 {
 
 constexpr int GT_BK = 64, GT_TILE_M = 256, GT_TILE_N = 256;
+// mm, grad_x: row tiles of at most 256, 128, 64 or 32 rows, so that a few large experts still fill the GPU
+constexpr int GT_TILE_PICKS = 4;
 constexpr int GT_A_BYTES = 128 * GT_BK * 2, GT_STAGE = 2 * GT_A_BYTES;
 // grad_w: stages of one accumulation in TMEM (512 rows).  The tensor core truncates each sum it adds to
 // (1.2e-9 of the result a row: 3.8e-5 after 32,768 rows), so longer contractions are summed in registers
@@ -50,7 +52,7 @@ struct GroupSmem {
     static constexpr int N_BAR = 3 * NS + 5;                            // full, empty, tail; tfull, tempty x 2; drain
     static constexpr int OFF_INT = OFF_BAR + N_BAR * 8 + 8;
     // grad_w needs no tile table and reads the offsets from memory, which leaves room for its fifth stage
-    static constexpr int N_INT = MODE == K3_GROUP_GRAD_W ? 0 : 2 * (K3MOE_TRAIN_MAX_EXPERTS + 1) + 34;
+    static constexpr int N_INT = MODE == K3_GROUP_GRAD_W ? 0 : 2 * (K3MOE_TRAIN_MAX_EXPERTS + 1) + GT_TILE_PICKS * THREADS / 32;
     static constexpr int BYTES = OFF_INT + N_INT * 4 + 1024;
     static_assert(BYTES <= kMaxSmem, "shared memory");
 };
@@ -65,7 +67,8 @@ struct GroupTcArgs {
     const int32_t *offsets;
     int E, rows, M, Nc;      // M: the tile-row extent; Nc: grad_w's column extent (n_in)
     int K;                   // contraction of mm and grad_x
-    int l2_tiles;            // row tiles of GT_L2_ROWS bytes
+    int l2_rows;             // rows of GT_L2_ROWS bytes
+    int pairs;               // CTA pairs that fit the GPU
     int expert_coord;        // 0: one weight for all experts
     int wide_a, wide_b;      // MN-major operands whose width is a multiple of 64: both 64 x 64 boxes in one copy
     int bf16, accumulate;
@@ -129,11 +132,11 @@ struct GroupWalk {
             // row tiles (in groups that fit the L2) next to each other on the same block of weights
             int t = s_tile[e + 1] - s_tile[e], first = 0;
             const int all = t;
-            if (t > a.l2_tiles) {
-                const int g = w / (a.l2_tiles * mb);
-                first = g * a.l2_tiles;
+            if (rows > a.l2_rows) {
+                const int group = max(1, (int)((int64_t)a.l2_rows * t / rows)), g = w / (group * mb);
+                first = g * group;
                 w -= first * mb;
-                t = min(a.l2_tiles, t - first);
+                t = min(group, t - first);
             }
             j.m0 = (w / t) * GT_TILE_M;
             const int i = first + w % t;
@@ -203,10 +206,12 @@ __global__ void __launch_bounds__(GroupSmem<MODE>::THREADS, 1)
     griddep_enter();
     if (warp == 1) tmem_alloc_pair(smem_u32(tmem_holder), 512);
     tc_fence_before();                                   // the CTA-wide barriers below publish the address
-    const bool offsets_ok = W ? group_offsets_ok<SM::THREADS>(args.offsets, args.E, args.rows, args.status)
-                              : group_tiles<SM::THREADS>(args.offsets, args.E, args.rows, GT_TILE_N, s_int, s_tile,
-                                                         s_tile + K3MOE_TRAIN_MAX_EXPERTS + 1, args.status);
     const int mb = (args.M + GT_TILE_M - 1) / GT_TILE_M, cb = W ? (args.Nc + GT_TILE_N - 1) / GT_TILE_N : 1;
+    const bool offsets_ok =
+        W ? group_offsets_ok<SM::THREADS>(args.offsets, args.E, args.rows, args.status)
+          : group_tiles<SM::THREADS, GT_TILE_N, GT_TILE_PICKS>(args.offsets, args.E, args.rows, s_int, s_tile,
+                                                               s_tile + K3MOE_TRAIN_MAX_EXPERTS + 1, args.status, mb,
+                                                               args.pairs);
     // every CTA reads the same offsets, so all agree on a refusal
     const int jobs = !offsets_ok ? 0 : W ? args.E * mb * cb : s_tile[args.E] * mb;
 
@@ -590,6 +595,7 @@ int k3_group_tc(int mode, const K3Group &g, cudaStream_t st)
     a.out = g.out;
     a.ldo = g.ldo;
     a.stride_o = g.stride_o;
+    a.pairs = k3_num_sms() / 2;
     a.status = g.status;
     bool ok = true;
     if (mode == K3_GROUP_GRAD_W) {
@@ -615,7 +621,7 @@ int k3_group_tc(int mode, const K3Group &g, cudaStream_t st)
     a.K = mm ? g.n_in : g.n_out;
     // one weight for all experts: a single matrix at coordinate 0
     a.expert_coord = g.E > 1 && g.stride_b > 0;
-    a.l2_tiles = (int)std::max<int64_t>(1, GT_L2_ROWS / ((int64_t)GT_TILE_N * a.K * 2));
+    a.l2_rows = (int)std::max<int64_t>(GT_TILE_N, GT_L2_ROWS / ((int64_t)a.K * 2));
     const int64_t nw = a.expert_coord ? g.E : 1, sw = a.expert_coord ? g.stride_b : (int64_t)g.n_out * g.ldb;
     a.wide_a = !mm && g.n_in % 64 == 0;
     ok = a.wide_a ? encode_wide(&maps.a, g.dtype, g.b, g.n_in, g.n_out, nw, g.ldb, sw)
@@ -623,8 +629,9 @@ int k3_group_tc(int mode, const K3Group &g, cudaStream_t st)
     for (int i = 0; i < 5; ++i) ok = ok && encode_rows(&maps.b[i], g.dtype, g.a, a.K, g.rows, 0, g.lda, 0, 128 >> i);
     maps.out = maps.a;
     if (!ok) return K3MOE_ERR_CUDA;
-    // at most one partly filled tile an expert with rows
-    const int64_t jobs = ((int64_t)g.rows / GT_TILE_N + std::min(g.E, g.rows)) * ((a.M + GT_TILE_M - 1) / GT_TILE_M);
+    // at most one partly filled tile an expert with rows, in the narrowest tiles
+    const int64_t jobs = ((int64_t)g.rows / (GT_TILE_N >> (GT_TILE_PICKS - 1)) + std::min(g.E, g.rows)) *
+                         ((a.M + GT_TILE_M - 1) / GT_TILE_M);
     if (jobs >= (1LL << 30)) return K3MOE_ERR_SHAPE;
     return mm ? launch_typed<K3_GROUP_MM>(maps, a, g.out_dtype, jobs, st)
               : launch_typed<K3_GROUP_GRAD_X>(maps, a, g.out_dtype, jobs, st);
