@@ -46,8 +46,10 @@ struct GroupSmem {
     // grad_w's epilogue keeps 64 sums a thread and writes every value in fp32: four warps a TMEM quarter
     static constexpr int EPI_WARPS = MODE == K3_GROUP_GRAD_W ? 16 : 8;
     static constexpr int THREADS = 96 + 32 * EPI_WARPS;                 // TMA, MMA, tails, epilogue
-    static constexpr int OFF_OUT = NS * GT_STAGE;                       // grad_w: a 4 KB output box a warp
-    static constexpr int OUT_BYTES = MODE == K3_GROUP_GRAD_W ? EPI_WARPS * 4096 : 0;
+    static constexpr int OFF_OUT = NS * GT_STAGE;
+    // output staging of a warp: grad_w one 4 KB box, else two pieces of 16 rows x 32 16-bit values
+    static constexpr int OUT_WARP = MODE == K3_GROUP_GRAD_W ? 4096 : 2048;
+    static constexpr int OUT_BYTES = EPI_WARPS * OUT_WARP;
     static constexpr int OFF_BAR = OFF_OUT + OUT_BYTES;
     static constexpr int N_BAR = 3 * NS + 5;                            // full, empty, tail; tfull, tempty x 2; drain
     static constexpr int OFF_INT = OFF_BAR + N_BAR * 8 + 8;
@@ -72,6 +74,7 @@ struct GroupTcArgs {
     int expert_coord;        // 0: one weight for all experts
     int wide_a, wide_b;      // MN-major operands whose width is a multiple of 64: both 64 x 64 boxes in one copy
     int bf16, accumulate;
+    int out16;               // mm, grad_x: output rows on 16-byte boundaries
     void *out;
     int64_t ldo, stride_o;
     int *status;
@@ -362,7 +365,7 @@ __global__ void __launch_bounds__(GroupSmem<MODE>::THREADS, 1)
         const uint32_t tempty0 = cluster_addr(smem_u32(tempty), 0);
         RingPos<2> acc;
         O *out = static_cast<O *>(args.out);
-        uint8_t *box = smem + SM::OFF_OUT + (warp - 3) * 4096;
+        uint8_t *box = smem + SM::OFF_OUT + (warp - 3) * SM::OUT_WARP;
         bool ok = true;
         for (GroupWalk<MODE> walk(args, s_off, s_tile, mb, cb, jobs); walk.valid() && ok; walk.next()) {
             const GroupJob j = walk.get();
@@ -456,7 +459,30 @@ __global__ void __launch_bounds__(GroupSmem<MODE>::THREADS, 1)
                     uint32_t v[16];
                     tmem_ld16(tbase + acc.slot * GT_TILE_N + c, v);
                     tc_wait_ld();
-                    if (m < args.M) {
+                    if (sizeof(O) == 2 && args.out16) {
+                        // a lane holds one output column: turned in shared memory into 16-byte pieces of rows
+                        // (stored as they are, 64 bytes an instruction, a tile's outputs took 6 us)
+                        O *st = reinterpret_cast<O *>(box + (c / (16 * PARTS) & 1) * 1024);
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) st[i * 32 + lane] = from_f32<O>(__uint_as_float(v[i]));
+                        __syncwarp();
+#pragma unroll
+                        for (int i = 0; i < 16; i += 8) {
+                            const int r = i + (lane >> 2), m8 = m0 + (lane & 3) * 8;
+                            const uint4 w = *reinterpret_cast<const uint4 *>(st + r * 32 + (lane & 3) * 8);
+                            if (c + r < j.n) {
+                                O *o = out + (int64_t)(j.c0 + c + r) * args.ldo + m8;
+                                if (m8 + 8 <= args.M) {
+                                    *reinterpret_cast<uint4 *>(o) = w;
+                                } else {
+                                    const O *e = reinterpret_cast<const O *>(&w);
+#pragma unroll
+                                    for (int q8 = 0; q8 < 8; ++q8)
+                                        if (m8 + q8 < args.M) o[q8] = e[q8];
+                                }
+                            }
+                        }
+                    } else if (m < args.M) {
                         O *o = out + (int64_t)(j.c0 + c) * args.ldo + m;
 #pragma unroll
                         for (int i = 0; i < 16; ++i)
@@ -628,6 +654,7 @@ int k3_group_tc(int mode, const K3Group &g, cudaStream_t st)
                   : encode_rows(&maps.a, g.dtype, g.b, g.n_in, g.n_out, nw, g.ldb, sw, mm ? 128 : 64);
     for (int i = 0; i < 5; ++i) ok = ok && encode_rows(&maps.b[i], g.dtype, g.a, a.K, g.rows, 0, g.lda, 0, 128 >> i);
     maps.out = maps.a;
+    a.out16 = k3_rows16(g.out, g.ldo, g.out_dtype);
     if (!ok) return K3MOE_ERR_CUDA;
     // at most one partly filled tile an expert with rows, in the narrowest tiles
     const int64_t jobs = ((int64_t)g.rows / (GT_TILE_N >> (GT_TILE_PICKS - 1)) + std::min(g.E, g.rows)) *
