@@ -43,12 +43,13 @@ constexpr int64_t GT_L2_ROWS = 32 << 20;
 template <int MODE>
 struct GroupSmem {
     static constexpr int NS = MODE == K3_GROUP_GRAD_W ? 5 : 6;
-    // grad_w's epilogue keeps 64 sums a thread and writes every value in fp32: four warps a TMEM quarter
+    // grad_w's epilogue keeps 64 sums a thread and writes every value in fp32: four warps a TMEM quarter.  With as
+    // many, mm and grad_x gain nothing at any length and lose 0.3 to 0.8 us a small call.
     static constexpr int EPI_WARPS = MODE == K3_GROUP_GRAD_W ? 16 : 8;
     static constexpr int THREADS = 96 + 32 * EPI_WARPS;                 // TMA, MMA, tails, epilogue
     static constexpr int OFF_OUT = NS * GT_STAGE;
-    // output staging of a warp: grad_w one 4 KB box, else two pieces of 16 rows x 32 16-bit values
-    static constexpr int OUT_WARP = MODE == K3_GROUP_GRAD_W ? 4096 : 2048;
+    // output staging of a warp: grad_w one 4 KB box, else 16 rows x 32 16-bit values
+    static constexpr int OUT_WARP = MODE == K3_GROUP_GRAD_W ? 4096 : 1024;
     static constexpr int OUT_BYTES = EPI_WARPS * OUT_WARP;
     static constexpr int OFF_BAR = OFF_OUT + OUT_BYTES;
     static constexpr int N_BAR = 3 * NS + 5;                            // full, empty, tail; tfull, tempty x 2; drain
@@ -460,26 +461,36 @@ __global__ void __launch_bounds__(GroupSmem<MODE>::THREADS, 1)
                     tmem_ld16(tbase + acc.slot * GT_TILE_N + c, v);
                     tc_wait_ld();
                     if (sizeof(O) == 2 && args.out16) {
-                        // a lane holds one output column: turned in shared memory into 16-byte pieces of rows
-                        // (stored as they are, 64 bytes an instruction, a tile's outputs took 6 us)
-                        O *st = reinterpret_cast<O *>(box + (c / (16 * PARTS) & 1) * 1024);
+                        // a lane holds one output column of 16 rows: turned in shared memory, two rows to a word,
+                        // into 16-byte pieces of rows (stored as they are, 64 bytes an instruction, a tile's
+                        // outputs took 6 us)
+                        using T = std::conditional_t<sizeof(O) == 2, O, __half>;
+                        uint32_t *st = reinterpret_cast<uint32_t *>(box);
+                        __syncwarp();                                    // the previous pieces have been read
 #pragma unroll
-                        for (int i = 0; i < 16; ++i) st[i * 32 + lane] = from_f32<O>(__uint_as_float(v[i]));
+                        for (int i = 0; i < 8; ++i)
+                            st[i * 32 + lane] = pack2<T>(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1]));
                         __syncwarp();
+                        // lane: rows 2 p and 2 p + 1, columns m0 + 8 (lane % 4) .. + 7; odd pairs read their halves in the
+                        // other order, which keeps the banks apart
+                        const int p = lane >> 2, m8 = m0 + (lane & 3) * 8, odd = p & 1;
+                        const uint4 *src = reinterpret_cast<const uint4 *>(st + p * 32 + (lane & 3) * 8);
+                        const uint4 x = src[odd], y = src[1 - odd], a = odd ? y : x, b = odd ? x : y;
+                        const uint4 row[2] = {{__byte_perm(a.x, a.y, 0x5410), __byte_perm(a.z, a.w, 0x5410),
+                                               __byte_perm(b.x, b.y, 0x5410), __byte_perm(b.z, b.w, 0x5410)},
+                                              {__byte_perm(a.x, a.y, 0x7632), __byte_perm(a.z, a.w, 0x7632),
+                                               __byte_perm(b.x, b.y, 0x7632), __byte_perm(b.z, b.w, 0x7632)}};
 #pragma unroll
-                        for (int i = 0; i < 16; i += 8) {
-                            const int r = i + (lane >> 2), m8 = m0 + (lane & 3) * 8;
-                            const uint4 w = *reinterpret_cast<const uint4 *>(st + r * 32 + (lane & 3) * 8);
-                            if (c + r < j.n) {
-                                O *o = out + (int64_t)(j.c0 + c + r) * args.ldo + m8;
-                                if (m8 + 8 <= args.M) {
-                                    *reinterpret_cast<uint4 *>(o) = w;
-                                } else {
-                                    const O *e = reinterpret_cast<const O *>(&w);
+                        for (int i = 0; i < 2; ++i) {
+                            if (c + 2 * p + i >= j.n) continue;
+                            O *o = out + (int64_t)(j.c0 + c + 2 * p + i) * args.ldo + m8;
+                            if (m8 + 8 <= args.M) {
+                                *reinterpret_cast<uint4 *>(o) = row[i];
+                            } else {
+                                const O *e = reinterpret_cast<const O *>(row + i);
 #pragma unroll
-                                    for (int q8 = 0; q8 < 8; ++q8)
-                                        if (m8 + q8 < args.M) o[q8] = e[q8];
-                                }
+                                for (int q8 = 0; q8 < 8; ++q8)
+                                    if (m8 + q8 < args.M) o[q8] = e[q8];
                             }
                         }
                     } else if (m < args.M) {
