@@ -217,74 +217,81 @@ __device__ __forceinline__ F2 one_plus_exp_neg(F2 v)
     return fma2({a, b}, f2(1.0f), f2(1.0f));
 }
 
-// limit tanh(v / limit) = v num / den for |v| <= limit within 3e-7, relative also near 0, with x = (v / limit)^2:
-// Lambert's continued fraction t / (1 + t^2 / (3 + t^2 / (5 + t^2 / (7 + t^2 / 9)))) as one quotient (itself off
-// by 6e-8 at 1); 1 <= den <= 1.46.
-__device__ __forceinline__ void tanh_quotient(F2 x, F2 &num, F2 &den)
+// The unit's constants.  tanh(x) = x (1 + TANH_N x^2) / (1 + TANH_D1 x^2 + TANH_D2 x^4) for |x| <= 1 within 7e-8 of
+// itself: the quotient of these degrees with the smallest largest relative error there (fitted in fp64; 2.1e-7
+// evaluated in fp32).  limit tanh(v / limit) takes them with limit's powers folded in, from v^2 itself.
+constexpr double TANH_N = 0.09437645428558641, TANH_D1 = 0.4277082447645945, TANH_D2 = 0.009246752739316303;
+struct SoftLimit {
+    float limit, inv, small;              // 1 / limit; the quotient serves |v| <= small
+    float n, d1, d2, neg_inv2;            // its coefficients; -1 / limit^2
+};
+struct GluArgs {
+    SoftLimit g, u;
+};
+__device__ __forceinline__ void tanh_quotient(F2 v2, const SoftLimit &c, F2 &num, F2 &den)
 {
-    num = fma2(x, fma2(x, f2(1.0f / 945.0f), f2(105.0f / 945.0f)), f2(1.0f));
-    den = fma2(x, fma2(x, f2(15.0f / 945.0f), f2(420.0f / 945.0f)), f2(1.0f));
+    num = fma2(v2, f2(c.n), f2(1.0f));
+    den = fma2(v2, fma2(v2, f2(c.d2), f2(c.d1)), f2(1.0f));
 }
 // tanh of any x: beyond 1 (e^2x - 1) / (e^2x + 1), with tanh 10 = 1 in fp32
 __device__ __forceinline__ float tanh_any(float x)
 {
-    F2 num, den;
-    tanh_quotient(f2(x * x), num, den);
+    const float v = x * x, num = fmaf(v, (float)TANH_N, 1.0f), den = fmaf(v, fmaf(v, (float)TANH_D2, (float)TANH_D1), 1.0f);
     float e;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(2.8853900817779268f * fminf(fmaxf(x, -10.0f), 10.0f)));
     const float big = (e - 1.0f) * rcp_fast(e + 1.0f);
-    return fabsf(x) <= 1.0f ? x * num.x * rcp_fast(den.x) : x != x ? x : big;
+    return fabsf(x) <= 1.0f ? x * num * rcp_fast(den) : x != x ? x : big;
+}
+
+// sigmoid of any x as p q, a few 2^-22 of it: both stay normal numbers where the sigmoid itself is a subnormal
+__device__ __forceinline__ void sigmoid_any(float x, float &p, float &q)
+{
+    p = expf(fminf(0.5f * x, 0.0f));
+    q = p * rcp_fast(1.0f + expf(-fabsf(x)));
 }
 
 // The unit a = s f(g) h(u), s = sigmoid(g), of two elements: SiLU f = g, h = u; SiTU f = beta tanh(g / beta),
-// h = linear_beta tanh(u / linear_beta).  GRAD: (da/dg, da/du) instead of a.  SMALL: all tanh arguments are
-// within [-1, 1] and |g| <= 60, so that the sigmoid and both tanh share one reciprocal of a finite product.
+// h = linear_beta tanh(u / linear_beta).  o0 = a t; GRAD: (o0, o1) = (da/dg, da/du) t.  SMALL: all tanh arguments
+// are within [-1, 1] and |g| <= 60, so that the sigmoid and both tanh share one reciprocal of a finite product.
 template <int ACT, bool GRAD, bool SMALL>
-__device__ __forceinline__ void glu_two(F2 g, F2 u, const K3Act &c, F2 &o0, F2 &o1)
+__device__ __forceinline__ void glu_two(F2 g, F2 u, F2 t, const GluArgs &c, F2 &o0, F2 &o1)
 {
-    const F2 ds = one_plus_exp_neg(g), one = f2(1.0f);
+    const F2 one = f2(1.0f), neg = f2(-1.0f);
     if (ACT == K3MOE_ACT_SILU) {
-        const F2 s = rcp2(ds), f = mul2(g, s);
-        o0 = GRAD ? mul2(u, fma2(f, fma2(s, f2(-1.0f), one), s)) : mul2(f, u);
-        o1 = f;
+        const F2 s = rcp2(one_plus_exp_neg(g)), f = mul2(g, s);
+        o0 = GRAD ? mul2(mul2(u, fma2(f, fma2(s, neg, one), s)), t) : mul2(mul2(f, u), t);
+        o1 = mul2(f, t);
         return;
     }
-    F2 s, f, h, tg2, tu2;                                // tg2, tu2: the tanh squared
     if (SMALL) {
-        const F2 xg = mul2(mul2(g, g), f2(c.inv_beta * c.inv_beta));
-        const F2 xu = mul2(mul2(u, u), f2(c.inv_linear_beta * c.inv_linear_beta));
         F2 ng, dg, nu, du;
-        tanh_quotient(xg, ng, dg);
-        tanh_quotient(xu, nu, du);
+        tanh_quotient(mul2(g, g), c.g, ng, dg);
+        tanh_quotient(mul2(u, u), c.u, nu, du);
         ng = mul2(ng, g);
         nu = mul2(nu, u);
-        const F2 dgu = mul2(dg, du), r = rcp2(mul2(ds, dgu));
-        if (!GRAD) {
-            o0 = mul2(mul2(ng, nu), r);
-            return;
+        const F2 ds = one_plus_exp_neg(g), dgu = mul2(dg, du), r = rcp2(mul2(ds, dgu));
+        if (GRAD) {
+            // da/dg = h s (f (1 - s) + 1 - (f / beta)^2), da/du = s f (1 - (h / linear_beta)^2)
+            const F2 rs = mul2(r, ds), s = mul2(r, dgu), f = mul2(ng, mul2(rs, du)), h = mul2(nu, mul2(rs, dg)), st = mul2(s, t);
+            o0 = mul2(mul2(h, st), fma2(f, fma2(f, f2(c.g.neg_inv2), fma2(s, neg, one)), one));
+            o1 = mul2(mul2(f, st), fma2(mul2(h, f2(c.u.neg_inv2)), h, one));
+        } else {
+            o0 = mul2(mul2(ng, nu), mul2(r, t));
         }
-        const F2 rs = mul2(r, ds);
-        s = mul2(r, dgu);
-        f = mul2(ng, mul2(rs, du));
-        h = mul2(nu, mul2(rs, dg));
-        tg2 = mul2(mul2(f, f), f2(c.inv_beta * c.inv_beta));
-        tu2 = mul2(mul2(h, h), f2(c.inv_linear_beta * c.inv_linear_beta));
     } else {
-        const F2 tg = {tanh_any(g.x * c.inv_beta), tanh_any(g.y * c.inv_beta)};
-        const F2 tu = {tanh_any(u.x * c.inv_linear_beta), tanh_any(u.y * c.inv_linear_beta)};
-        s = rcp2(ds);
-        f = mul2(tg, f2(c.beta));
-        h = mul2(tu, f2(c.linear_beta));
-        tg2 = mul2(tg, tg);
-        tu2 = mul2(tu, tu);
-    }
-    const F2 sf = mul2(s, f), neg = f2(-1.0f);
-    if (GRAD) {
-        // da/dg = h s (f (1 - s) + 1 - tg^2), da/du = s f (1 - tu^2)
-        o0 = mul2(mul2(h, s), fma2(tg2, neg, fma2(sf, neg, fma2(f, one, one))));
-        o1 = mul2(sf, fma2(tu2, neg, one));
-    } else {
-        o0 = mul2(sf, h);
+        F2 p, q;                                         // s = p q
+        sigmoid_any(g.x, p.x, q.x);
+        sigmoid_any(g.y, p.y, q.y);
+        const F2 tg = {tanh_any(g.x * c.g.inv), tanh_any(g.y * c.g.inv)};
+        const F2 tu = {tanh_any(u.x * c.u.inv), tanh_any(u.y * c.u.inv)};
+        const F2 f = mul2(tg, f2(c.g.limit)), h = mul2(tu, f2(c.u.limit));
+        if (GRAD) {
+            o0 = mul2(mul2(mul2(h, p), mul2(q, t)),
+                      fma2(f, fma2(mul2(p, q), neg, one), fma2(mul2(tg, tg), neg, one)));
+            o1 = mul2(mul2(mul2(f, p), mul2(q, t)), fma2(mul2(tu, tu), neg, one));
+        } else {
+            o0 = mul2(mul2(mul2(f, p), mul2(h, q)), t);
+        }
     }
 }
 
@@ -303,61 +310,75 @@ __device__ __forceinline__ bool all_within(const Vec<T, V> &v, float limit)
     }
 }
 
-// V outputs from loaded inputs g, u (and the output's gradient).
+// V outputs from loaded inputs g, u (and the output's gradient).  Where all values are finite (SMALL) a dropped
+// element's factor is cleared; elsewhere its results are, since 0 x NaN is not 0.
 template <class T, int V, int ACT, bool DROP, bool GRAD, bool SMALL>
-__device__ __forceinline__ void glu_piece(const Vec<T, V> (&in)[2 + GRAD], const uint32_t (&w)[V], const K3Act &act,
+__device__ __forceinline__ void glu_piece(const Vec<T, V> (&in)[2 + GRAD], const uint32_t (&w)[V], const GluArgs &act,
                                           const DropArgs &a, Vec<T, V> &o0, Vec<T, V> &o1)
 {
-    const F2 scale = f2(a.scale);
+    constexpr bool FACTOR = DROP && SMALL && ACT == K3MOE_ACT_SITU, RESULT = DROP && !FACTOR;
 #pragma unroll
     for (int j = 0; j < V; j += 2) {
         const int k = V == 1 ? 0 : j + 1;
         const float2 g = in[0].get2(j), u = in[1].get2(j);
-        F2 v0, v1, t = scale;
-        glu_two<ACT, GRAD, SMALL>({g.x, g.y}, {u.x, u.y}, act, v0, v1);
+        F2 v0, v1, t = f2(a.scale);
         if (GRAD) {
             const float2 d = in[1 + GRAD].get2(j);
-            t = mul2({d.x, d.y}, scale);
+            t = mul2({d.x, d.y}, t);
         }
-        if (DROP || GRAD) v0 = mul2(v0, t);
-        if (GRAD) v1 = mul2(v1, t);
-        o0.set2(j, kept<DROP>(v0.x, w[j], a), kept<DROP>(v0.y, w[k], a));
-        if (GRAD) o1.set2(j, kept<DROP>(v1.x, w[j], a), kept<DROP>(v1.y, w[k], a));
+        t = {kept<FACTOR>(t.x, w[j], a), kept<FACTOR>(t.y, w[k], a)};
+        glu_two<ACT, GRAD, SMALL>({g.x, g.y}, {u.x, u.y}, t, act, v0, v1);
+        o0.set2(j, kept<RESULT>(v0.x, w[j], a), kept<RESULT>(v0.y, w[k], a));
+        if (GRAD) o1.set2(j, kept<RESULT>(v1.x, w[j], a), kept<RESULT>(v1.y, w[k], a));
     }
 }
 
-// Pieces of V elements over the [rows, width] matrix; piece i is row i / nv, column (i % nv) V.  Of 217 (SiLU)
-// to 415 (SiTU's gradient) warp instructions per 8 elements about 100 are the generator's; the arithmetic pipes
-// bind next to HBM.  32,768 x 3072 bf16, p = 0.1: SiLU 110 us (5.5 TB/s; without dropout 94 us, 6.4 TB/s), SiTU
-// 155 us, the gradients 160 and 217 us.  CTAs an SM (4, gradients 3) by measurement: more cost registers that
-// spill, fewer leave latency open.
+// From a thread's piece to its next: `col` pieces further in the row, and a row more where that is past the row's
+// end (nv pieces).  The addresses move by bytes[0], or by bytes[1] with that row more.
+struct GluWalk {
+    int64_t gu[2], da[2], out[2];
+    int col, nv;
+    __device__ __forceinline__ bool next(int &c) const
+    {
+        c += col;
+        const bool over = c >= nv;
+        if (over) c -= nv;
+        return over;
+    }
+};
+template <class P>
+__device__ __forceinline__ void move_on(P *&p, const int64_t (&bytes)[2], bool over)
+{
+    p = reinterpret_cast<P *>(reinterpret_cast<uintptr_t>(p) + (over ? bytes[1] : bytes[0]));
+}
+
+// Pieces of V elements over the [rows, width] matrix; piece i is row i / nv, column (i % nv) V.  About 100 of the
+// warp instructions per 8 elements are the generator's; the arithmetic pipes bind next to HBM.  32,768 x 3072 bf16,
+// p = 0.1: SiLU 111 us (5.4 TB/s; without dropout 99 us, 6.1 TB/s), SiTU 152 us, the gradients 158 and 197 us.  CTAs
+// an SM (4, gradients 3 in registers) by measurement: more cost registers that spill, fewer leave latency open.
 template <class T, int V, int ACT, bool DROP, bool GRAD>
 __global__ void __launch_bounds__(PIPE_THREADS, GRAD ? 3 : 4) glu_kernel(const T *da, int64_t ldda, const T *gu, int64_t ldgu,
-                                                                         int rows, int width, const K3Act act,
-                                                                         const DropArgs a, T *out, int64_t ldo)
+                                                                         int rows, int width, const GluArgs act,
+                                                                         const DropArgs a, const GluWalk walk, T *out,
+                                                                         int64_t ldo)
 {
     griddep_enter();
-    const int nv = width / V;
+    const int nv = walk.nv;
     const int64_t total = (int64_t)rows * nv, step = (int64_t)gridDim.x * PIPE_THREADS;
-    const int64_t i0 = (int64_t)blockIdx.x * PIPE_THREADS + threadIdx.x, row_step = step / nv;
-    const int col_step = (int)(step - row_step * nv);
-    int64_t row = i0 / nv, out_row = row;                // of the piece being fetched; of the one being computed
-    int col = (int)(i0 - row * nv), out_col = col;
-    auto advance = [&](int64_t &r, int &c) {
-        r += row_step;
-        c += col_step;
-        if (c >= nv) {
-            c -= nv;
-            ++r;
-        }
-    };
+    const int64_t i0 = (int64_t)blockIdx.x * PIPE_THREADS + threadIdx.x;
+    const int64_t row = i0 / nv;
+    int col = (int)(i0 - row * nv), out_col = col;       // of the piece being fetched; of the one being computed
+    const T *gu_at = gu + row * ldgu + (int64_t)col * V, *da_at = GRAD ? da + row * ldda + (int64_t)col * V : nullptr;
+    T *out_at = out + row * ldo + (int64_t)col * V;
     for_pieces<T, V, 2 + GRAD, DROP && V == 8>(
         i0, step, total,
         [&](const T *(&p)[2 + GRAD]) {
-            p[0] = gu + row * ldgu + (int64_t)col * V;
-            p[1] = p[0] + width;
-            if (GRAD) p[1 + GRAD] = da + row * ldda + (int64_t)col * V;
-            advance(row, col);
+            p[0] = gu_at;
+            p[1] = gu_at + width;
+            if (GRAD) p[1 + GRAD] = da_at;
+            const bool over = walk.next(col);
+            move_on(gu_at, walk.gu, over);
+            if (GRAD) move_on(da_at, walk.da, over);
         },
         [&](int64_t i, const Vec<T, V>(&in)[2 + GRAD]) {
             uint32_t w[V] = {};
@@ -365,13 +386,12 @@ __global__ void __launch_bounds__(PIPE_THREADS, GRAD ? 3 : 4) glu_kernel(const T
             Vec<T, V> o0, o1;
             // one branch a piece: tanh arguments beyond 1 (or NaN) are rare
             const bool small = ACT == K3MOE_ACT_SILU ||
-                               (all_within<T, V>(in[0], fminf(act.beta, 60.0f)) && all_within<T, V>(in[1], act.linear_beta));
+                               (all_within<T, V>(in[0], act.g.small) && all_within<T, V>(in[1], act.u.small));
             if (small) glu_piece<T, V, ACT, DROP, GRAD, true>(in, w, act, a, o0, o1);
             else glu_piece<T, V, ACT, DROP, GRAD, false>(in, w, act, a, o0, o1);
-            T *dst = out + out_row * ldo + (int64_t)out_col * V;
-            *reinterpret_cast<Vec<T, V> *>(dst) = o0;
-            if (GRAD) *reinterpret_cast<Vec<T, V> *>(dst + width) = o1;
-            advance(out_row, out_col);
+            *reinterpret_cast<Vec<T, V> *>(out_at) = o0;
+            if (GRAD) *reinterpret_cast<Vec<T, V> *>(out_at + width) = o1;
+            move_on(out_at, walk.out, walk.next(out_col));
         });
 }
 
@@ -403,16 +423,18 @@ static void with_bool(bool b, F f)
     else f(std::false_type());
 }
 
-// CTAs for `pieces`: as many as are resident at once (the loops stride the rest), since a
-// second, partly filled round of CTAs costs as much as a full one.  `fit` is the kernel's own memory.
+// CTAs for `pieces`: as many as are resident at once (the loops stride the rest, since a second, partly filled round
+// of CTAs costs as much as a full one), and no more than `few` an SM where each thread then has 64 pieces or more.
+// `fit` is the kernel's own memory.
 template <class F>
-static unsigned resident_grid(F kern, int64_t pieces, int sms, int &fit)
+static unsigned resident_grid(F kern, int64_t pieces, int sms, int &fit, int few = 32)
 {
     int n = fit;
     if (!n) {
         if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kern, PIPE_THREADS, 0) != cudaSuccess || n < 1) n = 1;
         fit = n;
     }
+    if (pieces >= (int64_t)64 * PIPE_THREADS * few * sms) n = std::min(n, few);
     return (unsigned)std::min<int64_t>((pieces + PIPE_THREADS - 1) / PIPE_THREADS, (int64_t)n * sms);
 }
 
@@ -458,18 +480,42 @@ extern "C" int k3moe_dropout(const void *x, const void *residual, int64_t n, int
 
 template <class T, int V, bool GRAD>
 static void launch_glu(const void *da, int64_t ldda, const void *gu, int64_t ldgu, int rows, int width,
-                       const K3Act &act, const DropArgs &a, void *out, int64_t ldo, int sms, cudaStream_t st)
+                       bool is_situ, const GluArgs &act, const DropArgs &a, void *out, int64_t ldo, int sms,
+                       cudaStream_t st)
 {
     with_bool(a.threshold != 0, [&](auto drop) {
-        with_bool(act.kind == K3MOE_ACT_SITU, [&](auto situ) {
+        with_bool(is_situ, [&](auto situ) {
             constexpr int ACT = decltype(situ)::value ? K3MOE_ACT_SITU : K3MOE_ACT_SILU;
             auto kern = glu_kernel<T, V, ACT, decltype(drop)::value, GRAD>;
             static int fit = 0;
-            k3_launch(kern, resident_grid(kern, (int64_t)rows * (width / V), sms, fit), PIPE_THREADS, 0, st, (const T *)da,
-                      ldda,
-                      (const T *)gu, ldgu, rows, width, act, a, (T *)out, ldo);
+            GluWalk walk;
+            walk.nv = width / V;
+            // SiLU's gradient with the generator is bound by HBM, which serves long runs of its five streams better from
+            // fewer CTAs: 158 us with 2 an SM, 168 with 3, 173 with 4 (32,768 x 3072), but 33 against 31 us at 5,003 rows
+            constexpr int FEW = GRAD && V == 8 && decltype(drop)::value && ACT == K3MOE_ACT_SILU ? 2 : 32;
+            const unsigned grid = resident_grid(kern, (int64_t)rows * walk.nv, sms, fit, FEW);
+            const int64_t step = (int64_t)grid * PIPE_THREADS, row_step = step / walk.nv;
+            walk.col = (int)(step - row_step * walk.nv);
+            auto moves = [&](int64_t ld, int64_t (&bytes)[2]) {
+                bytes[0] = (row_step * ld + (int64_t)walk.col * V) * (int64_t)sizeof(T);
+                bytes[1] = bytes[0] + (ld - (int64_t)walk.nv * V) * (int64_t)sizeof(T);
+            };
+            moves(ldgu, walk.gu);
+            moves(ldda, walk.da);
+            moves(ldo, walk.out);
+            k3_launch(kern, grid, PIPE_THREADS, 0, st, (const T *)da, ldda, (const T *)gu, ldgu, rows, width, act, a, walk,
+                      (T *)out, ldo);
         });
     });
+}
+
+static SoftLimit soft_limit(float limit, float largest)
+{
+    const double inv = 1.0 / (double)limit, inv2 = inv * inv;
+    // beyond these limits the folded coefficients would leave fp32's range: all values by the general form
+    const bool folds = limit >= 0x1p-20f && limit <= 0x1p20f;
+    return {limit, (float)inv, folds ? std::min(limit, largest) : -1.0f, (float)(TANH_N * inv2), (float)(TANH_D1 * inv2),
+            (float)(TANH_D2 * inv2 * inv2), (float)-inv2};
 }
 
 template <bool GRAD>
@@ -492,20 +538,16 @@ static int glu_run(const void *da, int64_t ldda, const void *gu, int64_t ldgu, i
     if (rows == 0) return K3MOE_OK;
     const int sms = k3_num_sms();
     if (!sms) return K3MOE_ERR_CUDA;
-    K3Act c;
-    c.kind = act;
-    c.beta = beta > 0.f ? beta : 4.0f;
-    c.linear_beta = linear_beta > 0.f ? linear_beta : 25.0f;
-    c.inv_beta = 1.0f / c.beta;
-    c.inv_linear_beta = 1.0f / c.linear_beta;
+    const bool situ = act == K3MOE_ACT_SITU;
+    const GluArgs c = {soft_limit(beta > 0.f ? beta : 4.0f, 60.0f), soft_limit(linear_beta > 0.f ? linear_beta : 25.0f, 0x1p20f)};
     const bool vec = width % 8 == 0 && k3_rows16(gu, ldgu, dtype) && k3_rows16(out, ldo, dtype) &&
                      (!GRAD || k3_rows16(da, ldda, dtype));
     if (dtype == K3MOE_TYPE_BF16)
-        vec ? launch_glu<__nv_bfloat16, 8, GRAD>(da, ldda, gu, ldgu, rows, width, c, a, out, ldo, sms, st)
-            : launch_glu<__nv_bfloat16, 1, GRAD>(da, ldda, gu, ldgu, rows, width, c, a, out, ldo, sms, st);
+        vec ? launch_glu<__nv_bfloat16, 8, GRAD>(da, ldda, gu, ldgu, rows, width, situ, c, a, out, ldo, sms, st)
+            : launch_glu<__nv_bfloat16, 1, GRAD>(da, ldda, gu, ldgu, rows, width, situ, c, a, out, ldo, sms, st);
     else
-        vec ? launch_glu<__half, 8, GRAD>(da, ldda, gu, ldgu, rows, width, c, a, out, ldo, sms, st)
-            : launch_glu<__half, 1, GRAD>(da, ldda, gu, ldgu, rows, width, c, a, out, ldo, sms, st);
+        vec ? launch_glu<__half, 8, GRAD>(da, ldda, gu, ldgu, rows, width, situ, c, a, out, ldo, sms, st)
+            : launch_glu<__half, 1, GRAD>(da, ldda, gu, ldgu, rows, width, situ, c, a, out, ldo, sms, st);
     k3_note_launch();
     return cudaGetLastError() == cudaSuccess ? K3MOE_OK : K3MOE_ERR_CUDA;
 }

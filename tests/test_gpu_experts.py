@@ -436,6 +436,27 @@ def test_glu_betas_strides_and_extremes():
     assert torch.isnan(a[0][keep]).all() and (a[0][~keep] == 0).all()
 
 
+@pytest.mark.parametrize("beta,linear_beta", [(1e-9, 1e20), (1e20, 1e-9), (1e6, 1e6), (2e6, 0.5), (70.0, 25.0)])
+def test_glu_limits_far_from_the_usual(beta, linear_beta):
+    # values below, around and above each limit; no term cancels in the unit itself, so its error is relative:
+    # a few 2^-22 for each of the three factors.  The gradients' 1 - tanh^2 has that error beside 1.
+    gen = _gen(11)
+    rows, width = 24, 64
+    around = [torch.tensor([1e-3, 0.3, 1.0, 3.0], device="cuda").repeat(width // 4) * min(b, top) for b, top in ((beta, 30.0), (linear_beta, 1e20))]
+    gu = (torch.randn(rows, 2 * width, generator=gen, device="cuda") * torch.cat(around)).to(BF)
+    gu[:, :4] = torch.randn(rows, 4, generator=gen, device="cuda").to(BF)
+    da = _rand(gen, rows, width)
+    n, d = _np(gu), _np(da)
+    want = ox.glu_dropout(n, 0.25, SEED, OFFSET, "situ", beta, linear_beta)
+    kw = dict(p=0.25, seed=SEED, offset=OFFSET, act="situ", situ_beta=beta, situ_linear_beta=linear_beta)
+    _close(ex.glu_dropout(gu, **kw), want, 2.0 ** -20 * np.abs(want))
+    g, u = np.split(n, 2, 1)
+    s, f, h = 1 / (1 + np.exp(-g)), np.abs(beta * np.tanh(g / beta)), np.abs(linear_beta * np.tanh(u / linear_beta))
+    slack = 2.0 ** -20 * np.abs(d) / 0.75 * s
+    _close(ex.glu_dropout_grad(da, gu, **kw), ox.glu_dropout_grad(d, n, 0.25, SEED, OFFSET, "situ", beta, linear_beta),
+           np.concatenate([slack * h * (1 + f), slack * f], 1))
+
+
 @pytest.mark.parametrize("dt", [BF, F16, F32], ids=["bf16", "f16", "f32"])
 @pytest.mark.parametrize("n,p", [(1, 0.5), (3, 0.1), (4, 0.0), (1000, 0.3), (4099, 0.5), (300_001, 0.1)])
 def test_dropout(n, p, dt):
