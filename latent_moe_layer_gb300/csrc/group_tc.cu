@@ -71,7 +71,7 @@ struct GroupTcArgs {
     int E, rows, M, Nc;      // M: the tile-row extent; Nc: grad_w's column extent (n_in)
     int K;                   // contraction of mm and grad_x
     int l2_rows;             // rows of GT_L2_ROWS bytes
-    int pairs;               // CTA pairs that fit the GPU
+    int pairs;               // clusters of the launch
     int expert_coord;        // 0: one weight for all experts
     int wide_a, wide_b;      // MN-major operands whose width is a multiple of 64: both 64 x 64 boxes in one copy
     int bf16, accumulate;
@@ -170,7 +170,10 @@ __device__ __forceinline__ void load_rows(const CUtensorMap *maps, uint32_t dst,
 }
 
 // CUT: grad_w's rows end inside 16 bytes (a variant of its own for the registers it costs).
-template <int MODE, class O, bool CUT>
+// SPLIT (mm, grad_x): the pairs of a cluster of 2 SPLIT CTAs share one tile's contraction, for calls of few tiles.  The
+// caller gives every tile a cluster of its own: each pair leaves its part of the sum in its shared memory (the ring
+// is done with), and the pairs add up the parts of a share of the tile each, in a fixed order, and store it.
+template <int MODE, class O, bool CUT, int SPLIT>
 __global__ void __launch_bounds__(GroupSmem<MODE>::THREADS, 1)
     group_tc_kernel(const __grid_constant__ GroupMaps maps, const GroupTcArgs args)
 {
@@ -186,7 +189,9 @@ __global__ void __launch_bounds__(GroupSmem<MODE>::THREADS, 1)
     int *s_int = (int *)(smem + SM::OFF_INT), *s_tile = s_int + K3MOE_TRAIN_MAX_EXPERTS + 1;
     const int *s_off = W ? args.offsets : s_int;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const uint32_t rank = cluster_ctarank();
+    // this CTA's place in its pair, the pair's place in the cluster, the cluster rank of the pair's even CTA
+    const uint32_t rank = cluster_ctarank() & 1, pair = SPLIT > 1 ? cluster_ctarank() >> 1 : 0, lead = 2 * pair;
+    static_assert(SPLIT == 1 || !W, "grad_w does not split");
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < NS; ++i) {
@@ -222,11 +227,55 @@ __global__ void __launch_bounds__(GroupSmem<MODE>::THREADS, 1)
     tc_fence_after();
     const uint32_t tmem = *tmem_holder;
 
+    // mm, grad_x: a warp's 32 output columns (one a lane) of 16 rows, from fp32
+    auto store16 = [&](const GroupJob &j, int m0, int c, const uint32_t (&v)[16], uint8_t *box) {
+        const int m = m0 + lane;
+        if (sizeof(O) == 2 && args.out16) {
+            // a lane holds one output column of 16 rows: turned in shared memory, two rows to a word,
+            // into 16-byte pieces of rows (stored as they are, 64 bytes an instruction, a tile's
+            // outputs took 6 us)
+            using T = std::conditional_t<sizeof(O) == 2, O, __half>;
+            uint32_t *st = reinterpret_cast<uint32_t *>(box);
+            __syncwarp();                                    // the previous pieces have been read
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                st[i * 32 + lane] = pack2<T>(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1]));
+            __syncwarp();
+            // lane: rows 2 p and 2 p + 1, columns m0 + 8 (lane % 4) .. + 7; odd pairs read their halves in the
+            // other order, which keeps the banks apart
+            const int p = lane >> 2, m8 = m0 + (lane & 3) * 8, odd = p & 1;
+            const uint4 *src = reinterpret_cast<const uint4 *>(st + p * 32 + (lane & 3) * 8);
+            const uint4 x = src[odd], y = src[1 - odd], a = odd ? y : x, b = odd ? x : y;
+            const uint4 row[2] = {{__byte_perm(a.x, a.y, 0x5410), __byte_perm(a.z, a.w, 0x5410),
+                                   __byte_perm(b.x, b.y, 0x5410), __byte_perm(b.z, b.w, 0x5410)},
+                                  {__byte_perm(a.x, a.y, 0x7632), __byte_perm(a.z, a.w, 0x7632),
+                                   __byte_perm(b.x, b.y, 0x7632), __byte_perm(b.z, b.w, 0x7632)}};
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                if (c + 2 * p + i >= j.n) continue;
+                O *o = static_cast<O *>(args.out) + (int64_t)(j.c0 + c + 2 * p + i) * args.ldo + m8;
+                if (m8 + 8 <= args.M) {
+                    *reinterpret_cast<uint4 *>(o) = row[i];
+                } else {
+                    const O *e = reinterpret_cast<const O *>(row + i);
+#pragma unroll
+                    for (int q8 = 0; q8 < 8; ++q8)
+                        if (m8 + q8 < args.M) o[q8] = e[q8];
+                }
+            }
+        } else if (m < args.M) {
+            O *o = static_cast<O *>(args.out) + (int64_t)(j.c0 + c) * args.ldo + m;
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+                if (c + i < j.n) o[i * args.ldo] = from_f32<O>(__uint_as_float(v[i]));
+        }
+    };
+
     // The producer and issuer warps run their loops as whole warps, one elected lane doing the work.
     if (warp == 0) {
         // ------------------------------------------------------------ TMA producer (each CTA its half)
         const bool one = elect_one();
-        const uint32_t full0 = cluster_addr(smem_u32(full), 0);
+        const uint32_t full0 = cluster_addr(smem_u32(full), lead);
         RingPos<NS> p, t;                                // stages; tails
         uint32_t issued = 0;
         bool ok = true;
@@ -236,7 +285,8 @@ __global__ void __launch_bounds__(GroupSmem<MODE>::THREADS, 1)
             const int m = j.m0 + 128 * (int)rank, e = args.expert_coord * walk.e;
             const int c = j.c0 + half * (int)rank, r0 = walk.off0;
             const uint32_t bytes = GT_A_BYTES + half * 128;
-            for (int s = 0; s < j.steps; ++s, ++issued, p.next()) {
+            const int s1 = j.steps * ((int)pair + 1) / SPLIT;            // this pair's stages
+            for (int s = j.steps * (int)pair / SPLIT; s < s1; ++s, ++issued, p.next()) {
                 if (!pair_wait(smem_u32(empty + p.slot), p.phase ^ 1, abort_flag, args.status, 61)) {
                     ok = false;
                     break;
@@ -308,9 +358,10 @@ __global__ void __launch_bounds__(GroupSmem<MODE>::THREADS, 1)
         for (GroupWalk<MODE> walk(args, s_off, s_tile, mb, cb, jobs); walk.valid() && ok; walk.next()) {
             const GroupJob j = walk.get();
             const uint32_t idesc = idesc_f16(GT_TILE_M, (j.n + 15) & ~15, args.bf16) | major;
-            for (int s = 0; s < j.steps; ++s, p.next()) {
-                const bool begin = s == 0 || (W && s % GT_CHUNK == 0), last = s == j.steps - 1;
-                const bool end = last || (W && (s + 1) % GT_CHUNK == 0);
+            const int s0 = j.steps * (int)pair / SPLIT, s1 = j.steps * ((int)pair + 1) / SPLIT;
+            for (int s = s0; s < s1; ++s, p.next()) {
+                const bool begin = s == s0 || (W && s % GT_CHUNK == 0), last = s == j.steps - 1;
+                const bool end = s == s1 - 1 || (W && (s + 1) % GT_CHUNK == 0);
                 if (begin) {
                     ok = pair_wait(smem_u32(tempty + acc.slot), acc.phase ^ 1, abort_flag, args.status, 63);
                     tc_fence_after();
@@ -328,15 +379,15 @@ __global__ void __launch_bounds__(GroupSmem<MODE>::THREADS, 1)
                     for (int kk = 0; kk < GT_BK / 16; ++kk)
                         if (kk < kk_n)
                             tc_mma_f16_pair(d, ad + a_step * kk, bd + b_step * kk, idesc, (!begin || kk > 0) ? 1u : 0u);
-                    tc_commit_pair(smem_u32(empty + p.slot));
-                    if (end) tc_commit_pair(smem_u32(tfull + acc.slot));
+                    tc_commit_pair(smem_u32(empty + p.slot), lead);
+                    if (end) tc_commit_pair(smem_u32(tfull + acc.slot), lead);
                 }
                 __syncwarp();
                 if (end) acc.next();
             }
         }
         // every issued MMA completes before TMEM is released
-        if (one) tc_commit_pair(smem_u32(drain));
+        if (one) tc_commit_pair(smem_u32(drain), lead);
         __syncwarp();
         mbar_wait(smem_u32(drain), 0, 0xFFFFFFFFu);
     } else if (W && warp == 2) {
@@ -356,14 +407,14 @@ __global__ void __launch_bounds__(GroupSmem<MODE>::THREADS, 1)
             for (int r = j.last; r & 15; ++r) *reinterpret_cast<uint4 *>(st + r * 128) = make_uint4(0, 0, 0, 0);
             fence_proxy_async_smem();
             __syncwarp();
-            if (lane == 0) mbar_arrive_cluster(cluster_addr(smem_u32(full + slot), 0));
+            if (lane == 0) mbar_arrive_cluster(cluster_addr(smem_u32(full + slot), lead));
         }
     } else if (warp >= 3) {
         // ------------------------------------------------------------ epilogue (each CTA its 128 rows)
         constexpr int PARTS = SM::EPI_WARPS / 4, COLS = GT_TILE_N / PARTS;
         const int q = warp & 3, part = (warp - 3) >> 2;                  // TMEM lanes 32q .. 32q + 31
         const uint32_t tbase = tmem + ((uint32_t)(32 * q) << 16);
-        const uint32_t tempty0 = cluster_addr(smem_u32(tempty), 0);
+        const uint32_t tempty0 = cluster_addr(smem_u32(tempty), lead);
         RingPos<2> acc;
         O *out = static_cast<O *>(args.out);
         uint8_t *box = smem + SM::OFF_OUT + (warp - 3) * SM::OUT_WARP;
@@ -455,49 +506,16 @@ __global__ void __launch_bounds__(GroupSmem<MODE>::THREADS, 1)
                 ok = pair_wait(smem_u32(tfull + acc.slot), acc.phase, abort_flag, args.status, 66);
                 if (!ok) break;
                 tc_fence_after();
-                const int m = m0 + lane;
                 for (int c = 16 * part; c < j.n; c += 16 * PARTS) {
                     uint32_t v[16];
                     tmem_ld16(tbase + acc.slot * GT_TILE_N + c, v);
                     tc_wait_ld();
-                    if (sizeof(O) == 2 && args.out16) {
-                        // a lane holds one output column of 16 rows: turned in shared memory, two rows to a word,
-                        // into 16-byte pieces of rows (stored as they are, 64 bytes an instruction, a tile's
-                        // outputs took 6 us)
-                        using T = std::conditional_t<sizeof(O) == 2, O, __half>;
-                        uint32_t *st = reinterpret_cast<uint32_t *>(box);
-                        __syncwarp();                                    // the previous pieces have been read
+                    if (SPLIT > 1) {
+                        uint4 *part = reinterpret_cast<uint4 *>(smem) + c / 4 * 128 + 32 * q + lane;   // [n / 4][128][4]
 #pragma unroll
-                        for (int i = 0; i < 8; ++i)
-                            st[i * 32 + lane] = pack2<T>(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1]));
-                        __syncwarp();
-                        // lane: rows 2 p and 2 p + 1, columns m0 + 8 (lane % 4) .. + 7; odd pairs read their halves in the
-                        // other order, which keeps the banks apart
-                        const int p = lane >> 2, m8 = m0 + (lane & 3) * 8, odd = p & 1;
-                        const uint4 *src = reinterpret_cast<const uint4 *>(st + p * 32 + (lane & 3) * 8);
-                        const uint4 x = src[odd], y = src[1 - odd], a = odd ? y : x, b = odd ? x : y;
-                        const uint4 row[2] = {{__byte_perm(a.x, a.y, 0x5410), __byte_perm(a.z, a.w, 0x5410),
-                                               __byte_perm(b.x, b.y, 0x5410), __byte_perm(b.z, b.w, 0x5410)},
-                                              {__byte_perm(a.x, a.y, 0x7632), __byte_perm(a.z, a.w, 0x7632),
-                                               __byte_perm(b.x, b.y, 0x7632), __byte_perm(b.z, b.w, 0x7632)}};
-#pragma unroll
-                        for (int i = 0; i < 2; ++i) {
-                            if (c + 2 * p + i >= j.n) continue;
-                            O *o = out + (int64_t)(j.c0 + c + 2 * p + i) * args.ldo + m8;
-                            if (m8 + 8 <= args.M) {
-                                *reinterpret_cast<uint4 *>(o) = row[i];
-                            } else {
-                                const O *e = reinterpret_cast<const O *>(row + i);
-#pragma unroll
-                                for (int q8 = 0; q8 < 8; ++q8)
-                                    if (m8 + q8 < args.M) o[q8] = e[q8];
-                            }
-                        }
-                    } else if (m < args.M) {
-                        O *o = out + (int64_t)(j.c0 + c) * args.ldo + m;
-#pragma unroll
-                        for (int i = 0; i < 16; ++i)
-                            if (c + i < j.n) o[i * args.ldo] = from_f32<O>(__uint_as_float(v[i]));
+                        for (int i = 0; i < 4; ++i) part[i * 128] = make_uint4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+                    } else {
+                        store16(j, m0, c, v, box);
                     }
                 }
             }
@@ -510,6 +528,37 @@ __global__ void __launch_bounds__(GroupSmem<MODE>::THREADS, 1)
     }
     tc_fence_before();
     __syncthreads();
+    if (SPLIT > 1) {
+        cluster_sync();                                  // every pair's part is in its shared memory
+        const GroupWalk<MODE> walk(args, s_off, s_tile, mb, cb, jobs);
+        if (warp >= 3 && walk.valid()) {
+            const GroupJob j = walk.get();
+            // 16 rows x 32 columns a piece, the pieces dealt out over the pairs' warps
+            const int pieces = ((j.n + 15) >> 4) * 4;
+            for (int i = (warp - 3) * SPLIT + (int)pair; i < pieces; i += SPLIT * SM::EPI_WARPS) {
+                const int q = i & 3, c = (i >> 2) * 16;
+                const uint32_t at = (c / 4 * 128 + 32 * q + lane) * 16;
+                float sum[16];
+#pragma unroll
+                for (int p = 0; p < SPLIT; ++p) {        // its own part first, then the next pair's: no CTA is asked by all
+                    const uint32_t from = cluster_addr(smem_u32(smem), 2 * ((pair + p) % SPLIT) + rank) + at;
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const float4 x = p ? ld_cluster_f32x4(from + k * 2048)
+                                           : *reinterpret_cast<const float4 *>(smem + at + k * 2048);
+                        sum[4 * k] = p ? sum[4 * k] + x.x : x.x;
+                        sum[4 * k + 1] = p ? sum[4 * k + 1] + x.y : x.y;
+                        sum[4 * k + 2] = p ? sum[4 * k + 2] + x.z : x.z;
+                        sum[4 * k + 3] = p ? sum[4 * k + 3] + x.w : x.w;
+                    }
+                }
+                uint32_t v[16];
+#pragma unroll
+                for (int k = 0; k < 16; ++k) v[k] = __float_as_uint(sum[k]);
+                store16(j, j.m0 + 128 * (int)rank + 32 * q, c, v, smem + SM::OFF_OUT + (warp - 3) * SM::OUT_WARP);
+            }
+        }
+    }
     // the issuer's last commit arrives in both CTAs: the other one waits for it too before it may exit
     if (rank == 1 && threadIdx.x == 32) mbar_wait(smem_u32(drain), 0, 0xFFFFFFFFu);
     cluster_sync();                                      // no arrival or MMA of the pair is outstanding past this
@@ -572,40 +621,122 @@ static bool encode_wide(CUtensorMap *m, int type, const void *base, int64_t cols
     return encode(m, type, base, n2 > 0 ? 4 : 3, {64, rows, cols / 64, n2}, {ld, 64, stride2}, {64, 64, 2, 1});
 }
 
-template <int MODE, class O, bool CUT = false>
-static int launch_tc(const GroupMaps &maps, const GroupTcArgs &a, int64_t max_jobs, cudaStream_t st)
+// Clusters of 2 SPLIT CTAs that are on the GPU together (0: an error).
+template <int MODE, class O, bool CUT, int SPLIT>
+static int fit_clusters(cudaLaunchConfig_t &cfg, cudaLaunchAttribute (&attr)[2], cudaStream_t st)
 {
     using SM = GroupSmem<MODE>;
-    if constexpr (MODE == K3_GROUP_GRAD_W && !CUT)
-        if (a.Nc * sizeof(O) % 16) return launch_tc<MODE, O, true>(maps, a, max_jobs, st);
-    auto kern = group_tc_kernel<MODE, O, CUT>;
+    auto kern = group_tc_kernel<MODE, O, CUT, SPLIT>;
     static unsigned long long attr_set = 0;
-    if (!k3_smem_attr(kern, SM::BYTES, attr_set)) return K3MOE_ERR_CUDA;
+    if (!k3_smem_attr(kern, SM::BYTES, attr_set)) return 0;
     const int sms = k3_num_sms();
-    if (sms < 2) return K3MOE_ERR_CUDA;
-    cudaLaunchAttribute attr[2];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim = {2, 1, 1};
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(2 * (unsigned)std::min<int64_t>(max_jobs, sms / 2));
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim = {2 * SPLIT, 1, 1};
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
+    cfg.gridDim = dim3(sms / (2 * SPLIT) * (2 * SPLIT));
     cfg.blockDim = SM::THREADS;
     cfg.dynamicSmemBytes = SM::BYTES;
     cfg.stream = st;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
-    cudaLaunchKernelEx(&cfg, kern, maps, a);
+    if (SPLIT == 1) return sms / 2;
+    static int fit = 0;
+    if (!fit) {
+        int n = 0;
+        cfg.numAttrs = 1;
+        if (cudaOccupancyMaxActiveClusters(&n, kern, &cfg) != cudaSuccess) {
+            cudaGetLastError();
+            n = 0;
+        }
+        cfg.numAttrs = 2;
+        fit = n > 0 ? n : -1;
+    }
+    return std::max(fit, 0);
+}
+
+template <int MODE, class O, bool CUT = false, int SPLIT = 1>
+static int launch_tc(const GroupMaps &maps, GroupTcArgs a, int64_t max_jobs, cudaStream_t st)
+{
+    if constexpr (MODE == K3_GROUP_GRAD_W && !CUT)
+        if (a.Nc * sizeof(O) % 16) return launch_tc<MODE, O, true>(maps, a, max_jobs, st);
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[2];
+    const int fit = fit_clusters<MODE, O, CUT, SPLIT>(cfg, attr, st);
+    if (fit < 1) return K3MOE_ERR_CUDA;
+    a.pairs = (int)std::min<int64_t>(max_jobs, fit);
+    cfg.gridDim = dim3(2 * SPLIT * (unsigned)a.pairs);
+    cudaLaunchKernelEx(&cfg, group_tc_kernel<MODE, O, CUT, SPLIT>, maps, a);
     k3_note_launch();
     return cudaGetLastError() == cudaSuccess ? K3MOE_OK : K3MOE_ERR_CUDA;
+}
+
+// mm, grad_x: most tiles of the widest kind: at most one partly filled one an expert with rows.
+static int64_t widest_tiles(const GroupTcArgs &a)
+{
+    return ((int64_t)a.rows / GT_TILE_N + std::min(a.E, a.rows)) * ((a.M + GT_TILE_M - 1) / GT_TILE_M);
+}
+
+// mm, grad_x: cycles that a call takes on `clusters` clusters of `split` pairs beyond its launch, its rows spread evenly
+// and its tiles chosen as the kernel does.  Measured on 33 shapes of one to 2,048 rows and 256 to 6144 contraction values,
+// the sum is within 10 %: a stage costs 256 + n cycles and not less than 370, a tile's end 26 n; adding up the parts
+// 1,600 and, as the network between SMs brings 8 bytes a cycle, 66 for each column that comes from another pair.
+static int64_t tile_cycles(const GroupTcArgs &a, int split, int clusters)
+{
+    const int64_t mb = (a.M + GT_TILE_M - 1) / GT_TILE_M, steps = (a.K + GT_BK - 1) / GT_BK;
+    const int64_t live = std::min(a.E, a.rows), each = (a.rows + live - 1) / live;
+    int64_t best = 0, n = 0, rounds = 0;
+    for (int i = 0; i < GT_TILE_PICKS; ++i) {
+        const int64_t tile = GT_TILE_N >> i, tiles = (each + tile - 1) / tile, r = (live * tiles * mb + clusters - 1) / clusters;
+        if (i == 0 || r * (256 + tile) < best) {
+            best = r * (256 + tile);
+            rounds = r;
+            n = ((each + tiles - 1) / tiles + 15) & ~(int64_t)15;
+        }
+    }
+    return rounds * ((steps + split - 1) / split) * std::max<int64_t>(370, 256 + n) + 26 * n +
+           (split > 1 ? 1600 + 66 * n * (split - 1) / split : 0);
+}
+
+// One pair a tile, or two or four where every tile then has a cluster of its own (whatever the offsets hold) and
+// that is faster: 1 row, 6144 to 64: 9.8 us with four, 14.5 with two, 22.8 with one; 16 experts of a row, 4096 to 512:
+// 12.7 with two, 17.1 with one; 1,024 rows, 1024 to 512: 10.8, 8.4, 8.0.
+template <int MODE, class O>
+static int launch_rows(const GroupMaps &maps, const GroupTcArgs &a, int64_t max_jobs, cudaStream_t st)
+{
+    const int64_t tiles = widest_tiles(a), steps = (a.K + GT_BK - 1) / GT_BK;
+    const int pairs = k3_num_sms() / 2;
+    if (tiles <= pairs / 2) {
+        cudaLaunchConfig_t cfg = {};
+        cudaLaunchAttribute attr[2];
+        int64_t best = tile_cycles(a, 1, pairs);
+        int split = 1;
+        const int fit[2] = {fit_clusters<MODE, O, false, 2>(cfg, attr, st), fit_clusters<MODE, O, false, 4>(cfg, attr, st)};
+        for (int i = 0; i < 2; ++i) {
+            if (tiles > fit[i] || steps < (2 << i)) continue;            // each pair has a stage
+            const int64_t c = tile_cycles(a, 2 << i, fit[i]);
+            if (c < best) best = c, split = 2 << i;
+        }
+        if (split == 4) return launch_tc<MODE, O, false, 4>(maps, a, max_jobs, st);
+        if (split == 2) return launch_tc<MODE, O, false, 2>(maps, a, max_jobs, st);
+    }
+    return launch_tc<MODE, O>(maps, a, max_jobs, st);
+}
+
+template <int MODE, class O>
+static int launch_mode(const GroupMaps &maps, const GroupTcArgs &a, int64_t max_jobs, cudaStream_t st)
+{
+    if constexpr (MODE == K3_GROUP_GRAD_W) return launch_tc<MODE, O>(maps, a, max_jobs, st);
+    else return launch_rows<MODE, O>(maps, a, max_jobs, st);
 }
 
 template <int MODE>
 static int launch_typed(const GroupMaps &maps, const GroupTcArgs &a, int out_type, int64_t max_jobs, cudaStream_t st)
 {
-    if (out_type == K3MOE_TYPE_F32) return launch_tc<MODE, float>(maps, a, max_jobs, st);
-    if (out_type == K3MOE_TYPE_BF16) return launch_tc<MODE, __nv_bfloat16>(maps, a, max_jobs, st);
-    return launch_tc<MODE, __half>(maps, a, max_jobs, st);
+    if (k3_num_sms() < 2) return K3MOE_ERR_CUDA;
+    if (out_type == K3MOE_TYPE_F32) return launch_mode<MODE, float>(maps, a, max_jobs, st);
+    if (out_type == K3MOE_TYPE_BF16) return launch_mode<MODE, __nv_bfloat16>(maps, a, max_jobs, st);
+    return launch_mode<MODE, __half>(maps, a, max_jobs, st);
 }
 
 }  // namespace k3
@@ -632,7 +763,6 @@ int k3_group_tc(int mode, const K3Group &g, cudaStream_t st)
     a.out = g.out;
     a.ldo = g.ldo;
     a.stride_o = g.stride_o;
-    a.pairs = k3_num_sms() / 2;
     a.status = g.status;
     bool ok = true;
     if (mode == K3_GROUP_GRAD_W) {

@@ -36,6 +36,17 @@ __device__ __forceinline__ uint32_t cluster_addr(uint32_t saddr, uint32_t rank)
     return r;
 }
 
+// Four values in the shared memory of any CTA of the cluster.
+__device__ __forceinline__ float4 ld_cluster_f32x4(uint32_t cluster_addr)
+{
+    float4 v;
+    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+                 : "r"(cluster_addr)
+                 : "memory");
+    return v;
+}
+
 // Arrive on a barrier anywhere in the cluster.
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t cluster_bar)
 {
@@ -159,12 +170,13 @@ __device__ __forceinline__ void tc_mma_f16_pair(uint32_t d_tmem, uint64_t adesc,
         : "memory");
 }
 
-// Arrive on `bar`'s offset in both CTAs once the pair MMAs issued so far by this thread have completed.
-__device__ __forceinline__ void tc_commit_pair(uint32_t bar)
+// Arrive on `bar`'s offset in both CTAs of the pair (of the cluster's CTAs lead, lead + 1) once the pair MMAs issued
+// so far by this thread have completed.
+__device__ __forceinline__ void tc_commit_pair(uint32_t bar, uint32_t lead = 0)
 {
     asm volatile(
         "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar),
-        "h"((uint16_t)3)
+        "h"((uint16_t)(3u << lead))
         : "memory");
 }
 

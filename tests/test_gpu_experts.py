@@ -201,6 +201,24 @@ def test_group_products(sizes, K, N, dt):
 
 
 @TYPES
+@pytest.mark.parametrize("sizes,long,short", [([1], 4096, 256), ([5], 2056, 72), ([0, 300], 3104, 520), ([257, 0, 3], 1000, 96),
+                                              ([40] * 6, 2048, 600), ([513, 1, 1], 2048, 256), ([700], 1608, 640),
+                                              ([256], 320, 256), ([16, 31], 2049 * 8, 40)])
+def test_group_products_of_few_tiles_and_long_contractions(sizes, long, short, dt):
+    for K, N in ((long, short), (short, long)):
+        off_d, off, x, dy, w = _group_inputs(sizes, K, N, dt, before=3, after=20)
+        a, b = int(off[0]), int(off[-1])
+        for t in (x, dy):
+            t[:a], t[b:] = float("nan"), float("inf")
+        _check_group(off_d, off, x, dy, w)
+        _check_group(off_d, off, x, dy, w, F32)
+        y, dx = ex.group_mm(x, w, off_d), ex.group_mm_grad_x(dy, w, off_d)
+        for _ in range(5):
+            assert torch.equal(ex.group_mm(x, w, off_d)[a:b], y[a:b])
+            assert torch.equal(ex.group_mm_grad_x(dy, w, off_d)[a:b], dx[a:b])
+
+
+@TYPES
 @pytest.mark.parametrize("sizes,K,N", [([3, 9], 7, 5), ([20, 0, 70], 33, 100), ([65], 129, 66)])
 def test_group_products_of_odd_widths(sizes, K, N, dt):
     _check_group(*_group_inputs(sizes, K, N, dt))
