@@ -16,11 +16,14 @@
 // cores bind at N = 256, the intake below.  Two accumulator sets (2 x 256 TMEM columns) let the epilogue
 // of one tile overlap the next tile's MMAs.
 //
-// Measured, bf16: 57,344 rows over 28 experts, 3584 to 6144: 1.33 ms, 1.9 PFLOP/s (513 cycles a stage, 512 are
-// the MMAs'); 8192^3 in one group 0.574 ms, 1.92 PFLOP/s; 65,536 rows over 112 experts 1.66-1.71 ms (467
-// cycles a stage at N = 192 to 208), 2.0 ms under the power cap; 251 rows over 112 experts 0.65 ms, the weights
-// at 6.8 TB/s; grad_w of 16,381 rows over 56 experts, 3584 x 3072 in fp32: 0.54 ms, of which the stores alone
-// take 0.43 (5.7 TB/s).
+// Where a call has few tiles, two or four pairs share a tile's contraction and add up their parts through
+// distributed shared memory (SPLIT below).
+//
+// Measured, bf16: 57,344 rows over 28 experts, 3584 to 6144: 1.27-1.34 ms, 1.9-2.0 PFLOP/s (513 cycles a stage, 512
+// are the MMAs'); 8192^3 in one group 0.574 ms, 1.92 PFLOP/s; 65,536 rows over 112 experts 1.64-1.71 ms (467
+// cycles a stage at N = 192 to 208), 1.9-2.0 ms under the power cap; 251 rows over 112 experts 0.63-0.65 ms, the
+// weights at 6.8 TB/s; grad_w of 16,381 rows over 56 experts, 3584 x 3072 in fp32: 0.54-0.57 ms, of which the stores
+// alone take 0.43 (5.7 TB/s); 1 row, 6144 to 64, 9.7 us (22.5 with one pair).
 #include <cudaTypedefs.h>
 
 #include "experts.h"
@@ -170,7 +173,7 @@ __device__ __forceinline__ void load_rows(const CUtensorMap *maps, uint32_t dst,
 }
 
 // CUT: grad_w's rows end inside 16 bytes (a variant of its own for the registers it costs).
-// SPLIT (mm, grad_x): the pairs of a cluster of 2 SPLIT CTAs share one tile's contraction, for calls of few tiles.  The
+// SPLIT: the pairs of a cluster of 2 SPLIT CTAs share one tile's contraction, for calls of few tiles.  The
 // caller gives every tile a cluster of its own: each pair leaves its part of the sum in its shared memory (the ring
 // is done with), and the pairs add up the parts of a share of the tile each, in a fixed order, and store it.
 template <int MODE, class O, bool CUT, int SPLIT>
@@ -191,7 +194,9 @@ __global__ void __launch_bounds__(GroupSmem<MODE>::THREADS, 1)
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     // this CTA's place in its pair, the pair's place in the cluster, the cluster rank of the pair's even CTA
     const uint32_t rank = cluster_ctarank() & 1, pair = SPLIT > 1 ? cluster_ctarank() >> 1 : 0, lead = 2 * pair;
-    static_assert(SPLIT == 1 || !W, "grad_w does not split");
+    // its stages of a job
+    auto first_stage = [&](const GroupJob &j) { return SPLIT == 1 ? 0 : (int)((uint32_t)j.steps * pair / SPLIT); };
+    auto end_stage = [&](const GroupJob &j) { return SPLIT == 1 ? j.steps : (int)((uint32_t)j.steps * (pair + 1) / SPLIT); };
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < NS; ++i) {
@@ -271,6 +276,75 @@ __global__ void __launch_bounds__(GroupSmem<MODE>::THREADS, 1)
         }
     };
 
+    // grad_w: 32 rows and CW columns (128 bytes a row); fill(h, v) gives the lane's row at columns h .. h + 15
+    constexpr int CW = 128 / (int)sizeof(O);
+    auto store_box = [&](const GroupJob &j, int e, int m0, int c, uint8_t *box, auto fill) {
+        // a box that crosses the last column of rows that end inside 16 bytes: the copy engine
+        // would write those 16 bytes whole, so its values are stored one by one
+        const bool cut = CUT && j.c0 + c + CW > args.Nc;
+        if (m0 < args.M && j.c0 + c < args.Nc) {                         // else wholly outside
+            if (!cut && lane == 0) bulk_wait_read<0>();                  // the box's previous store has read it
+            __syncwarp();
+#pragma unroll
+            for (int h = 0; h < CW; h += 16) {
+                uint32_t v[16] = {};
+                fill(h, v);
+                if (cut) {
+                    O *o = static_cast<O *>(args.out) + e * args.stride_o + (int64_t)(m0 + lane) * args.ldo + j.c0 + c + h;
+#pragma unroll
+                    for (int i = 0; i < 16; ++i)
+                        if (m0 + lane < args.M && j.c0 + c + h + i < args.Nc)
+                            o[i] = from_f32<O>(__uint_as_float(v[i]) + (args.accumulate ? to_f32(o[i]) : 0.f));
+                    continue;
+                }
+                // 16-byte pieces at the 128-byte swizzle's place: piece p of row r at p ^ (r % 8)
+#pragma unroll
+                for (int p = 0; p < (int)sizeof(O); ++p) {
+                    uint4 w;
+                    if (sizeof(O) == 4) {
+                        const uint32_t *f = v + (4 * p & 15);
+                        w = make_uint4(f[0], f[1], f[2], f[3]);
+                    } else {
+                        Vec<std::conditional_t<sizeof(O) == 4, __half, O>, 8> o;
+#pragma unroll
+                        for (int i = 0; i < 8; i += 2)
+                            o.set2(i, __uint_as_float(v[(8 * p + i) & 15]), __uint_as_float(v[(8 * p + i + 1) & 15]));
+                        w = make_uint4(o.w[0], o.w[1], o.w[2], o.w[3]);
+                    }
+                    const int piece = h * (int)sizeof(O) / 16 + p;
+                    *reinterpret_cast<uint4 *>(box + lane * 128 + ((piece ^ (lane & 7)) << 4)) = w;
+                }
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (!cut && lane == 0) {
+                if (args.accumulate) tma_add_3d(&maps.out, smem_u32(box), j.c0 + c, m0, e);
+                else tma_store_3d(&maps.out, smem_u32(box), j.c0 + c, m0, e);
+                bulk_commit();
+            }
+        }
+    };
+    // SPLIT: the sum of the pairs' parts at 16 columns from c, row `row` of this CTA's; its own part first, then the next
+    // pair's, so that no CTA is asked by all at once
+    auto add_parts = [&](int c, int row, uint32_t (&v)[16]) {
+        const uint32_t at = (c / 4 * 128 + row) * 16;
+        float sum[16];
+#pragma unroll
+        for (int p = 0; p < SPLIT; ++p) {
+            const uint32_t from = cluster_addr(smem_u32(smem), 2 * ((pair + p) % SPLIT) + rank) + at;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const float4 x = p ? ld_cluster_f32x4(from + k * 2048) : *reinterpret_cast<const float4 *>(smem + at + k * 2048);
+                sum[4 * k] = p ? sum[4 * k] + x.x : x.x;
+                sum[4 * k + 1] = p ? sum[4 * k + 1] + x.y : x.y;
+                sum[4 * k + 2] = p ? sum[4 * k + 2] + x.z : x.z;
+                sum[4 * k + 3] = p ? sum[4 * k + 3] + x.w : x.w;
+            }
+        }
+#pragma unroll
+        for (int k = 0; k < 16; ++k) v[k] = __float_as_uint(sum[k]);
+    };
+
     // The producer and issuer warps run their loops as whole warps, one elected lane doing the work.
     if (warp == 0) {
         // ------------------------------------------------------------ TMA producer (each CTA its half)
@@ -285,8 +359,8 @@ __global__ void __launch_bounds__(GroupSmem<MODE>::THREADS, 1)
             const int m = j.m0 + 128 * (int)rank, e = args.expert_coord * walk.e;
             const int c = j.c0 + half * (int)rank, r0 = walk.off0;
             const uint32_t bytes = GT_A_BYTES + half * 128;
-            const int s1 = j.steps * ((int)pair + 1) / SPLIT;            // this pair's stages
-            for (int s = j.steps * (int)pair / SPLIT; s < s1; ++s, ++issued, p.next()) {
+            const int s1 = end_stage(j);
+            for (int s = first_stage(j); s < s1; ++s, ++issued, p.next()) {
                 if (!pair_wait(smem_u32(empty + p.slot), p.phase ^ 1, abort_flag, args.status, 61)) {
                     ok = false;
                     break;
@@ -358,7 +432,7 @@ __global__ void __launch_bounds__(GroupSmem<MODE>::THREADS, 1)
         for (GroupWalk<MODE> walk(args, s_off, s_tile, mb, cb, jobs); walk.valid() && ok; walk.next()) {
             const GroupJob j = walk.get();
             const uint32_t idesc = idesc_f16(GT_TILE_M, (j.n + 15) & ~15, args.bf16) | major;
-            const int s0 = j.steps * (int)pair / SPLIT, s1 = j.steps * ((int)pair + 1) / SPLIT;
+            const int s0 = first_stage(j), s1 = end_stage(j);
             for (int s = s0; s < s1; ++s, p.next()) {
                 const bool begin = s == s0 || (W && s % GT_CHUNK == 0), last = s == j.steps - 1;
                 const bool end = s == s1 - 1 || (W && (s + 1) % GT_CHUNK == 0);
@@ -396,8 +470,8 @@ __global__ void __launch_bounds__(GroupSmem<MODE>::THREADS, 1)
         uint32_t it = 0;
         for (GroupWalk<MODE> walk(args, s_off, s_tile, mb, cb, jobs); walk.valid(); walk.next()) {
             const GroupJob j = walk.get();
-            it += j.steps;
-            if (j.steps == 0 || !(j.last & 15)) continue;
+            it += end_stage(j) - first_stage(j);
+            if (j.steps == 0 || !(j.last & 15) || pair != SPLIT - 1) continue;       // the last pair has the last stage
             const int slot = (it - 1) % NS;
             if (!pair_wait(smem_u32(tail + t.slot), t.phase, abort_flag, args.status, 65)) break;
             t.next();
@@ -416,22 +490,21 @@ __global__ void __launch_bounds__(GroupSmem<MODE>::THREADS, 1)
         const uint32_t tbase = tmem + ((uint32_t)(32 * q) << 16);
         const uint32_t tempty0 = cluster_addr(smem_u32(tempty), lead);
         RingPos<2> acc;
-        O *out = static_cast<O *>(args.out);
         uint8_t *box = smem + SM::OFF_OUT + (warp - 3) * SM::OUT_WARP;
         bool ok = true;
         for (GroupWalk<MODE> walk(args, s_off, s_tile, mb, cb, jobs); walk.valid() && ok; walk.next()) {
             const GroupJob j = walk.get();
             const int m0 = j.m0 + 128 * (int)rank + 32 * q;
             if (W) {
-                constexpr int CW = 128 / (int)sizeof(O);                 // columns of a 128-byte box row
-                const int chunks = (j.steps + GT_CHUNK - 1) / GT_CHUNK;
-                if (chunks == 0 && args.accumulate) continue;            // an expert without rows: nothing, or zeros
+                const int s0 = first_stage(j), s1 = end_stage(j);
+                const int chunks = s1 > s0 || SPLIT == 1 ? (s1 + GT_CHUNK - 1) / GT_CHUNK - s0 / GT_CHUNK : 0;
+                if (j.steps == 0 && args.accumulate) continue;           // an expert without rows: nothing, or zeros
                 float sum[COLS];
                 for (int ch = 0; ch < chunks; ++ch) {
                     ok = pair_wait(smem_u32(tfull + acc.slot), acc.phase, abort_flag, args.status, 66);
                     if (!ok) break;
                     tc_fence_after();
-                    if (chunks == 1) break;                              // stored from TMEM below
+                    if (SPLIT == 1 && chunks == 1) break;                // stored from TMEM below
 #pragma unroll
                     for (int g = 0; g < COLS / 8; ++g) {
                         uint32_t v[8];
@@ -447,60 +520,25 @@ __global__ void __launch_bounds__(GroupSmem<MODE>::THREADS, 1)
                     acc.next();
                 }
                 if (!ok) break;
+                if (SPLIT > 1) {
+                    float4 *mine = reinterpret_cast<float4 *>(smem) + part * COLS / 4 * 128 + 32 * q + lane;
 #pragma unroll
-                for (int g0 = 0; g0 < COLS; g0 += CW) {
-                    const int c = part * COLS + g0;
-                    // a box that crosses the last column of rows that end inside 16 bytes: the copy engine
-                    // would write those 16 bytes whole, so its values are stored one by one
-                    const bool cut = CUT && j.c0 + c + CW > args.Nc;
-                    if (m0 < args.M && j.c0 + c < args.Nc) {             // else wholly outside
-                        if (!cut && lane == 0) bulk_wait_read<0>();      // the box's previous store has read it
-                        __syncwarp();
-#pragma unroll
-                        for (int h = 0; h < CW; h += 16) {
-                            uint32_t v[16] = {};
-                            if (chunks == 1) {
-                                tmem_ld16(tbase + acc.slot * GT_TILE_N + c + h, v);
-                                tc_wait_ld();
-                            } else if (chunks > 1) {
-#pragma unroll
-                                for (int i = 0; i < 16; ++i) v[i] = __float_as_uint(sum[g0 + h + i]);
-                            }
-                            if (cut) {
-                                O *o = out + walk.e * args.stride_o + (int64_t)(m0 + lane) * args.ldo + j.c0 + c + h;
-#pragma unroll
-                                for (int i = 0; i < 16; ++i)
-                                    if (m0 + lane < args.M && j.c0 + c + h + i < args.Nc)
-                                        o[i] = from_f32<O>(__uint_as_float(v[i]) + (args.accumulate ? to_f32(o[i]) : 0.f));
-                                continue;
-                            }
-                            // 16-byte pieces at the 128-byte swizzle's place: piece p of row r at p ^ (r % 8)
-#pragma unroll
-                            for (int p = 0; p < (int)sizeof(O); ++p) {
-                                uint4 w;
-                                if (sizeof(O) == 4) {
-                                    const uint32_t *f = v + (4 * p & 15);
-                                    w = make_uint4(f[0], f[1], f[2], f[3]);
-                                } else {
-                                    Vec<std::conditional_t<sizeof(O) == 4, __half, O>, 8> o;
-#pragma unroll
-                                    for (int i = 0; i < 8; i += 2)
-                                        o.set2(i, __uint_as_float(v[(8 * p + i) & 15]), __uint_as_float(v[(8 * p + i + 1) & 15]));
-                                    w = make_uint4(o.w[0], o.w[1], o.w[2], o.w[3]);
-                                }
-                                const int piece = h * (int)sizeof(O) / 16 + p;
-                                *reinterpret_cast<uint4 *>(box + lane * 128 + ((piece ^ (lane & 7)) << 4)) = w;
-                            }
-                        }
-                        fence_proxy_async_smem();
-                        __syncwarp();
-                        if (!cut && lane == 0) {
-                            if (args.accumulate) tma_add_3d(&maps.out, smem_u32(box), j.c0 + c, m0, walk.e);
-                            else tma_store_3d(&maps.out, smem_u32(box), j.c0 + c, m0, walk.e);
-                            bulk_commit();
-                        }
-                    }
+                    for (int g = 0; g < COLS / 4; ++g)
+                        if (j.c0 + part * COLS + 4 * g < args.Nc)
+                            mine[g * 128] = chunks ? make_float4(sum[4 * g], sum[4 * g + 1], sum[4 * g + 2], sum[4 * g + 3]) : float4{};
+                    continue;
                 }
+#pragma unroll
+                for (int g0 = 0; g0 < COLS; g0 += CW)
+                    store_box(j, walk.e, m0, part * COLS + g0, box, [&](int h, uint32_t (&v)[16]) {
+                        if (chunks == 1) {
+                            tmem_ld16(tbase + acc.slot * GT_TILE_N + part * COLS + g0 + h, v);
+                            tc_wait_ld();
+                        } else if (chunks > 1) {
+#pragma unroll
+                            for (int i = 0; i < 16; ++i) v[i] = __float_as_uint(sum[g0 + h + i]);
+                        }
+                    });
                 if (chunks != 1) continue;
             } else {
                 ok = pair_wait(smem_u32(tfull + acc.slot), acc.phase, abort_flag, args.status, 66);
@@ -524,41 +562,32 @@ __global__ void __launch_bounds__(GroupSmem<MODE>::THREADS, 1)
             if (lane == 0) mbar_arrive_cluster(tempty0 + acc.slot * 8);
             acc.next();
         }
-        if (W && lane == 0) bulk_wait<0>();
     }
-    tc_fence_before();
-    __syncthreads();
     if (SPLIT > 1) {
+        tc_fence_before();
+        __syncthreads();
         cluster_sync();                                  // every pair's part is in its shared memory
         const GroupWalk<MODE> walk(args, s_off, s_tile, mb, cb, jobs);
         if (warp >= 3 && walk.valid()) {
             const GroupJob j = walk.get();
-            // 16 rows x 32 columns a piece, the pieces dealt out over the pairs' warps
-            const int pieces = ((j.n + 15) >> 4) * 4;
+            uint8_t *box = smem + SM::OFF_OUT + (warp - 3) * SM::OUT_WARP;
+            // pieces of 32 rows of the accumulator, dealt out over the pairs' warps
+            const int width = W ? CW : 16, pieces = W && j.steps == 0 && args.accumulate ? 0 : (j.n + width - 1) / width * 4;
             for (int i = (warp - 3) * SPLIT + (int)pair; i < pieces; i += SPLIT * SM::EPI_WARPS) {
-                const int q = i & 3, c = (i >> 2) * 16;
-                const uint32_t at = (c / 4 * 128 + 32 * q + lane) * 16;
-                float sum[16];
-#pragma unroll
-                for (int p = 0; p < SPLIT; ++p) {        // its own part first, then the next pair's: no CTA is asked by all
-                    const uint32_t from = cluster_addr(smem_u32(smem), 2 * ((pair + p) % SPLIT) + rank) + at;
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        const float4 x = p ? ld_cluster_f32x4(from + k * 2048)
-                                           : *reinterpret_cast<const float4 *>(smem + at + k * 2048);
-                        sum[4 * k] = p ? sum[4 * k] + x.x : x.x;
-                        sum[4 * k + 1] = p ? sum[4 * k + 1] + x.y : x.y;
-                        sum[4 * k + 2] = p ? sum[4 * k + 2] + x.z : x.z;
-                        sum[4 * k + 3] = p ? sum[4 * k + 3] + x.w : x.w;
-                    }
+                const int row = 32 * (i & 3), c = (i >> 2) * width, m0 = j.m0 + 128 * (int)rank + row;
+                if (W) {
+                    store_box(j, walk.e, m0, c, box, [&](int h, uint32_t (&v)[16]) { add_parts(c + h, row + lane, v); });
+                } else {
+                    uint32_t v[16];
+                    add_parts(c, row + lane, v);
+                    store16(j, m0, c, v, box);
                 }
-                uint32_t v[16];
-#pragma unroll
-                for (int k = 0; k < 16; ++k) v[k] = __float_as_uint(sum[k]);
-                store16(j, j.m0 + 128 * (int)rank + 32 * q, c, v, smem + SM::OFF_OUT + (warp - 3) * SM::OUT_WARP);
             }
         }
     }
+    if (W && warp >= 3 && lane == 0) bulk_wait<0>();
+    tc_fence_before();
+    __syncthreads();
     // the issuer's last commit arrives in both CTAs: the other one waits for it too before it may exit
     if (rank == 1 && threadIdx.x == 32) mbar_wait(smem_u32(drain), 0, 0xFFFFFFFFu);
     cluster_sync();                                      // no arrival or MMA of the pair is outstanding past this
@@ -723,10 +752,36 @@ static int launch_rows(const GroupMaps &maps, const GroupTcArgs &a, int64_t max_
     return launch_tc<MODE, O>(maps, a, max_jobs, st);
 }
 
+// grad_w the same way, its rows spread evenly: 550 cycles a stage, 500 and 40 a column for the parts.  One expert,
+// 2048 x 256, 32,768 rows: 62 us with four pairs a tile, 97 with two, 168 with one; 1,500 rows, 256 x 256: 16.9, 18.9, 21.0;
+// 1,000 rows: 17 with any.
+template <class O>
+static int launch_grad_w(const GroupMaps &maps, const GroupTcArgs &a, int64_t jobs, cudaStream_t st)
+{
+    constexpr int MODE = K3_GROUP_GRAD_W;
+    const int pairs = k3_num_sms() / 2;
+    if (jobs <= pairs / 2 && a.Nc * sizeof(O) % 16 == 0) {
+        cudaLaunchConfig_t cfg = {};
+        cudaLaunchAttribute attr[2];
+        const int64_t steps = (((int64_t)a.rows + a.E - 1) / a.E + GT_BK - 1) / GT_BK, n = std::min(a.Nc, GT_TILE_N);
+        const int fit[2] = {fit_clusters<MODE, O, false, 2>(cfg, attr, st), fit_clusters<MODE, O, false, 4>(cfg, attr, st)};
+        int64_t best = steps * 550;
+        int split = 1;
+        for (int i = 0; i < 2; ++i) {
+            const int k = 2 << i;
+            const int64_t c = (steps + k - 1) / k * 550 + 500 + 40 * n * (k - 1) / k;
+            if (jobs <= fit[i] && c < best) best = c, split = k;
+        }
+        if (split == 4) return launch_tc<MODE, O, false, 4>(maps, a, jobs, st);
+        if (split == 2) return launch_tc<MODE, O, false, 2>(maps, a, jobs, st);
+    }
+    return launch_tc<MODE, O>(maps, a, jobs, st);
+}
+
 template <int MODE, class O>
 static int launch_mode(const GroupMaps &maps, const GroupTcArgs &a, int64_t max_jobs, cudaStream_t st)
 {
-    if constexpr (MODE == K3_GROUP_GRAD_W) return launch_tc<MODE, O>(maps, a, max_jobs, st);
+    if constexpr (MODE == K3_GROUP_GRAD_W) return launch_grad_w<O>(maps, a, max_jobs, st);
     else return launch_rows<MODE, O>(maps, a, max_jobs, st);
 }
 

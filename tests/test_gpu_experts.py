@@ -298,6 +298,25 @@ def test_group_products_of_odd_widths_in_16_byte_rows(dt):
     _close(dw[..., :K], 2 * want, 2 * (rows + 3) * 2.0 ** -23 * mag)
 
 
+@TYPES
+@pytest.mark.parametrize("sizes,K,N", [([9001], 72, 264), ([6000, 1, 0, 70, 64, 3900], 256, 256), ([7003, 2100], 200, 520),
+                                       ([2600] * 5, 512, 1000), ([0, 12000], 8, 16)])
+def test_grad_w_of_few_tiles_and_many_rows(sizes, K, N, dt):
+    off_d, off, x, dy, _ = _group_inputs(sizes, K, N, dt, before=3, after=20)
+    a, b = int(off[0]), int(off[-1])
+    for t in (x, dy):
+        t[:a], t[b:] = float("nan"), float("inf")
+    xn, dn, rows = _np(x[:b]), _np(dy[:b]), np.diff(off)[:, None, None]
+    want, mag = ox.group_mm_grad_w(dn, xn, off), ox.group_mm_grad_w(np.abs(dn), np.abs(xn), off)
+    for o in (F32, dt):
+        dw = ex.group_mm_grad_w(dy, x, off_d, out_dtype=o)
+        _close(dw, want, (rows + 2) * 2.0 ** -23 * mag)
+        assert all(torch.equal(ex.group_mm_grad_w(dy, x, off_d, out_dtype=o), dw) for _ in range(3))
+    dw = torch.ones(len(sizes), N, K, device="cuda")
+    ex.group_mm_grad_w(dy, x, off_d, out=dw, accumulate=True)
+    _close(dw, 1 + want, (rows + 4) * 2.0 ** -23 * (1 + mag))
+
+
 def test_grad_w_of_long_groups_keeps_fp32_precision():
     # sums of 512-row parts in fp32: a rounding (2^-24) per part and the parts' own truncation (n 2^-23 / 16 of
     # a running sum at most); against the norm of the result 2e-6 covers both at any length
