@@ -252,7 +252,7 @@ __device__ __forceinline__ void sigmoid_any(float x, float &p, float &q)
 
 // The unit a = s f(g) h(u), s = sigmoid(g), of two elements: SiLU f = g, h = u; SiTU f = beta tanh(g / beta),
 // h = linear_beta tanh(u / linear_beta).  o0 = a t; GRAD: (o0, o1) = (da/dg, da/du) t.  SMALL: all tanh arguments
-// are within [-1, 1] and |g| <= 60, so that the sigmoid and both tanh share one reciprocal of a finite product.
+// are within [-1, 1] and |g| <= 60, so that the sigmoid and both tanh can share one reciprocal of a finite product.
 template <int ACT, bool GRAD, bool SMALL>
 __device__ __forceinline__ void glu_two(F2 g, F2 u, F2 t, const GluArgs &c, F2 &o0, F2 &o1)
 {
@@ -269,14 +269,15 @@ __device__ __forceinline__ void glu_two(F2 g, F2 u, F2 t, const GluArgs &c, F2 &
         tanh_quotient(mul2(u, u), c.u, nu, du);
         ng = mul2(ng, g);
         nu = mul2(nu, u);
-        const F2 ds = one_plus_exp_neg(g), dgu = mul2(dg, du), r = rcp2(mul2(ds, dgu));
+        const F2 ds = one_plus_exp_neg(g);
         if (GRAD) {
+            // a reciprocal each: the pipe of products binds (32,768 x 3072: 185 us, 197 with one of the product)
             // da/dg = h s (f (1 - s) + 1 - (f / beta)^2), da/du = s f (1 - (h / linear_beta)^2)
-            const F2 rs = mul2(r, ds), s = mul2(r, dgu), f = mul2(ng, mul2(rs, du)), h = mul2(nu, mul2(rs, dg)), st = mul2(s, t);
+            const F2 s = rcp2(ds), f = mul2(ng, rcp2(dg)), h = mul2(nu, rcp2(du)), st = mul2(s, t);
             o0 = mul2(mul2(h, st), fma2(f, fma2(f, f2(c.g.neg_inv2), fma2(s, neg, one)), one));
             o1 = mul2(mul2(f, st), fma2(mul2(h, f2(c.u.neg_inv2)), h, one));
         } else {
-            o0 = mul2(mul2(ng, nu), mul2(r, t));
+            o0 = mul2(mul2(ng, nu), mul2(rcp2(mul2(ds, mul2(dg, du))), t));
         }
     } else {
         F2 p, q;                                         // s = p q
@@ -354,7 +355,7 @@ __device__ __forceinline__ void move_on(P *&p, const int64_t (&bytes)[2], bool o
 
 // Pieces of V elements over the [rows, width] matrix; piece i is row i / nv, column (i % nv) V.  About 100 of the
 // warp instructions per 8 elements are the generator's; the arithmetic pipes bind next to HBM.  32,768 x 3072 bf16,
-// p = 0.1: SiLU 111 us (5.4 TB/s; without dropout 99 us, 6.1 TB/s), SiTU 152 us, the gradients 158 and 197 us.  CTAs
+// p = 0.1: SiLU 111 us (5.4 TB/s; without dropout 99 us, 6.1 TB/s), SiTU 152 us, the gradients 158 and 185 us.  CTAs
 // an SM (4, gradients 3 in registers) by measurement: more cost registers that spill, fewer leave latency open.
 template <class T, int V, int ACT, bool DROP, bool GRAD>
 __global__ void __launch_bounds__(PIPE_THREADS, GRAD ? 3 : 4) glu_kernel(const T *da, int64_t ldda, const T *gu, int64_t ldgu,
