@@ -395,7 +395,7 @@ int k3moe_rows_combine_grad(const void *dz, int64_t lddz, const void *y, int64_t
  * dtype F16 or BF16 for all inputs; out_dtype the same or F32.  accumulate (grad_w, F32 only): dw
  * is added to; otherwise an expert without rows gets zeros.  Results do not depend on timing.
  * Tensor-core kernels run where every row starts on a 16-byte boundary (pointers 16-byte aligned,
- * leading dimensions and strides multiples of 16 bytes), CUDA-core kernels elsewhere. */
+ * leading dimensions and strides multiples of 16 bytes), a slower kernel elsewhere. */
 int k3moe_group_mm(const int32_t *offsets, int n_experts, int rows, int n_in, int n_out, const void *x, int64_t ldx,
                    const void *w, int64_t ldw, int64_t stride_w, int dtype, void *y, int64_t ldy, int out_dtype,
                    int32_t *status, cudaStream_t stream);

@@ -1,96 +1,128 @@
-// Products grouped by expert (k3moe_group_mm, _grad_x, _grad_w): argument checks, and the CUDA-core
-// kernel of shapes and strides that the tensor-core kernels cannot take.
+// Products grouped by expert (k3moe_group_mm, _grad_x, _grad_w): argument checks, and the kernel of shapes
+// and strides that the copy engine, which feeds the main kernel (group_tc.cu), cannot address.
 #include "experts.h"
 #include "group_sched.cuh"
 
 namespace k3 {
 
-constexpr int GG_TILE = 64, GG_K = 16, GG_THREADS = 256;
+constexpr int GG_TILE = 64, GG_K = 32, GG_THREADS = 256, GG_ROW = GG_K + 8;    // 80-byte rows: no bank is hit twice
+// k steps summed by the tensor cores, which truncate, before the sum is added in fp32 (512 values, see group_tc.cu)
+constexpr int GG_CHUNK = 16;
 
-// 64 x 64 outputs per CTA, 4 x 4 per thread, contraction in steps of 16 through shared memory, fp32
-// sums in contraction order.  Any size, stride and alignment, at 19 TFLOP/s (65,536 rows, 3584 to 6144: shared
-// memory and FMA issue bind it; the tensor-core kernels take 1.7 ms there, this one 152).  Tile rows m run over the output's
-// contiguous axis for mm and grad_x (m = n_out / n_in index, columns = rows of x), and over n_out for
-// grad_w (columns = n_in).
+template <class T>
+__device__ __forceinline__ void mma_16816(float (&d)[4], const uint32_t (&a)[4], const uint32_t (&b)[2])
+{
+    if (std::is_same<T, __half>::value)
+        asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                     : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+                     : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b[0]), "r"(b[1]));
+    else
+        asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                     : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+                     : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b[0]), "r"(b[1]));
+}
+
+// Four 8 x 8 blocks of 16-bit values: lane i gives the address of row i % 8 of block i / 8.
+__device__ __forceinline__ void load_blocks(uint32_t (&r)[4], const void *row)
+{
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"((uint32_t)__cvta_generic_to_shared(row))
+                 : "memory");
+}
+
+// 64 x 64 outputs per CTA, 32 x 16 a warp, the contraction in steps of 32 through shared memory; the next step's
+// values are in flight meanwhile, one element a load, so any size, stride and alignment goes.  Those loads bind it:
+// 4,099 rows over 8 experts, 1001 to 2003: 267 us, 62 TFLOP/s (fp32 sums on the CUDA cores: 820); the gradients 281 and 316.
+// Tile rows x are output rows (tokens' rows; n_out for grad_w), columns y the output's contiguous axis.
 template <int MODE, class T, class O>
-__global__ void __launch_bounds__(GG_THREADS) group_generic_kernel(const K3Group g)
+__global__ void __launch_bounds__(GG_THREADS, 3) group_generic_kernel(const K3Group g)
 {
     griddep_enter();
-    __shared__ float sa[GG_K][GG_TILE + 1], sb[GG_K][GG_TILE + 1];
+    constexpr bool W = MODE == K3_GROUP_GRAD_W;
+    constexpr bool X_K = !W, Y_K = MODE == K3_GROUP_MM;                  // operands contiguous along the contraction
+    constexpr int LOADS = GG_TILE * GG_K / GG_THREADS;
+    __shared__ __align__(16) uint16_t sx[2][GG_TILE][GG_ROW], sy[2][GG_TILE][GG_ROW];
     __shared__ int s_off[K3MOE_TRAIN_MAX_EXPERTS + 1], s_tile[K3MOE_TRAIN_MAX_EXPERTS + 1], s_tmp[GG_THREADS / 32];
     if (!group_tiles<GG_THREADS, GG_TILE>(g.offsets, g.E, g.rows, s_off, s_tile, s_tmp, g.status)) return;
-    const T *A = static_cast<const T *>(g.a), *B = static_cast<const T *>(g.b);
+    const uint16_t *A = static_cast<const uint16_t *>(g.a), *B = static_cast<const uint16_t *>(g.b);
     O *out = static_cast<O *>(g.out);
-    const int M = MODE == K3_GROUP_GRAD_X ? g.n_in : g.n_out;            // tile rows
-    const int m_blocks = (M + GG_TILE - 1) / GG_TILE;
-    const int c_blocks = MODE == K3_GROUP_GRAD_W ? (g.n_in + GG_TILE - 1) / GG_TILE : 1;
-    const long long jobs = MODE == K3_GROUP_GRAD_W ? (long long)g.E * m_blocks * c_blocks
-                                                   : (long long)s_tile[g.E] * m_blocks;
-    const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
+    const int NY = MODE == K3_GROUP_MM ? g.n_out : g.n_in;
+    const int y_blocks = (NY + GG_TILE - 1) / GG_TILE, x_blocks = W ? (g.n_out + GG_TILE - 1) / GG_TILE : 1;
+    const long long jobs = (W ? (long long)g.E * x_blocks : (long long)s_tile[g.E]) * y_blocks;
+    const int lane = threadIdx.x & 31, wx = (threadIdx.x >> 5 & 1) * 32, wy = (threadIdx.x >> 6) * 16;
     for (long long job = blockIdx.x; job < jobs; job += gridDim.x) {
-        const int m0 = (int)(job % m_blocks) * GG_TILE;
-        int e, c0, c1, k1;                       // columns [c0, c1), contraction [0, k1)
+        const int y0 = (int)(job % y_blocks) * GG_TILE, t = (int)(job / y_blocks);
+        int e, x0, x1, k1;                       // tile rows [x0, x1), contraction [0, k1)
         long long r0 = 0;
-        if (MODE == K3_GROUP_GRAD_W) {
-            e = (int)(job / m_blocks / c_blocks);
-            c0 = (int)(job / m_blocks % c_blocks) * GG_TILE;
-            c1 = min(g.n_in, c0 + GG_TILE);
+        if (W) {
+            e = t / x_blocks;
+            x0 = t % x_blocks * GG_TILE;
+            x1 = g.n_out;
             r0 = s_off[e];
             k1 = s_off[e + 1] - s_off[e];
         } else {
-            const int t = (int)(job / m_blocks);
             e = group_find(s_tile, g.E, t);
-            c0 = s_off[e] + (t - s_tile[e]) * GG_TILE;
-            c1 = min(s_off[e + 1], c0 + GG_TILE);
+            x0 = s_off[e] + (t - s_tile[e]) * GG_TILE;
+            x1 = s_off[e + 1];
             k1 = MODE == K3_GROUP_MM ? g.n_in : g.n_out;
         }
-        float acc[4][4] = {};
-        for (int k0 = 0; k0 < k1; k0 += GG_K) {
-            for (int i = threadIdx.x; i < GG_K * GG_TILE; i += GG_THREADS) {
+        const uint16_t *Be = B + (W ? r0 * g.ldb : e * g.stride_b), *Ae = A + (W ? r0 * g.lda : 0);
+        uint16_t vx[LOADS], vy[LOADS];
+        auto fetch = [&](int k0) {
+#pragma unroll
+            for (int i = 0; i < LOADS; ++i) {
                 // consecutive threads along the operand's contiguous axis
-                const bool a_k = MODE == K3_GROUP_MM, b_k = MODE != K3_GROUP_GRAD_W;
-                const int ka = a_k ? i % GG_K : i / GG_TILE, ma = a_k ? i / GG_K : i % GG_TILE;
-                const int kb = b_k ? i % GG_K : i / GG_TILE, cb = b_k ? i / GG_K : i % GG_TILE;
-                float va = 0.f, vb = 0.f;
-                if (k0 + ka < k1 && m0 + ma < M) {
-                    if (MODE == K3_GROUP_MM)
-                        va = to_f32(B[e * g.stride_b + (m0 + ma) * g.ldb + k0 + ka]);
-                    else if (MODE == K3_GROUP_GRAD_X)
-                        va = to_f32(B[e * g.stride_b + (k0 + ka) * g.ldb + m0 + ma]);
-                    else
-                        va = to_f32(A[(r0 + k0 + ka) * g.lda + m0 + ma]);
-                }
-                if (k0 + kb < k1 && c0 + cb < c1) {
-                    if (MODE == K3_GROUP_GRAD_W)
-                        vb = to_f32(B[(r0 + k0 + kb) * g.ldb + c0 + cb]);
-                    else
-                        vb = to_f32(A[(int64_t)(c0 + cb) * g.lda + k0 + kb]);
-                }
-                sa[ka][ma] = va;
-                sb[kb][cb] = vb;
+                const int at = threadIdx.x + i * GG_THREADS;
+                const int kx = k0 + (X_K ? at % GG_K : at / GG_TILE), x = x0 + (X_K ? at / GG_K : at % GG_TILE);
+                const int ky = k0 + (Y_K ? at % GG_K : at / GG_TILE), y = y0 + (Y_K ? at / GG_K : at % GG_TILE);
+                vx[i] = kx < k1 && x < x1 ? Ae[X_K ? x * g.lda + kx : kx * g.lda + x] : (uint16_t)0;
+                vy[i] = ky < k1 && y < NY ? Be[Y_K ? y * g.ldb + ky : ky * g.ldb + y] : (uint16_t)0;
             }
-            __syncthreads();
+        };
+        float acc[2][2][4] = {}, sum[2][2][4] = {};
+        const int steps = (k1 + GG_K - 1) / GG_K;
+        if (steps > 0) fetch(0);
+        for (int s = 0; s < steps; ++s) {
+            const int b = s & 1;
 #pragma unroll
-            for (int k = 0; k < GG_K; ++k)
+            for (int i = 0; i < LOADS; ++i) {
+                const int at = threadIdx.x + i * GG_THREADS;
+                sx[b][X_K ? at / GG_K : at % GG_TILE][X_K ? at % GG_K : at / GG_TILE] = vx[i];
+                sy[b][Y_K ? at / GG_K : at % GG_TILE][Y_K ? at % GG_K : at / GG_TILE] = vy[i];
+            }
+            __syncthreads();                     // one a step: the other buffer was read before it
+            if (s + 1 < steps) fetch((s + 1) * GG_K);
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
+            for (int k = 0; k < GG_K; k += 16) {
+                uint32_t fa[2][4], fy[4];
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) acc[i][j] = fmaf(sa[k][tx + 16 * i], sb[k][ty + 16 * j], acc[i][j]);
-            __syncthreads();
+                for (int i = 0; i < 2; ++i) load_blocks(fa[i], &sx[b][wx + 16 * i + (lane & 15)][k + (lane >> 4) * 8]);
+                load_blocks(fy, &sy[b][wy + (lane >> 4) * 8 + (lane & 7)][k + (lane >> 3 & 1) * 8]);
+                const uint32_t fb[2][2] = {{fy[0], fy[1]}, {fy[2], fy[3]}};
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) mma_16816<T>(acc[i][j], fa[i], fb[j]);
+            }
+            if (s % GG_CHUNK == GG_CHUNK - 1 || s == steps - 1) {
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    (&sum[0][0][0])[i] += (&acc[0][0][0])[i];
+                    (&acc[0][0][0])[i] = 0.f;
+                }
+            }
         }
+        __syncthreads();                         // the next job writes the buffers
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const int m = m0 + tx + 16 * i, c = c0 + ty + 16 * j;
-                if (m >= M || c >= c1) continue;
-                if (MODE == K3_GROUP_GRAD_W) {
-                    O *o = out + e * g.stride_o + m * g.ldo + c;
-                    *o = from_f32<O>(g.accumulate ? to_f32(*o) + acc[i][j] : acc[i][j]);
-                } else {
-                    out[c * g.ldo + m] = from_f32<O>(acc[i][j]);
-                }
-            }
+        for (int i = 0; i < 16; ++i) {
+            const int x = x0 + wx + (i >> 3) * 16 + (lane >> 2) + (i >> 1 & 1) * 8;
+            const int y = y0 + wy + (i >> 2 & 1) * 8 + (lane & 3) * 2 + (i & 1);
+            if (x >= x1 || y >= NY) continue;
+            O *o = out + (W ? e * g.stride_o : 0) + x * g.ldo + y;
+            const float v = (&sum[0][0][0])[i];
+            *o = from_f32<O>(W && g.accumulate ? to_f32(*o) + v : v);
+        }
     }
 }
 
@@ -99,7 +131,7 @@ static int launch_generic(const K3Group &g, cudaStream_t st)
 {
     const int sms = k3_num_sms();
     if (!sms) return K3MOE_ERR_CUDA;
-    k3_launch(group_generic_kernel<MODE, T, O>, 4 * sms, GG_THREADS, 0, st, g);
+    k3_launch(group_generic_kernel<MODE, T, O>, 3 * sms, GG_THREADS, 0, st, g);
     k3_note_launch();
     return cudaGetLastError() == cudaSuccess ? K3MOE_OK : K3MOE_ERR_CUDA;
 }
