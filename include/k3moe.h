@@ -348,7 +348,10 @@ int k3moe_ep_dispatch(k3moe_handle *h, const int32_t *idx, int tokens_per_rank, 
  *
  * Conventions beyond those above:
  *   - dtype, out_dtype: K3MOE_TYPE_*.  Leading dimensions ld* are in elements and at least the row
- *     length.  Sums are held in fp32 and rounded once, to the output's type, to nearest even.
+ *     length.  Sums are held in fp32 and rounded once, to the output's type, to nearest even.  The
+ *     products' tensor cores truncate as they add: an fp32 result (any length) has an error of up to
+ *     2e-6 of the sum of its terms' sizes; a 16-bit one is rounded from a sum that has lost up to
+ *     3.2e-9 (bf16) or 6.4e-9 (f16) of that sum for each contraction value up to 8192, and 2e-6 beyond.
  *   - offsets: device int32 [n_experts + 1], non-decreasing, from >= 0 to <= rows: expert e owns
  *     rows offsets[e] .. offsets[e+1] - 1.  Rows before offsets[0] and from offsets[n_experts] on
  *     belong to no expert: never written, and not read into any result.

@@ -6,8 +6,8 @@
 namespace k3 {
 
 constexpr int GG_TILE = 64, GG_K = 32, GG_THREADS = 256, GG_ROW = GG_K + 8;    // 80-byte rows: no bank is hit twice
-// k steps summed by the tensor cores, which truncate, before the sum is added in fp32 (512 values, see group_tc.cu)
-constexpr int GG_CHUNK = 16;
+// k steps summed by the tensor cores, which truncate, before the sum is added in fp32 (512 values, f16 256: see group_tc.cu)
+template <class T> constexpr int GG_CHUNK = std::is_same<T, __half>::value ? 8 : 16;
 
 template <class T>
 __device__ __forceinline__ void mma_16816(float (&d)[4], const uint32_t (&a)[4], const uint32_t (&b)[2])
@@ -105,7 +105,7 @@ __global__ void __launch_bounds__(GG_THREADS, 3) group_generic_kernel(const K3Gr
 #pragma unroll
                     for (int j = 0; j < 2; ++j) mma_16816<T>(acc[i][j], fa[i], fb[j]);
             }
-            if (s % GG_CHUNK == GG_CHUNK - 1 || s == steps - 1) {
+            if (s % GG_CHUNK<T> == GG_CHUNK<T> - 1 || s == steps - 1) {
 #pragma unroll
                 for (int i = 0; i < 16; ++i) {
                     (&sum[0][0][0])[i] += (&acc[0][0][0])[i];

@@ -36,18 +36,22 @@ constexpr int GT_BK = 64, GT_TILE_M = 256, GT_TILE_N = 256;
 // mm, grad_x: row tiles of at most 256, 128, 64 or 32 rows, so that a few large experts still fill the GPU
 constexpr int GT_TILE_PICKS = 4;
 constexpr int GT_A_BYTES = 128 * GT_BK * 2, GT_STAGE = 2 * GT_A_BYTES;
-// grad_w: stages of one accumulation in TMEM (512 rows).  The tensor core truncates each sum it adds to
-// (1.2e-9 of the result a row: 3.8e-5 after 32,768 rows), so longer contractions are summed in registers
-// (error 5e-7 at any length).
-constexpr int GT_CHUNK = 8;
+// The tensor core truncates what it adds, always towards zero: products of one sign lose 3.2e-9 of their sum a
+// contraction value in bf16 and 6.3e-9 in f16, whose products have more bits (products of random sign 1.2e-9).  grad_w,
+// and mm and grad_x with an fp32 output, therefore add up parts of 512 (f16: 256) values in fp32 registers: an error of
+// 1.7e-6 of the sum at any length.  mm and grad_x with a 16-bit output do so from GT_LONG values on: below, the loss is at
+// most 1/9 of the f16 output's own half unit in the last place (bf16: 1/100).  Parts cost fp32 outputs 2-12 % in bf16
+// (2,047 rows over 14 experts, 3584 to 3584: 71 -> 73 us; 16,384 over 112, 3584 to 6144: 820 -> 845), for 16-bit ones it
+// would be 67 -> 72 and 792 -> 824 us; parts of 256 8192^3 568 -> 755 us against 606 with 512.
+constexpr int GT_PART_BF16 = 3, GT_PART_F16 = 2;                        // log2 of a part's stages
+constexpr int GT_LONG = 8192;
 // mm, grad_x: bytes of activation rows whose tiles pass under one block of weights before the next block
 constexpr int64_t GT_L2_ROWS = 32 << 20;
 
-template <int MODE>
+template <int MODE, bool FOLD>
 struct GroupSmem {
     static constexpr int NS = MODE == K3_GROUP_GRAD_W ? 5 : 6;
-    // grad_w's epilogue keeps 64 sums a thread and writes every value in fp32: four warps a TMEM quarter.  With as
-    // many, mm and grad_x gain nothing at any length and lose 0.3 to 0.8 us a small call.
+    // grad_w's epilogue keeps 64 sums a thread and writes every value in fp32: four warps a TMEM quarter
     static constexpr int EPI_WARPS = MODE == K3_GROUP_GRAD_W ? 16 : 8;
     static constexpr int THREADS = 96 + 32 * EPI_WARPS;                 // TMA, MMA, tails, epilogue
     static constexpr int OFF_OUT = NS * GT_STAGE;
@@ -78,6 +82,7 @@ struct GroupTcArgs {
     int expert_coord;        // 0: one weight for all experts
     int wide_a, wide_b;      // MN-major operands whose width is a multiple of 64: both 64 x 64 boxes in one copy
     int bf16, accumulate;
+    int part;                // FOLD: log2 of a part's stages
     int out16;               // mm, grad_x: output rows on 16-byte boundaries
     void *out;
     int64_t ldo, stride_o;
@@ -172,15 +177,25 @@ __device__ __forceinline__ void load_rows(const CUtensorMap *maps, uint32_t dst,
     }
 }
 
+// (a, b) += (c, d), both sums in one instruction
+__device__ __forceinline__ void add2(float &a, float &b, uint32_t c, uint32_t d)
+{
+    asm("{\n\t.reg .b64 x, y;\n\tmov.b64 x, {%0, %1};\n\tmov.b64 y, {%2, %3};\n\tadd.rn.f32x2 x, x, y;\n\t"
+        "mov.b64 {%0, %1}, x;\n\t}"
+        : "+f"(a), "+f"(b)
+        : "r"(c), "r"(d));
+}
+
+// FOLD: parts of the contraction are added up in registers; grad_w always, see GT_LONG.
 // CUT: grad_w's rows end inside 16 bytes (a variant of its own for the registers it costs).
 // SPLIT: the pairs of a cluster of 2 SPLIT CTAs share one tile's contraction, for calls of few tiles.  The
 // caller gives every tile a cluster of its own: each pair leaves its part of the sum in its shared memory (the ring
 // is done with), and the pairs add up the parts of a share of the tile each, in a fixed order, and store it.
-template <int MODE, class O, bool CUT, int SPLIT>
-__global__ void __launch_bounds__(GroupSmem<MODE>::THREADS, 1)
+template <int MODE, class O, bool CUT, int SPLIT, bool FOLD>
+__global__ void __launch_bounds__(GroupSmem<MODE, FOLD>::THREADS, 1)
     group_tc_kernel(const __grid_constant__ GroupMaps maps, const GroupTcArgs args)
 {
-    using SM = GroupSmem<MODE>;
+    using SM = GroupSmem<MODE, FOLD>;
     constexpr int NS = SM::NS;
     constexpr bool W = MODE == K3_GROUP_GRAD_W;
     extern __shared__ uint8_t smem_raw[];
@@ -194,6 +209,11 @@ __global__ void __launch_bounds__(GroupSmem<MODE>::THREADS, 1)
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     // this CTA's place in its pair, the pair's place in the cluster, the cluster rank of the pair's even CTA
     const uint32_t rank = cluster_ctarank() & 1, pair = SPLIT > 1 ? cluster_ctarank() >> 1 : 0, lead = 2 * pair;
+    // FOLD: parts of the stages s0 .. s1 - 1 (parts begin at multiples of their length)
+    auto parts = [&](int s0, int s1) {
+        const int up = (s1 + (1 << args.part) - 1) >> args.part;
+        return SPLIT == 1 ? up : s1 > s0 ? up - (s0 >> args.part) : 0;
+    };
     // its stages of a job
     auto first_stage = [&](const GroupJob &j) { return SPLIT == 1 ? 0 : (int)((uint32_t)j.steps * pair / SPLIT); };
     auto end_stage = [&](const GroupJob &j) { return SPLIT == 1 ? j.steps : (int)((uint32_t)j.steps * (pair + 1) / SPLIT); };
@@ -324,6 +344,12 @@ __global__ void __launch_bounds__(GroupSmem<MODE>::THREADS, 1)
             }
         }
     };
+    // SPLIT: 16 columns from c of row `row` into this pair's part of the sum, [n / 4][128][4]
+    auto put_part = [&](int c, int row, const uint32_t (&v)[16]) {
+        uint4 *at = reinterpret_cast<uint4 *>(smem) + c / 4 * 128 + row;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) at[i * 128] = make_uint4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+    };
     // SPLIT: the sum of the pairs' parts at 16 columns from c, row `row` of this CTA's; its own part first, then the next
     // pair's, so that no CTA is asked by all at once
     auto add_parts = [&](int c, int row, uint32_t (&v)[16]) {
@@ -426,6 +452,7 @@ __global__ void __launch_bounds__(GroupSmem<MODE>::THREADS, 1)
         const uint64_t ad0 = MODE == K3_GROUP_MM ? smem_desc_sw128(a0) : smem_desc_mn_sw128(a0, GT_A_BYTES / 2);
         const uint64_t bd0 = W ? smem_desc_mn_sw128(a0 + GT_A_BYTES, GT_A_BYTES / 2) : smem_desc_sw128(a0 + GT_A_BYTES);
         const bool one = elect_one();
+        const int part_mask = (1 << args.part) - 1;
         RingPos<NS> p;
         RingPos<2> acc;
         bool ok = true;
@@ -434,8 +461,8 @@ __global__ void __launch_bounds__(GroupSmem<MODE>::THREADS, 1)
             const uint32_t idesc = idesc_f16(GT_TILE_M, (j.n + 15) & ~15, args.bf16) | major;
             const int s0 = first_stage(j), s1 = end_stage(j);
             for (int s = s0; s < s1; ++s, p.next()) {
-                const bool begin = s == s0 || (W && s % GT_CHUNK == 0), last = s == j.steps - 1;
-                const bool end = s == s1 - 1 || (W && (s + 1) % GT_CHUNK == 0);
+                const bool begin = s == s0 || (FOLD && (s & part_mask) == 0), last = s == j.steps - 1;
+                const bool end = s == s1 - 1 || (FOLD && (s & part_mask) == part_mask);
                 if (begin) {
                     ok = pair_wait(smem_u32(tempty + acc.slot), acc.phase ^ 1, abort_flag, args.status, 63);
                     tc_fence_after();
@@ -497,7 +524,7 @@ __global__ void __launch_bounds__(GroupSmem<MODE>::THREADS, 1)
             const int m0 = j.m0 + 128 * (int)rank + 32 * q;
             if (W) {
                 const int s0 = first_stage(j), s1 = end_stage(j);
-                const int chunks = s1 > s0 || SPLIT == 1 ? (s1 + GT_CHUNK - 1) / GT_CHUNK - s0 / GT_CHUNK : 0;
+                const int chunks = parts(s0, s1);
                 if (j.steps == 0 && args.accumulate) continue;           // an expert without rows: nothing, or zeros
                 float sum[COLS];
                 for (int ch = 0; ch < chunks; ++ch) {
@@ -540,6 +567,41 @@ __global__ void __launch_bounds__(GroupSmem<MODE>::THREADS, 1)
                         }
                     });
                 if (chunks != 1) continue;
+            } else if (FOLD) {
+                // the warp's columns are 16 (part + PARTS i) .. + 15, so that narrow tiles occupy all warps
+                const int chunks = parts(first_stage(j), end_stage(j));
+                float sum[COLS] = {};
+                for (int ch = 0; ch < chunks; ++ch) {
+                    ok = pair_wait(smem_u32(tfull + acc.slot), acc.phase, abort_flag, args.status, 66);
+                    if (!ok) break;
+                    tc_fence_after();
+#pragma unroll
+                    for (int g = 0; g < COLS / 16; ++g) {
+                        const int c = 16 * (part + PARTS * g);
+                        if (c >= j.n) break;
+                        uint32_t v[16];
+                        tmem_ld16(tbase + acc.slot * GT_TILE_N + c, v);
+                        tc_wait_ld();
+#pragma unroll
+                        for (int i = 0; i < 16; i += 2) add2(sum[16 * g + i], sum[16 * g + i + 1], v[i], v[i + 1]);
+                    }
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive_cluster(tempty0 + acc.slot * 8);
+                    acc.next();
+                }
+                if (!ok) break;
+#pragma unroll
+                for (int g = 0; g < COLS / 16; ++g) {
+                    const int c = 16 * (part + PARTS * g);
+                    if (c >= j.n) break;
+                    uint32_t v[16];
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) v[i] = __float_as_uint(sum[16 * g + i]);
+                    if (SPLIT > 1) put_part(c, 32 * q + lane, v);
+                    else store16(j, m0, c, v, box);
+                }
+                continue;
             } else {
                 ok = pair_wait(smem_u32(tfull + acc.slot), acc.phase, abort_flag, args.status, 66);
                 if (!ok) break;
@@ -548,13 +610,8 @@ __global__ void __launch_bounds__(GroupSmem<MODE>::THREADS, 1)
                     uint32_t v[16];
                     tmem_ld16(tbase + acc.slot * GT_TILE_N + c, v);
                     tc_wait_ld();
-                    if (SPLIT > 1) {
-                        uint4 *part = reinterpret_cast<uint4 *>(smem) + c / 4 * 128 + 32 * q + lane;   // [n / 4][128][4]
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) part[i * 128] = make_uint4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
-                    } else {
-                        store16(j, m0, c, v, box);
-                    }
+                    if (SPLIT > 1) put_part(c, 32 * q + lane, v);
+                    else store16(j, m0, c, v, box);
                 }
             }
             tc_fence_before();
@@ -651,11 +708,11 @@ static bool encode_wide(CUtensorMap *m, int type, const void *base, int64_t cols
 }
 
 // Clusters of 2 SPLIT CTAs that are on the GPU together (0: an error).
-template <int MODE, class O, bool CUT, int SPLIT>
+template <int MODE, class O, bool CUT, int SPLIT, bool FOLD>
 static int fit_clusters(cudaLaunchConfig_t &cfg, cudaLaunchAttribute (&attr)[2], cudaStream_t st)
 {
-    using SM = GroupSmem<MODE>;
-    auto kern = group_tc_kernel<MODE, O, CUT, SPLIT>;
+    using SM = GroupSmem<MODE, FOLD>;
+    auto kern = group_tc_kernel<MODE, O, CUT, SPLIT, FOLD>;
     static unsigned long long attr_set = 0;
     if (!k3_smem_attr(kern, SM::BYTES, attr_set)) return 0;
     const int sms = k3_num_sms();
@@ -684,18 +741,18 @@ static int fit_clusters(cudaLaunchConfig_t &cfg, cudaLaunchAttribute (&attr)[2],
     return std::max(fit, 0);
 }
 
-template <int MODE, class O, bool CUT = false, int SPLIT = 1>
+template <int MODE, class O, bool FOLD, bool CUT = false, int SPLIT = 1>
 static int launch_tc(const GroupMaps &maps, GroupTcArgs a, int64_t max_jobs, cudaStream_t st)
 {
     if constexpr (MODE == K3_GROUP_GRAD_W && !CUT)
-        if (a.Nc * sizeof(O) % 16) return launch_tc<MODE, O, true>(maps, a, max_jobs, st);
+        if (a.Nc * sizeof(O) % 16) return launch_tc<MODE, O, FOLD, true>(maps, a, max_jobs, st);
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[2];
-    const int fit = fit_clusters<MODE, O, CUT, SPLIT>(cfg, attr, st);
+    const int fit = fit_clusters<MODE, O, CUT, SPLIT, FOLD>(cfg, attr, st);
     if (fit < 1) return K3MOE_ERR_CUDA;
     a.pairs = (int)std::min<int64_t>(max_jobs, fit);
     cfg.gridDim = dim3(2 * SPLIT * (unsigned)a.pairs);
-    cudaLaunchKernelEx(&cfg, group_tc_kernel<MODE, O, CUT, SPLIT>, maps, a);
+    cudaLaunchKernelEx(&cfg, group_tc_kernel<MODE, O, CUT, SPLIT, FOLD>, maps, a);
     k3_note_launch();
     return cudaGetLastError() == cudaSuccess ? K3MOE_OK : K3MOE_ERR_CUDA;
 }
@@ -730,7 +787,7 @@ static int64_t tile_cycles(const GroupTcArgs &a, int split, int clusters)
 // One pair a tile, or two or four where every tile then has a cluster of its own (whatever the offsets hold) and
 // that is faster: 1 row, 6144 to 64: 9.8 us with four, 14.5 with two, 22.8 with one; 16 experts of a row, 4096 to 512:
 // 12.7 with two, 17.1 with one; 1,024 rows, 1024 to 512: 10.8, 8.4, 8.0.
-template <int MODE, class O>
+template <int MODE, class O, bool FOLD>
 static int launch_rows(const GroupMaps &maps, const GroupTcArgs &a, int64_t max_jobs, cudaStream_t st)
 {
     const int64_t tiles = widest_tiles(a), steps = (a.K + GT_BK - 1) / GT_BK;
@@ -740,16 +797,17 @@ static int launch_rows(const GroupMaps &maps, const GroupTcArgs &a, int64_t max_
         cudaLaunchAttribute attr[2];
         int64_t best = tile_cycles(a, 1, pairs);
         int split = 1;
-        const int fit[2] = {fit_clusters<MODE, O, false, 2>(cfg, attr, st), fit_clusters<MODE, O, false, 4>(cfg, attr, st)};
+        const int fit[2] = {fit_clusters<MODE, O, false, 2, FOLD>(cfg, attr, st),
+                            fit_clusters<MODE, O, false, 4, FOLD>(cfg, attr, st)};
         for (int i = 0; i < 2; ++i) {
             if (tiles > fit[i] || steps < (2 << i)) continue;            // each pair has a stage
             const int64_t c = tile_cycles(a, 2 << i, fit[i]);
             if (c < best) best = c, split = 2 << i;
         }
-        if (split == 4) return launch_tc<MODE, O, false, 4>(maps, a, max_jobs, st);
-        if (split == 2) return launch_tc<MODE, O, false, 2>(maps, a, max_jobs, st);
+        if (split == 4) return launch_tc<MODE, O, FOLD, false, 4>(maps, a, max_jobs, st);
+        if (split == 2) return launch_tc<MODE, O, FOLD, false, 2>(maps, a, max_jobs, st);
     }
-    return launch_tc<MODE, O>(maps, a, max_jobs, st);
+    return launch_tc<MODE, O, FOLD>(maps, a, max_jobs, st);
 }
 
 // grad_w the same way, its rows spread evenly: 550 cycles a stage, 500 and 40 a column for the parts.  One expert,
@@ -764,7 +822,8 @@ static int launch_grad_w(const GroupMaps &maps, const GroupTcArgs &a, int64_t jo
         cudaLaunchConfig_t cfg = {};
         cudaLaunchAttribute attr[2];
         const int64_t steps = (((int64_t)a.rows + a.E - 1) / a.E + GT_BK - 1) / GT_BK, n = std::min(a.Nc, GT_TILE_N);
-        const int fit[2] = {fit_clusters<MODE, O, false, 2>(cfg, attr, st), fit_clusters<MODE, O, false, 4>(cfg, attr, st)};
+        const int fit[2] = {fit_clusters<MODE, O, false, 2, true>(cfg, attr, st),
+                            fit_clusters<MODE, O, false, 4, true>(cfg, attr, st)};
         int64_t best = steps * 550;
         int split = 1;
         for (int i = 0; i < 2; ++i) {
@@ -772,17 +831,18 @@ static int launch_grad_w(const GroupMaps &maps, const GroupTcArgs &a, int64_t jo
             const int64_t c = (steps + k - 1) / k * 550 + 500 + 40 * n * (k - 1) / k;
             if (jobs <= fit[i] && c < best) best = c, split = k;
         }
-        if (split == 4) return launch_tc<MODE, O, false, 4>(maps, a, jobs, st);
-        if (split == 2) return launch_tc<MODE, O, false, 2>(maps, a, jobs, st);
+        if (split == 4) return launch_tc<MODE, O, true, false, 4>(maps, a, jobs, st);
+        if (split == 2) return launch_tc<MODE, O, true, false, 2>(maps, a, jobs, st);
     }
-    return launch_tc<MODE, O>(maps, a, jobs, st);
+    return launch_tc<MODE, O, true>(maps, a, jobs, st);
 }
 
 template <int MODE, class O>
 static int launch_mode(const GroupMaps &maps, const GroupTcArgs &a, int64_t max_jobs, cudaStream_t st)
 {
     if constexpr (MODE == K3_GROUP_GRAD_W) return launch_grad_w<O>(maps, a, max_jobs, st);
-    else return launch_rows<MODE, O>(maps, a, max_jobs, st);
+    else if (a.K > (sizeof(O) == 4 ? GT_BK << a.part : GT_LONG)) return launch_rows<MODE, O, true>(maps, a, max_jobs, st);
+    else return launch_rows<MODE, O, false>(maps, a, max_jobs, st);
 }
 
 template <int MODE>
@@ -814,6 +874,7 @@ int k3_group_tc(int mode, const K3Group &g, cudaStream_t st)
     a.E = g.E;
     a.rows = g.rows;
     a.bf16 = g.dtype == K3MOE_TYPE_BF16;
+    a.part = a.bf16 ? GT_PART_BF16 : GT_PART_F16;
     a.accumulate = g.accumulate;
     a.out = g.out;
     a.ldo = g.ldo;
