@@ -233,21 +233,25 @@ __device__ __forceinline__ void tanh_quotient(F2 v2, const SoftLimit &c, F2 &num
     num = fma2(v2, f2(c.n), f2(1.0f));
     den = fma2(v2, fma2(v2, f2(c.d2), f2(c.d1)), f2(1.0f));
 }
-// tanh of any x: beyond 1 (e^2x - 1) / (e^2x + 1), with tanh 10 = 1 in fp32
-__device__ __forceinline__ float tanh_any(float x)
+// tanh of any x, beyond 1 as (1 - t) / (1 + t) with t = e^-2|x|, and its derivative 1 - tanh^2 = 4 t / (1 + t)^2, which
+// keeps its bits where the difference would have none left
+__device__ __forceinline__ float tanh_any(float x, float &slope)
 {
     const float v = x * x, num = fmaf(v, (float)TANH_N, 1.0f), den = fmaf(v, fmaf(v, (float)TANH_D2, (float)TANH_D1), 1.0f);
-    float e;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(2.8853900817779268f * fminf(fmaxf(x, -10.0f), 10.0f)));
-    const float big = (e - 1.0f) * rcp_fast(e + 1.0f);
-    return fabsf(x) <= 1.0f ? x * num * rcp_fast(den) : x != x ? x : big;
+    const float t = expf(-2.0f * fabsf(x)), r = rcp_fast(1.0f + t);
+    slope = 2.0f * t * r * (2.0f * r);
+    return fabsf(x) <= 1.0f ? x * num * rcp_fast(den) : copysignf((1.0f - t) * r, x);
 }
 
-// sigmoid of any x as p q, a few 2^-22 of it: both stay normal numbers where the sigmoid itself is a subnormal
-__device__ __forceinline__ void sigmoid_any(float x, float &p, float &q)
+// sigmoid of any x as p q, a few 2^-22 of it: both stay normal numbers where the sigmoid itself is a subnormal; c is
+// 1 - sigmoid, without the difference
+__device__ __forceinline__ void sigmoid_any(float x, float &p, float &q, float &c)
 {
-    p = expf(fminf(0.5f * x, 0.0f));
-    q = p * rcp_fast(1.0f + expf(-fabsf(x)));
+    const float e = expf(-0.5f * fabsf(x)), r = rcp_fast(fmaf(e, e, 1.0f)), low = e * r;      // sigmoid(|x|) = r, of -|x| e low
+    const bool neg = x < 0.0f;
+    p = neg ? e : 1.0f;
+    q = neg ? low : r;
+    c = neg ? r : e * low;
 }
 
 // The unit a = s f(g) h(u), s = sigmoid(g), of two elements: SiLU f = g, h = u; SiTU f = beta tanh(g / beta),
@@ -280,16 +284,16 @@ __device__ __forceinline__ void glu_two(F2 g, F2 u, F2 t, const GluArgs &c, F2 &
             o0 = mul2(mul2(ng, nu), mul2(rcp2(mul2(ds, mul2(dg, du))), t));
         }
     } else {
-        F2 p, q;                                         // s = p q
-        sigmoid_any(g.x, p.x, q.x);
-        sigmoid_any(g.y, p.y, q.y);
-        const F2 tg = {tanh_any(g.x * c.g.inv), tanh_any(g.y * c.g.inv)};
-        const F2 tu = {tanh_any(u.x * c.u.inv), tanh_any(u.y * c.u.inv)};
+        F2 p, q, c1;                                     // s = p q, 1 - s
+        sigmoid_any(g.x, p.x, q.x, c1.x);
+        sigmoid_any(g.y, p.y, q.y, c1.y);
+        F2 dg, du;                                       // 1 - tanh^2
+        const F2 tg = {tanh_any(g.x * c.g.inv, dg.x), tanh_any(g.y * c.g.inv, dg.y)};
+        const F2 tu = {tanh_any(u.x * c.u.inv, du.x), tanh_any(u.y * c.u.inv, du.y)};
         const F2 f = mul2(tg, f2(c.g.limit)), h = mul2(tu, f2(c.u.limit));
         if (GRAD) {
-            o0 = mul2(mul2(mul2(h, p), mul2(q, t)),
-                      fma2(f, fma2(mul2(p, q), neg, one), fma2(mul2(tg, tg), neg, one)));
-            o1 = mul2(mul2(mul2(f, p), mul2(q, t)), fma2(mul2(tu, tu), neg, one));
+            o0 = mul2(mul2(mul2(h, p), mul2(q, t)), fma2(f, c1, dg));
+            o1 = mul2(mul2(mul2(f, p), mul2(q, t)), du);
         } else {
             o0 = mul2(mul2(mul2(f, p), mul2(h, q)), t);
         }

@@ -36,25 +36,27 @@ def dropout(x, p, seed, offset, residual=None):
 
 
 def _branches(g, u, act, beta, linear_beta):
-    """s, f(g), f'(g), h(u), h'(u) of a = s f h."""
-    s = 1.0 / (1.0 + np.exp(-g))
-    if act == "silu":
-        return s, g, np.ones_like(g), u, np.ones_like(u)
-    tg, tu = np.tanh(g / beta), np.tanh(u / linear_beta)
-    return s, beta * tg, 1.0 - tg * tg, linear_beta * tu, 1.0 - tu * tu
+    """s, 1 - s, f(g), f'(g), h(u), h'(u) of a = s f h, without differences that cancel."""
+    with np.errstate(over="ignore"):
+        s, rest = 1.0 / (1.0 + np.exp(-g)), 1.0 / (1.0 + np.exp(g))
+        if act == "silu":
+            return s, rest, g, np.ones_like(g), u, np.ones_like(u)
+        slope = lambda x: 1.0 / np.square(np.cosh(x))  # noqa: E731
+        return (s, rest, beta * np.tanh(g / beta), slope(g / beta), linear_beta * np.tanh(u / linear_beta),
+                slope(u / linear_beta))
 
 
 def glu_dropout(gu, p, seed, offset, act="silu", beta=4.0, linear_beta=25.0):
     g, u = np.split(np.asarray(gu, dtype=np.float64), 2, axis=1)
-    s, f, _, h, _ = _branches(g, u, act, beta, linear_beta)
+    s, _, f, _, h, _ = _branches(g, u, act, beta, linear_beta)
     return dropout(s * f * h, p, seed, offset)
 
 
 def glu_dropout_grad(da, gu, p, seed, offset, act="silu", beta=4.0, linear_beta=25.0):
     g, u = np.split(np.asarray(gu, dtype=np.float64), 2, axis=1)
-    s, f, df, h, dh = _branches(g, u, act, beta, linear_beta)
+    s, rest, f, df, h, dh = _branches(g, u, act, beta, linear_beta)
     d = dropout(da, p, seed, offset)
-    return np.concatenate([d * h * (s * (1 - s) * f + s * df), d * s * f * dh], 1)
+    return np.concatenate([d * h * s * (rest * f + df), d * s * f * dh], 1)
 
 
 def plan_rows(idx, n_experts, first=0):
