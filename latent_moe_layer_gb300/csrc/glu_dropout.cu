@@ -175,8 +175,8 @@ __global__ void __launch_bounds__(PIPE_THREADS) dropout_kernel(const T *x, const
 }
 
 // ------------------------------------------------------------------ gated unit
-// Results are rounded to 16 bits, so the hardware exponential and reciprocal (2^-22 relative, subnormals
-// flushed) suffice; an infinite exponential gives the exact limits 0 and 1.
+// Results are rounded to 16 bits, so the hardware exponential and reciprocal suffice (2^-22 relative, and the rounding of
+// the exponential's argument, 2^-24 of it); an infinite exponential gives the exact limits 0 and 1.
 __device__ __forceinline__ float rcp_fast(float x)
 {
     float y;
@@ -207,15 +207,21 @@ __device__ __forceinline__ F2 mul2(F2 a, F2 b)
     return d;
 }
 __device__ __forceinline__ F2 rcp2(F2 a) { return {rcp_fast(a.x), rcp_fast(a.y)}; }
-// 1 + exp(-v)
+// 2^-SHIFT (1 + exp(-v))
+template <int SHIFT>
 __device__ __forceinline__ F2 one_plus_exp_neg(F2 v)
 {
-    const F2 t = mul2(v, f2(-1.4426950408889634f));
+    const F2 t = SHIFT ? fma2(v, f2(-1.4426950408889634f), f2((float)-SHIFT)) : mul2(v, f2(-1.4426950408889634f));
     float a, b;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(a) : "f"(t.x));
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(b) : "f"(t.y));
-    return fma2({a, b}, f2(1.0f), f2(1.0f));
+    return fma2({a, b}, f2(1.0f), f2(1.0f / (1 << SHIFT)));
 }
+// SiLU takes its sigmoid as 2^10 s: s itself is a subnormal from -87.34 down, which the reciprocal flushes, and g s is not.
+// So gates count down to -94.2 (the exponential alone leaves fp32 at -88.7); below, the unit is 0.  The other factor,
+// dropout's, brings the 2^-10 along; products keep 14 bits where the result is bf16's smallest normal number, more above.
+constexpr int SILU_SHIFT = 10;
+constexpr float SILU_UNIT = 1.0f / (1 << SILU_SHIFT);
 
 // The unit's constants.  tanh(x) = x (1 + TANH_N x^2) / (1 + TANH_D1 x^2 + TANH_D2 x^4) for |x| <= 1 within 7e-8 of
 // itself: the quotient of these degrees with the smallest largest relative error there (fitted in fp64; 2.1e-7
@@ -262,9 +268,14 @@ __device__ __forceinline__ void glu_two(F2 g, F2 u, F2 t, const GluArgs &c, F2 &
 {
     const F2 one = f2(1.0f), neg = f2(-1.0f);
     if (ACT == K3MOE_ACT_SILU) {
-        const F2 s = rcp2(one_plus_exp_neg(g)), f = mul2(g, s);
-        o0 = GRAD ? mul2(mul2(u, fma2(f, fma2(s, neg, one), s)), t) : mul2(mul2(f, u), t);
-        o1 = mul2(f, t);
+        // t has the factor SILU_UNIT
+        const F2 s = rcp2(one_plus_exp_neg<SILU_SHIFT>(g)), gt = mul2(g, t);
+        if (GRAD) {
+            o0 = mul2(mul2(mul2(u, t), s), fma2(g, fma2(s, f2(-SILU_UNIT), one), one));    // u s (1 + g (1 - s))
+            o1 = mul2(gt, s);
+        } else {
+            o0 = mul2(mul2(gt, u), s);
+        }
         return;
     }
     if (SMALL) {
@@ -273,7 +284,7 @@ __device__ __forceinline__ void glu_two(F2 g, F2 u, F2 t, const GluArgs &c, F2 &
         tanh_quotient(mul2(u, u), c.u, nu, du);
         ng = mul2(ng, g);
         nu = mul2(nu, u);
-        const F2 ds = one_plus_exp_neg(g);
+        const F2 ds = one_plus_exp_neg<0>(g);
         if (GRAD) {
             // a reciprocal each: the pipe of products binds (32,768 x 3072: 185 us, 197 with one of the product)
             // da/dg = h s (f (1 - s) + 1 - (f / beta)^2), da/du = s f (1 - (h / linear_beta)^2)
@@ -326,7 +337,7 @@ __device__ __forceinline__ void glu_piece(const Vec<T, V> (&in)[2 + GRAD], const
     for (int j = 0; j < V; j += 2) {
         const int k = V == 1 ? 0 : j + 1;
         const float2 g = in[0].get2(j), u = in[1].get2(j);
-        F2 v0, v1, t = f2(a.scale);
+        F2 v0, v1, t = f2(ACT == K3MOE_ACT_SILU ? a.scale * SILU_UNIT : a.scale);
         if (GRAD) {
             const float2 d = in[1 + GRAD].get2(j);
             t = mul2({d.x, d.y}, t);
@@ -359,13 +370,15 @@ __device__ __forceinline__ void move_on(P *&p, const int64_t (&bytes)[2], bool o
 
 // Pieces of V elements over the [rows, width] matrix; piece i is row i / nv, column (i % nv) V.  About 100 of the
 // warp instructions per 8 elements are the generator's; the arithmetic pipes bind next to HBM.  32,768 x 3072 bf16,
-// p = 0.1: SiLU 111 us (5.4 TB/s; without dropout 99 us, 6.1 TB/s), SiTU 152 us, the gradients 158 and 185 us.  CTAs
-// an SM (4, gradients 3 in registers) by measurement: more cost registers that spill, fewer leave latency open.
+// p = 0.1, back to back: SiLU 106 us (5.7 TB/s; without dropout 90 us, 6.7 TB/s), SiTU 146 us, the gradients 152 and 182
+// us.  CTAs an SM (registers) by measurement: more cost registers that spill, fewer leave latency open.  SiLU's gradient
+// took 187 us with the 72 registers of three CTAs, its forward without dropout 96 with the 54 of four.
+template <int ACT, bool DROP, bool GRAD>
+constexpr int glu_ctas() { return ACT == K3MOE_ACT_SILU ? (GRAD || DROP ? 4 : 5) : GRAD ? 3 : 4; }
 template <class T, int V, int ACT, bool DROP, bool GRAD>
-__global__ void __launch_bounds__(PIPE_THREADS, GRAD ? 3 : 4) glu_kernel(const T *da, int64_t ldda, const T *gu, int64_t ldgu,
-                                                                         int rows, int width, const GluArgs act,
-                                                                         const DropArgs a, const GluWalk walk, T *out,
-                                                                         int64_t ldo)
+__global__ void __launch_bounds__(PIPE_THREADS, glu_ctas<ACT, DROP, GRAD>())
+    glu_kernel(const T *da, int64_t ldda, const T *gu, int64_t ldgu, int rows, int width, const GluArgs act,
+               const DropArgs a, const GluWalk walk, T *out, int64_t ldo)
 {
     griddep_enter();
     const int nv = walk.nv;

@@ -80,3 +80,37 @@ def test_situ_of_infinite_inputs_has_its_limits():
     got = _np(ex.glu_dropout_grad(da, gu, act="situ"))[0]
     assert np.isfinite(got).all() and got[0] == 0 and got[1] == 0 and got[2] == 0          # saturated gates
     assert (got[8 + 2:8 + 5] == 0).all()                                                    # saturated up values
+
+
+@pytest.mark.parametrize("width", [64, 33])
+def test_silu_keeps_gates_whose_sigmoid_is_subnormal(width):
+    # e^-87.34 is fp32's smallest normal number; g e^g stays one of bf16's down to -91.8, and longer beside a large u.
+    # The hardware's exponential rounds its argument, |g| log2 e: |g| 2^-23 beside the few 2^-22 of the factors.
+    rng = np.random.default_rng(width)
+    rows = 96
+    g = rng.uniform(-94, -80, (rows, width))
+    u = _signs(rng, (rows, width)) * np.exp2(rng.uniform(10, 110, (rows, width)))
+    g[::4, ::3] = rng.standard_normal((rows // 4, (width + 2) // 3))           # ordinary gates beside them
+    gu = torch.from_numpy(np.concatenate([g, u], 1)).cuda().to(BF)
+    da = torch.from_numpy(rng.uniform(1, 2, (rows, width)) * 2.0 ** 14).cuda().to(BF)
+    n, d = _np(gu), _np(da)
+    slack = 2.0 ** -20 + np.abs(n[:, :width]) * 2.0 ** -23
+    for p in (0.0, 0.5):
+        kw = dict(p=p, seed=SEED, offset=OFFSET)
+        _close(ex.glu_dropout(gu, **kw), ox.glu_dropout(n, p, SEED, OFFSET), slack, "a")
+        # near its zero at g = -1.28 the gate's gradient cancels as its definition does
+        clear = np.concatenate([np.abs(n[:, :width] + 1.28) > 1, np.ones((rows, width), bool)], 1)
+        got, want = ex.glu_dropout_grad(da, gu, **kw), ox.glu_dropout_grad(d, n, p, SEED, OFFSET)
+        _close(got[torch.from_numpy(clear).cuda()], want[clear], np.concatenate([slack, slack], 1)[clear], "dgu")
+
+
+def test_silu_keeps_the_smallest_and_the_largest_results():
+    # results around bf16's smallest normal numbers and near its largest: 14 bits are left at 2^-126
+    g = torch.tensor([3.0, 1.0, -2.0, 5.0, 40.0, 1e30, 1e38, 2.0 ** 100], dtype=BF, device="cuda")
+    u = torch.tensor([2.0 ** -125, 2.0 ** -122, 2.0 ** -120, 2.0 ** -118, 2.0 ** -128, 1e8, 2.0, 2.0 ** 27], dtype=BF, device="cuda")
+    gu = torch.cat([g, u])[None].repeat(3, 1)
+    n = _np(gu)
+    _close(ex.glu_dropout(gu), ox.glu_dropout(n, 0, 0, 0), 2.0 ** -13, "a")
+    da = torch.full((3, 8), 0.5, dtype=BF, device="cuda")
+    got, want = ex.glu_dropout_grad(da, gu), ox.glu_dropout_grad(_np(da), n, 0, 0, 0)
+    _close(got, want, 2.0 ** -13, "dgu")
