@@ -97,10 +97,9 @@ __device__ __forceinline__ uint32_t e4m3_byte(float v)
 // 2^-X as fp32 for a block scale exponent -127 <= X <= 127.
 __device__ __forceinline__ float pow2_neg(int X) { return __uint_as_float((uint32_t)(127 - X) << 23); }
 
-// CL CTAs of a cluster take the same token tile and CL consecutive weight-row
-// blocks; each loads 1 / CL of the tile's activation boxes and multicasts them to
-// all CL, so the activation rows cross from L2 once per cluster, not once per CTA.
-template <int MODE, int CL>
+// Consecutive CTAs take consecutive weight-row blocks of one token tile, whose activation
+// rows each of them reads from L2.
+template <int MODE>
 __global__ void __launch_bounds__(THREADS, 1)
 mx_expert_kernel(const __grid_constant__ MxActMaps bmaps, const MxGemmArgs args)
 {
@@ -122,20 +121,12 @@ mx_expert_kernel(const __grid_constant__ MxActMaps bmaps, const MxGemmArgs args)
     constexpr int JOB_ROWS = MODE == MX_GLU ? 64 : 128;
     const int m_tiles = args.rows / JOB_ROWS;
     const uint32_t lim = args.spin_limit;
-    // job order: group jg = (tile, CL row blocks), cluster c takes groups c, c + nclusters, ...;
-    // rank r of the cluster takes row block (jg % groups per tile) CL + r of the group's tile
-    const int crank = CL > 1 ? (int)cluster_ctarank() : 0;
-    const int cid = CL > 1 ? (int)cluster_id_x() : (int)blockIdx.x;
-    const int ncl = CL > 1 ? (int)ncluster_x() : (int)gridDim.x;
-    const int mg = m_tiles / CL;
-    const int groups = __ldg(args.n_tiles) * mg;
-    auto job_of = [&](int jg) { return (jg / mg) * m_tiles + (jg % mg) * CL + crank; };
-    constexpr uint16_t CL_MASK = (uint16_t)((1u << CL) - 1u);
+    const int jobs = __ldg(args.n_tiles) * m_tiles;               // job t: tile t / m_tiles, row block t % m_tiles
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < NS; ++i) {
             mbar_init(smem_u32(full + i), 1);
-            mbar_init(smem_u32(empty + i), CL);        // every CTA of the cluster read the slot's activations
+            mbar_init(smem_u32(empty + i), 1);
         }
         for (int i = 0; i < NG; ++i) {
             mbar_init(smem_u32(gfull + i), 1);
@@ -160,7 +151,6 @@ mx_expert_kernel(const __grid_constant__ MxActMaps bmaps, const MxGemmArgs args)
     }
     tc_fence_before();
     __syncthreads();
-    if (CL > 1) cluster_sync();          // the cluster's barriers exist before any multicast reaches them
     tc_fence_after();
     const uint32_t tmem = *tmem_holder;
 
@@ -182,8 +172,7 @@ mx_expert_kernel(const __grid_constant__ MxActMaps bmaps, const MxGemmArgs args)
                 m0 = (t % m_tiles) * JOB_ROWS;
                 m1 = MODE == MX_GLU ? m0 : m0 + MX_WBOX;
             };
-            for (int jg = cid; jg < groups && ok && !*abort_flag; jg += ncl) {
-                const int t = job_of(jg);
+            for (int t = blockIdx.x; t < jobs && ok && !*abort_flag; t += gridDim.x) {
                 const int4 tile = __ldg(args.tiles + t / m_tiles);
                 const int g = tile.x, row0 = tile.y;
                 const CUtensorMap *w0, *w1;
@@ -225,17 +214,11 @@ mx_expert_kernel(const __grid_constant__ MxActMaps bmaps, const MxGemmArgs args)
                     const uint32_t bb = smem_u32(smem + OFF_B + slot * B_BYTES);
                     tma_load_2d_hint(a, w0, fb, MX_KS * s, m0, pol_w);
                     tma_load_2d_hint(a + MX_WBOX * MX_KS, w1, fb, MX_KS * s, m1, pol_w);
-                    // activation boxes: box i from rank i % CL, multicast to the whole cluster
-                    for (int i = crank; i < nbig + nsmall; i += CL) {
-                        const bool big = i < nbig;
-                        const uint32_t dst = bb + (big ? i * 64 * MX_KS : nbig * 64 * MX_KS + (i - nbig) * 16 * MX_KS);
-                        const CUtensorMap *bm = big ? &bmaps.big : &bmaps.small;
-                        const int r = big ? row0 + 64 * i : row0 + 64 * nbig + 16 * (i - nbig);
-                        if (CL > 1)
-                            tma_load_2d_mc(dst, bm, fb, MX_KS * s, r, CL_MASK, pol_b);
-                        else
-                            tma_load_2d_hint(dst, bm, fb, MX_KS * s, r, pol_b);
-                    }
+                    for (int b = 0; b < nbig; ++b)
+                        tma_load_2d_hint(bb + b * 64 * MX_KS, &bmaps.big, fb, MX_KS * s, row0 + 64 * b, pol_b);
+                    for (int b = 0; b < nsmall; ++b)
+                        tma_load_2d_hint(bb + (nbig * 64 + b * 16) * MX_KS, &bmaps.small, fb, MX_KS * s,
+                                         row0 + 64 * nbig + 16 * b, pol_b);
                 }
             }
             mx_drain(full, it, NS);
@@ -246,8 +229,7 @@ mx_expert_kernel(const __grid_constant__ MxActMaps bmaps, const MxGemmArgs args)
         if (lane == 0) {
             uint32_t it = 0, sit = 0, tc = 0;
             bool ok = true;
-            for (int jg = cid; jg < groups && ok && !*abort_flag; jg += ncl, ++tc) {
-                const int t = job_of(jg);
+            for (int t = blockIdx.x; t < jobs && ok && !*abort_flag; t += gridDim.x, ++tc) {
                 const int4 tile = __ldg(args.tiles + t / m_tiles);
                 const int nmma = min(MX_BN, max(16, (tile.z + 15) & ~15));
                 uint32_t idesc[4];
@@ -272,10 +254,7 @@ mx_expert_kernel(const __grid_constant__ MxActMaps bmaps, const MxGemmArgs args)
                     for (int kk = 0; kk < 4; ++kk)        // 32 K (32 bytes of both operands) per MMA
                         tc_mma_mx(dcol, adesc + 2 * kk, bdesc + 2 * kk, idesc[kk], sfa, sfa + 4,
                                   (s > 0 || kk > 0) ? 1u : 0u);
-                    if (CL > 1)
-                        tc_commit_mc(smem_u32(empty + slot), CL_MASK);   // the slot's activations came from every rank
-                    else
-                        tc_commit(smem_u32(empty + slot));
+                    tc_commit(smem_u32(empty + slot));
                     tc_commit(smem_u32(sempty + ss));
                 }
                 if (!ok) break;
@@ -290,8 +269,7 @@ mx_expert_kernel(const __grid_constant__ MxActMaps bmaps, const MxGemmArgs args)
         const uint32_t lane_base = tmem + ((uint32_t)(32 * q) << 16);
         uint32_t sit = 0, git = 0;
         bool ok = true;
-        for (int jg = cid; jg < groups && ok && !*abort_flag; jg += ncl) {
-            const int t = job_of(jg);
+        for (int t = blockIdx.x; t < jobs && ok && !*abort_flag; t += gridDim.x) {
             const int4 tile = __ldg(args.tiles + t / m_tiles);
             const int nmma = min(MX_BN, max(16, (tile.z + 15) & ~15));
             const int nsfb = (nmma + 31) >> 5;
@@ -343,8 +321,7 @@ mx_expert_kernel(const __grid_constant__ MxActMaps bmaps, const MxGemmArgs args)
         float *xbuf = reinterpret_cast<float *>(smem + OFF_X);
         uint32_t tc = 0, xit = 0;
         bool bad = false, ok = true;
-        for (int jg = cid; jg < groups && ok && !*abort_flag; jg += ncl, ++tc) {
-            const int t = job_of(jg);
+        for (int t = blockIdx.x; t < jobs && ok && !*abort_flag; t += gridDim.x, ++tc) {
             const int4 tile = __ldg(args.tiles + t / m_tiles);
             const int row0 = tile.y, nrows = tile.z;
             const int m0 = (t % m_tiles) * JOB_ROWS;
@@ -427,8 +404,6 @@ mx_expert_kernel(const __grid_constant__ MxActMaps bmaps, const MxGemmArgs args)
 
     tc_fence_before();
     __syncthreads();
-    // no CTA leaves while another rank may still multicast into its shared memory
-    if (CL > 1) cluster_sync();
     if (warp == 1) {
         tc_fence_after();
         tmem_dealloc(tmem, 512);
@@ -534,58 +509,21 @@ bool k3_encode_mx_act(MxActMaps *m, const uint8_t *q, const uint8_t *s, int rows
            encode_bytes(&m->ssmall, s, rows, K / 32, 16, 16, false);
 }
 
-template <int MODE, int CL>
-static int launch_mx(const MxActMaps &b, const MxGemmArgs &a, int max_jobs, cudaStream_t st)
+template <int MODE>
+static int launch_mx(const MxActMaps &b, const MxGemmArgs &a, int max_jobs, int num_sms, cudaStream_t st)
 {
-    auto kern = mx_expert_kernel<MODE, CL>;
+    auto kern = mx_expert_kernel<MODE>;
     static unsigned long long attr_set = 0;
-    static int max_clusters[64] = {};
     if (!k3_smem_attr(kern, SMEM_BYTES, attr_set)) return K3MOE_ERR_CUDA;
-    int dev = 0;
-    K3_CUDA_TRY(cudaGetDevice(&dev));
-    cudaLaunchAttribute attr[2];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = CL;
-    attr[0].val.clusterDim.y = 1;
-    attr[0].val.clusterDim.z = 1;
-    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[1].val.programmaticStreamSerializationAllowed = 1;
-    cudaLaunchConfig_t cfg = {};
-    cfg.blockDim = THREADS;
-    cfg.dynamicSmemBytes = SMEM_BYTES;
-    cfg.stream = st;
-    cfg.attrs = attr;
-    if (dev >= 64) return K3MOE_ERR_UNSUPPORTED;
-    if (!max_clusters[dev]) {
-        // how many clusters of CL one-CTA-per-SM blocks the GPU holds at once
-        int sms = 0;
-        K3_CUDA_TRY(cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev));
-        cfg.gridDim = dim3(CL * (sms / CL), 1, 1);
-        cfg.numAttrs = 1;
-        int n = 0;
-        K3_CUDA_TRY(cudaOccupancyMaxActiveClusters(&n, kern, &cfg));
-        if (n < 1) return K3MOE_ERR_CUDA;
-        max_clusters[dev] = n;
-    }
-    const int groups = max(1, (max_jobs + CL - 1) / CL);
-    cfg.gridDim = dim3(CL * min(max_clusters[dev], groups), 1, 1);
-    cfg.numAttrs = 2;
-    K3_CUDA_TRY(cudaLaunchKernelEx(&cfg, kern, b, a));
+    k3_launch(kern, max(1, min(max_jobs, num_sms)), THREADS, SMEM_BYTES, st, b, a);
     k3_note_launch();
-    return K3MOE_OK;
+    return cudaGetLastError() == cudaSuccess ? K3MOE_OK : K3MOE_ERR_CUDA;
 }
 
 int k3_launch_mx_expert(int mode, const MxActMaps &b, const MxGemmArgs &a, int max_jobs, int num_sms,
                         cudaStream_t st)
 {
-    (void)num_sms;
-    // clusters of 4 where the weight-row blocks split evenly (the K3 shapes: 48 and 28 blocks)
-    const int blocks = a.rows / (mode == MX_GLU ? 64 : 128);
-    if (blocks % 4 == 0)
-        return mode == MX_GLU ? launch_mx<MX_GLU, 4>(b, a, max_jobs, st) : launch_mx<MX_DOWN, 4>(b, a, max_jobs, st);
-    if (blocks % 2 == 0)
-        return mode == MX_GLU ? launch_mx<MX_GLU, 2>(b, a, max_jobs, st) : launch_mx<MX_DOWN, 2>(b, a, max_jobs, st);
-    return mode == MX_GLU ? launch_mx<MX_GLU, 1>(b, a, max_jobs, st) : launch_mx<MX_DOWN, 1>(b, a, max_jobs, st);
+    return mode == MX_GLU ? launch_mx<MX_GLU>(b, a, max_jobs, num_sms, st) : launch_mx<MX_DOWN>(b, a, max_jobs, num_sms, st);
 }
 
 int k3_launch_prep_mx8(const uint16_t *h, int T, int L, const int32_t *row_of, int K, uint8_t *q, uint8_t *s,
