@@ -4,6 +4,7 @@
 // for: a dropout takes 3.8 us through here, 8.4 us through Python and ctypes, 3 us of either the library's.
 #include <Python.h>
 
+#include <ATen/core/grad_mode.h>
 #include <ATen/ops/empty.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
@@ -53,10 +54,16 @@ void check(int rc, const char *what)
 }
 
 // ---------------------------------------------------------------------------- arguments
+// A tensor.  The calls record nothing for autograd, so one that needs gradients is refused where they would be
+// recorded, rather than left out of them.
 const at::Tensor &tensor(PyObject *o, const char *what)
 {
     if (!THPVariable_Check(o)) refuse(std::string(what) + ": a tensor");
-    return THPVariable_Unpack(o);
+    const at::Tensor &t = THPVariable_Unpack(o);
+    if (t.requires_grad() && at::GradMode::is_enabled())
+        refuse(std::string(what) + ": requires gradients, which these calls do not record (detach it, or call under torch.no_grad)",
+               K3MOE_ERR_UNSUPPORTED);
+    return t;
 }
 
 const at::Tensor *maybe(PyObject *o, const char *what) { return o == Py_None ? nullptr : &tensor(o, what); }
@@ -220,9 +227,17 @@ int act_code(PyObject *o)
 
 PyObject *wrap(at::Tensor t) { return THPVariable_Wrap(std::move(t)); }
 
-PyObject *wrap2(at::Tensor a, at::Tensor b)
+// The output of a call, `given` by the caller or new.  A given one was written in place: autograd is told, as any
+// graph that has saved it must notice.
+PyObject *written(at::Tensor t, PyObject *given)
 {
-    PyObject *x = wrap(std::move(a)), *y = x ? wrap(std::move(b)) : nullptr;
+    if (given != Py_None && !t.is_inference()) t.unsafeGetTensorImpl()->bump_version();
+    return wrap(std::move(t));
+}
+
+PyObject *pair(PyObject *x, at::Tensor b)
+{
+    PyObject *y = x ? wrap(std::move(b)) : nullptr;
     PyObject *t = y ? PyTuple_Pack(2, x, y) : nullptr;
     Py_XDECREF(x);
     Py_XDECREF(y);
@@ -245,7 +260,7 @@ PyObject *plan_rows(Args a)                  // idx, n_experts, first_expert
     check(entry<PLAN>(&k3moe_rows_plan)(x.p, (int)x.T, (int)x.K, first, E, static_cast<int32_t *>(offsets.data_ptr()),
                                         static_cast<int32_t *>(pos.data_ptr()), ws.data_ptr(), nb, at.stream),
           "plan_rows");
-    return wrap2(std::move(offsets), std::move(pos));
+    return pair(wrap(std::move(offsets)), std::move(pos));
 }
 
 PyObject *gather_rows(Args a)                // x, pos, n_rows, out
@@ -263,7 +278,7 @@ PyObject *gather_rows(Args a)                // x, pos, n_rows, out
                                             type_code(xt.scalar_type(), "x"), o.p, o.ld, (int)(n < 0 ? o.n : n), at.status(),
                                             at.stream),
           "gather_rows");
-    return wrap(std::move(out));
+    return written(std::move(out), a[3]);
 }
 
 PyObject *combine_rows(Args a)               // y, pos, weights, out
@@ -279,7 +294,7 @@ PyObject *combine_rows(Args a)               // y, pos, weights, out
     check(entry<COMBINE>(&k3moe_rows_combine)(y.p, y.ld, (int)y.n, pos.p, wp, (int)pos.T, (int)pos.K, (int)y.width,
                                               type_code(yt.scalar_type(), "y"), z.p, z.ld, at.status(), at.stream),
           "combine_rows");
-    return wrap(std::move(out));
+    return written(std::move(out), a[3]);
 }
 
 PyObject *combine_rows_grad(Args a)          // dz, y, pos, weights, out
@@ -297,7 +312,7 @@ PyObject *combine_rows_grad(Args a)          // dz, y, pos, weights, out
                                                         (int)y.width, type_code(yt.scalar_type(), "y"), dy.p, dy.ld,
                                                         static_cast<float *>(dw.data_ptr()), at.status(), at.stream),
           "combine_rows_grad");
-    return wrap2(std::move(out), std::move(dw));
+    return pair(written(std::move(out), a[4]), std::move(dw));
 }
 
 at::ScalarType scalar_type(PyObject *o, at::ScalarType otherwise)
@@ -326,7 +341,7 @@ PyObject *product(Args a, bool mm)           // rows, w, offsets, out, out_dtype
                                     type_code(t.scalar_type(), what), o.p, o.ld, type_code(type, "out"), at.status(),
                                     at.stream),
           mm ? "group_mm" : "group_mm_grad_x");
-    return wrap(std::move(out));
+    return written(std::move(out), a[3]);
 }
 
 PyObject *group_mm(Args a) { return product<MM>(a, true); }
@@ -354,7 +369,7 @@ PyObject *group_mm_grad_w(Args a)            // dy, x, offsets, out, out_dtype, 
                                                    x.ld, type_code(xt.scalar_type(), "x"), o.p, o.ld, o.stride,
                                                    type_code(type, "out"), accumulate, at.status(), at.stream),
           "group_mm_grad_w");
-    return wrap(std::move(out));
+    return written(std::move(out), a[3]);
 }
 
 PyObject *glu_dropout(Args a)                // gu, p, seed, offset, act, situ_beta, situ_linear_beta, out
@@ -371,7 +386,7 @@ PyObject *glu_dropout(Args a)                // gu, p, seed, offset, act, situ_b
     check(entry<GLU>(&k3moe_glu_dropout)(gu.p, gu.ld, (int)gu.n, (int)(gu.width / 2), type_code(gt.scalar_type(), "gu"), act,
                                          beta, linear, r.p, r.seed, r.offset, o.p, o.ld, at.stream),
           "glu_dropout");
-    return wrap(std::move(out));
+    return written(std::move(out), a[7]);
 }
 
 PyObject *glu_dropout_grad(Args a)           // da, gu, p, seed, offset, act, situ_beta, situ_linear_beta, out
@@ -391,7 +406,7 @@ PyObject *glu_dropout_grad(Args a)           // da, gu, p, seed, offset, act, si
                                                    type_code(gt.scalar_type(), "gu"), act, beta, linear, r.p, r.seed,
                                                    r.offset, o.p, o.ld, at.stream),
           "glu_dropout_grad");
-    return wrap(std::move(out));
+    return written(std::move(out), a[8]);
 }
 
 PyObject *dropout(Args a)                    // x, p, seed, offset, residual, out
@@ -407,7 +422,7 @@ PyObject *dropout(Args a)                    // x, p, seed, offset, residual, ou
     check(entry<DROPOUT>(&k3moe_dropout)(xt.data_ptr(), rp, xt.numel(), type_code(xt.scalar_type(), "x"), r.p, r.seed,
                                          r.offset, op, at.stream),
           "dropout");
-    return wrap(std::move(out));
+    return written(std::move(out), a[5]);
 }
 
 // No C++ exception leaves a call: refusals become the error class, others a RuntimeError.

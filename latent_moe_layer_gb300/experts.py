@@ -3,7 +3,9 @@ and k3moe_dropout calls of include/k3moe.h): tensors in, tensors out, argument m
 csrc/experts_py.cpp).
 
 Tensors live on one CUDA device; matrices have contiguous rows (any row stride).  Work is enqueued on
-`stream` (default: the current stream), and results are allocated there.  Argument errors raise K3Error;
+`stream` (default: the current stream), and results are allocated there.  Nothing is recorded for autograd: a
+tensor that requires gradients is refused unless gradients are off (torch.no_grad, or inside an autograd
+function); a given `out` counts as written in place.  Argument errors raise K3Error;
 errors found on the device (row offsets out of range, a wait that ran out) are kept in a status word
 per device, read by `status()`.
 """
