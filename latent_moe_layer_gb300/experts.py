@@ -53,7 +53,10 @@ def _new_status(dev):
 def status(device=None):
     """Synchronise the device, then read and clear its status word: 0 or the first device-side error
     (a K3MOE_ERR_* code) of these calls since the last read."""
-    dev = torch.cuda.current_device() if device is None else torch.device(device).index or 0
+    device = torch.device("cuda") if device is None else torch.device(device)
+    if device.type != "cuda":
+        raise K3Error(ERR_CODE["ARG"], "device: a CUDA device")
+    dev = torch.cuda.current_device() if device.index is None else device.index
     if dev not in _status:
         return 0
     torch.cuda.synchronize(dev)
@@ -66,10 +69,12 @@ def status(device=None):
 
 
 def _call(name, stream, *args):
-    """A native call, with `stream` (if given) as the current stream of its device."""
+    """A native call, with `stream` (if given) as the current stream of its device, which is the first tensor's."""
     fn = getattr(_native or native(), name)
     if stream is None:
         return fn(*args)
+    if getattr(args[0], "device", stream.device) != stream.device:
+        raise K3Error(ERR_CODE["ARG"], "stream: one of the tensors' device")
     with torch.cuda.stream(stream):
         return fn(*args)
 

@@ -27,3 +27,35 @@ def test_a_tensor_that_needs_gradients_is_refused_not_left_out():
         with torch.no_grad(), pytest.raises(K3Error) as err:      # then only the device is wrong
             call()
         assert err.value.code == ERR_CODE["ARG"]
+
+
+class _Elsewhere:
+    """Stands in for a tensor or a stream of a device, of which this machine may have none."""
+    def __init__(self, device):
+        self.device = torch.device(device)
+
+
+def test_a_stream_of_another_device_is_refused_not_ignored(monkeypatch):
+    ran = []
+    monkeypatch.setattr(ex, "_native", type("native", (), {"dropout": staticmethod(lambda *a: ran.append(a))}))
+    monkeypatch.setattr(torch.cuda, "stream", lambda s: torch.no_grad())         # any context manager
+    with pytest.raises(K3Error) as err:
+        ex.dropout(_Elsewhere("cuda:0"), 0.1, 1, 2, stream=_Elsewhere("cuda:1"))
+    assert err.value.code == ERR_CODE["ARG"] and "stream" in str(err.value) and not ran
+    ex.dropout(_Elsewhere("cuda:1"), 0.1, 1, 2, stream=_Elsewhere("cuda:1"))
+    ex.dropout(_Elsewhere("cuda:0"), 0.1, 1, 2)
+    assert len(ran) == 2
+
+
+def test_status_reads_the_current_device_unless_told_another(monkeypatch):
+    words = {d: torch.tensor([-10 - d, 0, 0, 0], dtype=torch.int32) for d in (0, 1)}
+    monkeypatch.setattr(ex, "_status", dict(words))
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 1)
+    monkeypatch.setattr(torch.cuda, "synchronize", lambda dev=None: None)
+    assert ex.status("cuda") == -11 and ex.status() == 0 and int(words[0][0]) == -10
+    words[1][0] = -11
+    assert ex.status(torch.device("cuda")) == -11
+    assert ex.status("cuda:0") == -10 and ex.status(0) == 0 and ex.status("cuda:7") == 0
+    with pytest.raises(K3Error) as err:
+        ex.status("cpu")
+    assert err.value.code == ERR_CODE["ARG"]
