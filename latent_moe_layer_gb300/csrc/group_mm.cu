@@ -176,6 +176,7 @@ static int group_check(const K3Group &g, int mode)
     if (g.E > K3MOE_TRAIN_MAX_EXPERTS) return K3MOE_ERR_SHAPE;
     if (g.dtype != K3MOE_TYPE_BF16 && g.dtype != K3MOE_TYPE_F16) return K3MOE_ERR_UNSUPPORTED;
     if (g.out_dtype != g.dtype && g.out_dtype != K3MOE_TYPE_F32) return K3MOE_ERR_UNSUPPORTED;
+    const size_t noff = sizeof(int32_t) * ((size_t)g.E + 1);
     if (mode == K3_GROUP_GRAD_W) {
         if (!g.out || (g.rows > 0 && (!g.a || !g.b))) return K3MOE_ERR_ARG;
         if (g.accumulate != 0 && g.accumulate != 1) return K3MOE_ERR_ARG;
@@ -184,7 +185,7 @@ static int group_check(const K3Group &g, int mode)
         if (g.E > 1 && g.stride_o < (int64_t)(g.n_out - 1) * g.ldo + g.n_in) return K3MOE_ERR_ARG;
         const size_t no = k3_span(1, (g.E - 1) * g.stride_o + (int64_t)(g.n_out - 1) * g.ldo + g.n_in, 0, g.out_dtype);
         if (k3_overlap(g.out, no, g.a, k3_span(g.rows, g.n_out, g.lda, g.dtype)) ||
-            k3_overlap(g.out, no, g.b, k3_span(g.rows, g.n_in, g.ldb, g.dtype)))
+            k3_overlap(g.out, no, g.b, k3_span(g.rows, g.n_in, g.ldb, g.dtype)) || k3_overlap(g.out, no, g.offsets, noff))
             return K3MOE_ERR_ALIAS;
         return K3MOE_OK;
     }
@@ -194,7 +195,8 @@ static int group_check(const K3Group &g, int mode)
     if (g.E > 1 && g.stride_b < 0) return K3MOE_ERR_ARG;      // 0: one weight for all groups
     const size_t no = k3_span(g.rows, out, g.ldo, g.out_dtype);
     const size_t nw = k3_span(1, (g.E - 1) * g.stride_b + (int64_t)(g.n_out - 1) * g.ldb + g.n_in, 0, g.dtype);
-    if (k3_overlap(g.out, no, g.a, k3_span(g.rows, in, g.lda, g.dtype)) || k3_overlap(g.out, no, g.b, nw))
+    if (k3_overlap(g.out, no, g.a, k3_span(g.rows, in, g.lda, g.dtype)) || k3_overlap(g.out, no, g.b, nw) ||
+        k3_overlap(g.out, no, g.offsets, noff))
         return K3MOE_ERR_ALIAS;
     return g.rows == 0 ? 1 : K3MOE_OK;
 }

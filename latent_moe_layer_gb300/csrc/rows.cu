@@ -349,7 +349,9 @@ extern "C" int k3moe_rows_plan(const int32_t *idx, int T, int K, int first_exper
     if ((uintptr_t)workspace & 3) return K3MOE_ERR_ALIGN;
     const int64_t n = (int64_t)T * K, per = plan_per(n);
     const size_t nb = (size_t)n * 4, no = sizeof(int32_t) * ((size_t)n_experts + 1);
-    if (k3_overlap(idx, nb, pos, nb) || k3_overlap(idx, nb, offsets, no) || k3_overlap(pos, nb, offsets, no))
+    const size_t nw = k3moe_rows_plan_workspace_bytes(T, K, n_experts);
+    if (k3_overlap(idx, nb, pos, nb) || k3_overlap(idx, nb, offsets, no) || k3_overlap(pos, nb, offsets, no) ||
+        k3_overlap(workspace, nw, idx, nb) || k3_overlap(workspace, nw, pos, nb) || k3_overlap(workspace, nw, offsets, no))
         return K3MOE_ERR_ALIAS;
     const int blocks = n > 0 ? (int)((n + per - 1) / per) : 1;
     int32_t *counts = blocks > 1 ? static_cast<int32_t *>(workspace) : nullptr;
@@ -392,7 +394,8 @@ extern "C" int k3moe_rows_gather(const void *x, int64_t ldx, const int32_t *pos,
     if (rc) return rc;
     if (T > 0 && (!x || !pos || !status || (n_rows > 0 && !out))) return K3MOE_ERR_ARG;
     if (ldx < D || ldo < D) return K3MOE_ERR_ARG;
-    if (k3_overlap(out, k3_span(n_rows, D, ldo, dtype), x, k3_span(T, D, ldx, dtype))) return K3MOE_ERR_ALIAS;
+    const size_t no = k3_span(n_rows, D, ldo, dtype);
+    if (k3_overlap(out, no, x, k3_span(T, D, ldx, dtype)) || k3_overlap(out, no, pos, (size_t)T * K * 4)) return K3MOE_ERR_ALIAS;
     if (T == 0) return K3MOE_OK;
     const int sms = k3_num_sms();
     if (!sms) return K3MOE_ERR_CUDA;
@@ -416,7 +419,9 @@ extern "C" int k3moe_rows_combine(const void *y, int64_t ldy, int n_rows, const 
     if (rc) return rc;
     if (T > 0 && (!z || !pos || !status || (n_rows > 0 && !y))) return K3MOE_ERR_ARG;
     if (ldy < D || ldz < D) return K3MOE_ERR_ARG;
-    if (k3_overlap(z, k3_span(T, D, ldz, dtype), y, k3_span(n_rows, D, ldy, dtype))) return K3MOE_ERR_ALIAS;
+    const size_t nz = k3_span(T, D, ldz, dtype), nt = (size_t)T * K * 4;
+    if (k3_overlap(z, nz, y, k3_span(n_rows, D, ldy, dtype)) || k3_overlap(z, nz, pos, nt) || k3_overlap(z, nz, weights, weights ? nt : 0))
+        return K3MOE_ERR_ALIAS;
     if (T == 0) return K3MOE_OK;
     const int sms = k3_num_sms();
     if (!sms) return K3MOE_ERR_CUDA;
@@ -442,10 +447,12 @@ extern "C" int k3moe_rows_combine_grad(const void *dz, int64_t lddz, const void 
     if (rc) return rc;
     if (T > 0 && (!dz || !pos || !weights || !dweights || !status || (n_rows > 0 && (!y || !dy)))) return K3MOE_ERR_ARG;
     if (lddz < D || ldy < D || lddy < D) return K3MOE_ERR_ARG;
-    const size_t ny = k3_span(n_rows, D, lddy, dtype), nt = (size_t)T * K * 4;
+    const size_t ndy = k3_span(n_rows, D, lddy, dtype), ny = k3_span(n_rows, D, ldy, dtype), nz = k3_span(T, D, lddz, dtype);
+    const size_t nt = (size_t)T * K * 4;
     const bool in_place = dy == y && lddy == ldy;
-    if (k3_overlap(dy, ny, dz, k3_span(T, D, lddz, dtype)) || k3_overlap(dweights, nt, weights, nt) ||
-        (!in_place && k3_overlap(dy, ny, y, k3_span(n_rows, D, ldy, dtype))))
+    if (k3_overlap(dy, ndy, dz, nz) || (!in_place && k3_overlap(dy, ndy, y, ny)) || k3_overlap(dy, ndy, pos, nt) ||
+        k3_overlap(dy, ndy, weights, nt) || k3_overlap(dweights, nt, dy, ndy) || k3_overlap(dweights, nt, dz, nz) ||
+        k3_overlap(dweights, nt, y, ny) || k3_overlap(dweights, nt, pos, nt) || k3_overlap(dweights, nt, weights, nt))
         return K3MOE_ERR_ALIAS;
     if (T == 0) return K3MOE_OK;
     const bool vec = D % 8 == 0 && k3_rows16(dz, lddz, dtype) && k3_rows16(y, ldy, dtype) && k3_rows16(dy, lddy, dtype);
