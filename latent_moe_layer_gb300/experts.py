@@ -17,6 +17,7 @@ import os
 
 import torch
 
+from . import build
 from .k3moe import ERR_CODE, EXPORTS, K3Error, lib
 
 _status = {}
@@ -30,6 +31,8 @@ def native():
         path = os.path.join(os.path.dirname(os.path.abspath(__file__)), "_experts.so")
         if not os.path.exists(path):
             raise ImportError(f"{path} is missing: run __graft_entry__.build() (python latent_moe_layer_gb300/build.py)")
+        if not build.binding_matches():
+            raise ImportError(f"{path} was built against another Python or PyTorch: build it again")
         spec = importlib.util.spec_from_file_location(__package__ + "._experts", path)
         mod = importlib.util.module_from_spec(spec)
         spec.loader.exec_module(mod)
