@@ -385,7 +385,8 @@ int k3moe_rows_combine(const void *y, int64_t ldy, int n_rows, const int32_t *po
                        int D, int dtype, void *z, int64_t ldz, int32_t *status, cudaStream_t stream);
 
 /* Gradient of rows_combine: dy[pos[t][k]] = weights[t][k] dz[t] and dweights[t][k] = <dz[t], y[pos[t][k]]>
- * (0 where pos < 0).  dy may be y itself (the same pointer and ldy). */
+ * (0 where pos < 0); rows of dy that no pair names are left as they are.  dy may be y itself (the same pointer
+ * and ldy). */
 int k3moe_rows_combine_grad(const void *dz, int64_t lddz, const void *y, int64_t ldy, int n_rows, const int32_t *pos,
                             const float *weights, int T, int K, int D, int dtype, void *dy, int64_t lddy,
                             float *dweights, int32_t *status, cudaStream_t stream);

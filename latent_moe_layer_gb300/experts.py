@@ -103,7 +103,8 @@ def combine_rows(y, pos, weights=None, out=None, stream=None):
 
 
 def combine_rows_grad(dz, y, pos, weights, out=None, stream=None):
-    """Gradient of combine_rows: (dy [rows of y, D], dweights [T, K] fp32).  `out` receives dy and may be y."""
+    """Gradient of combine_rows: (dy [rows of y, D], dweights [T, K] fp32).  `out` receives dy and may be y; rows that no
+    pair names are left as they are (uninitialised in a new `out`)."""
     return _call("combine_rows_grad", stream, dz, y, pos, weights, out)
 
 
