@@ -40,9 +40,9 @@ constexpr int GT_A_BYTES = 128 * GT_BK * 2, GT_STAGE = 2 * GT_A_BYTES;
 // contraction value in bf16 and 6.3e-9 in f16, whose products have more bits (products of random sign 1.2e-9).  grad_w,
 // and mm and grad_x with an fp32 output, therefore add up parts of 512 (f16: 256) values in fp32 registers: an error of
 // 1.7e-6 of the sum at any length.  mm and grad_x with a 16-bit output do so from GT_LONG values on: below, the loss is at
-// most 1/9 of the f16 output's own half unit in the last place (bf16: 1/100).  Parts cost fp32 outputs 2-12 % in bf16
-// (2,047 rows over 14 experts, 3584 to 3584: 71 -> 73 us; 16,384 over 112, 3584 to 6144: 820 -> 845), for 16-bit ones it
-// would be 67 -> 72 and 792 -> 824 us; parts of 256 8192^3 568 -> 755 us against 606 with 512.
+// most 1/9 of the f16 output's own half unit in the last place (bf16: 1/100).  Parts cost fp32 outputs 1-11 % in bf16
+// (2,047 rows over 14 experts, 3584 to 3584: 71 -> 73 us; 16,384 over 112, 3584 to 6144: 820 -> 845); for 16-bit ones it
+// would be 67 -> 71 and 792 -> 819 us, and in f16 60 -> 82.
 constexpr int GT_PART_BF16 = 3, GT_PART_F16 = 2;                        // log2 of a part's stages
 constexpr int GT_LONG = 8192;
 // mm, grad_x: bytes of activation rows whose tiles pass under one block of weights before the next block
@@ -177,7 +177,8 @@ __device__ __forceinline__ void load_rows(const CUtensorMap *maps, uint32_t dst,
     }
 }
 
-// (a, b) += (c, d), both sums in one instruction
+// (a, b) += (c, d), both sums in one instruction.  Sums that begin at zero and take a part in eight columns at a time leave
+// no register spilled, which the issuing loop would pay (251 rows over 112 experts, fp32 output: 745 us with 16, 734 with 8).
 __device__ __forceinline__ void add2(float &a, float &b, uint32_t c, uint32_t d)
 {
     asm("{\n\t.reg .b64 x, y;\n\tmov.b64 x, {%0, %1};\n\tmov.b64 y, {%2, %3};\n\tadd.rn.f32x2 x, x, y;\n\t"
@@ -526,7 +527,7 @@ __global__ void __launch_bounds__(GroupSmem<MODE, FOLD>::THREADS, 1)
                 const int s0 = first_stage(j), s1 = end_stage(j);
                 const int chunks = parts(s0, s1);
                 if (j.steps == 0 && args.accumulate) continue;           // an expert without rows: nothing, or zeros
-                float sum[COLS];
+                float sum[COLS] = {};
                 for (int ch = 0; ch < chunks; ++ch) {
                     ok = pair_wait(smem_u32(tfull + acc.slot), acc.phase, abort_flag, args.status, 66);
                     if (!ok) break;
@@ -538,8 +539,7 @@ __global__ void __launch_bounds__(GroupSmem<MODE, FOLD>::THREADS, 1)
                         tmem_ld8(tbase + acc.slot * GT_TILE_N + part * COLS + 8 * g, v);
                         tc_wait_ld();
 #pragma unroll
-                        for (int i = 0; i < 8; ++i)
-                            sum[8 * g + i] = (ch ? sum[8 * g + i] : 0.f) + __uint_as_float(v[i]);
+                        for (int i = 0; i < 8; i += 2) add2(sum[8 * g + i], sum[8 * g + i + 1], v[i], v[i + 1]);
                     }
                     tc_fence_before();
                     __syncwarp();
@@ -579,11 +579,14 @@ __global__ void __launch_bounds__(GroupSmem<MODE, FOLD>::THREADS, 1)
                     for (int g = 0; g < COLS / 16; ++g) {
                         const int c = 16 * (part + PARTS * g);
                         if (c >= j.n) break;
-                        uint32_t v[16];
-                        tmem_ld16(tbase + acc.slot * GT_TILE_N + c, v);
-                        tc_wait_ld();
 #pragma unroll
-                        for (int i = 0; i < 16; i += 2) add2(sum[16 * g + i], sum[16 * g + i + 1], v[i], v[i + 1]);
+                        for (int h = 0; h < 16; h += 8) {
+                            uint32_t v[8];
+                            tmem_ld8(tbase + acc.slot * GT_TILE_N + c + h, v);
+                            tc_wait_ld();
+#pragma unroll
+                            for (int i = 0; i < 8; i += 2) add2(sum[16 * g + h + i], sum[16 * g + h + i + 1], v[i], v[i + 1]);
+                        }
                     }
                     tc_fence_before();
                     __syncwarp();
