@@ -1,7 +1,8 @@
 // Python binding of the expert training operators: tensors in, tensors out.  It only checks and marshals
 // arguments and allocates results (PyTorch's allocator, on the current stream); the work is the library's, whose
 // entry points are handed over by address.  Native because a call's host time is what a decode-size step waits
-// for: a dropout takes 3.8 us through here, 8.4 us through Python and ctypes, 3 us of either the library's.
+// for: a dropout takes 2.3 us through here (3.8 with a new output), 8.4 us through Python and ctypes, 2 to 3 us of
+// either the library's.
 #include <Python.h>
 
 #include <ATen/core/grad_mode.h>

@@ -71,7 +71,7 @@ __device__ __forceinline__ float kept(float v, uint32_t word, const DropArgs &a)
 // With the generator a 16-bit piece costs about as much computing as HBM takes for its bytes, and warps that
 // load, then compute, spend the sum of the two.  So there (RING) each thread copies its next piece of 16 bytes
 // an input into shared memory ahead (cp.async; its own slots, so nothing is synchronised), which costs no
-// registers: 58.7 M bf16 elements 72 -> 58 us.  Without the generator, and for fp32, direct loads are 3-5 %
+// registers: 58.7 M bf16 elements take a fifth less.  Without the generator, and for fp32, direct loads are 3-5 %
 // faster (its computing hides behind the bytes).
 constexpr int PIPE = 2, PIPE_THREADS = 256;
 
@@ -131,8 +131,8 @@ __device__ __forceinline__ void for_pieces(int64_t i0, int64_t step, int64_t tot
 }
 
 // ------------------------------------------------------------------ dropout with residual
-// 58.7 M fp32 elements with a residual in 108 us (6.5 TB/s, HBM binds); in bf16 60 us (5.9 TB/s) and 53 us
-// without the residual (4.4 TB/s: the generator binds).
+// 58.7 M fp32 elements with a residual in 107 us (6.6 TB/s, HBM binds); in bf16 55 us (6.4 TB/s) and 52 us
+// without the residual (4.5 TB/s: the generator binds).
 template <class T, int V, bool DROP, bool RES>
 __global__ void __launch_bounds__(PIPE_THREADS) dropout_kernel(const T *x, const T *res, int64_t n, const DropArgs a,
                                                                T *out)
@@ -286,7 +286,7 @@ __device__ __forceinline__ void glu_two(F2 g, F2 u, F2 t, const GluArgs &c, F2 &
         nu = mul2(nu, u);
         const F2 ds = one_plus_exp_neg<0>(g);
         if (GRAD) {
-            // a reciprocal each: the pipe of products binds (32,768 x 3072: 185 us, 197 with one of the product)
+            // a reciprocal each: the pipe of products binds (one reciprocal of the product: 6 % more time)
             // da/dg = h s (f (1 - s) + 1 - (f / beta)^2), da/du = s f (1 - (h / linear_beta)^2)
             const F2 s = rcp2(ds), f = mul2(ng, rcp2(dg)), h = mul2(nu, rcp2(du)), st = mul2(s, t);
             o0 = mul2(mul2(h, st), fma2(f, fma2(f, f2(c.g.neg_inv2), fma2(s, neg, one)), one));
@@ -509,7 +509,7 @@ static void launch_glu(const void *da, int64_t ldda, const void *gu, int64_t ldg
             GluWalk walk;
             walk.nv = width / V;
             // SiLU's gradient with the generator is bound by HBM, which serves long runs of its five streams better from
-            // fewer CTAs: 158 us with 2 an SM, 168 with 3, 173 with 4 (32,768 x 3072), but 33 against 31 us at 5,003 rows
+            // fewer CTAs: 152 us with 2 an SM, 187 with 3 (32,768 x 3072); at 5,003 rows all that fit are 6 % faster
             constexpr int FEW = GRAD && V == 8 && decltype(drop)::value && ACT == K3MOE_ACT_SILU ? 2 : 32;
             const unsigned grid = resident_grid(kern, (int64_t)rows * walk.nv, sms, fit, FEW);
             const int64_t step = (int64_t)grid * PIPE_THREADS, row_step = step / walk.nv;

@@ -12,7 +12,7 @@ namespace k3 {
 // the 32 warps numbers 64 consecutive pairs against its own counters, in two rounds of 32 in which
 // lanes of the same expert find each other by match_any, and a scan over the warps' counters joins
 // them.  Order is by pair alone, no atomics decide it.  Bound by latency: 16 x 16 pairs over 896 experts
-// 3.8 us (one launch), 8192 x 16 pairs 9.9 us.
+// 4.2 us (one launch), 8192 x 16 pairs 10.2 us.
 constexpr int PLAN_THREADS = 1024, PLAN_SUB = 2048, PLAN_BLOCKS = 128;
 
 __device__ __forceinline__ int plan_expert(const int32_t *idx, int64_t p, int64_t n, int first, int E)
@@ -136,7 +136,7 @@ __global__ void __launch_bounds__(PLAN_THREADS) plan_place_kernel(const int32_t 
 
 // ------------------------------------------------------------------ gather
 // A CTA per token reads its row once and writes its K copies.  HBM writes bind it: 4096 x 16 rows of 3584
-// bf16 take 80 us, 6.2 TB/s.
+// bf16 take 79 us, 6.3 TB/s.
 template <class T, int V>
 __global__ void __launch_bounds__(256) rows_gather_kernel(const T *__restrict__ x, int64_t ldx,
                                                           const int32_t *__restrict__ pos, int T_, int K, int nv,
@@ -165,7 +165,7 @@ __global__ void __launch_bounds__(256) rows_gather_kernel(const T *__restrict__ 
 // `split` warps per token, each with every split-th piece of 32 V columns, so that nothing but memory keeps a
 // warp waiting: its lanes hold the token's rows and weights (32 at a time), and only rows that exist are
 // loaded, eight in flight, summed in k order.  Reads of 512 bytes here and there bind it: 4096 x 16 rows of
-// 3584 in 90 us, 5.5 TB/s; 16 tokens 2.8 us.
+// 3584 in 82 us, 6.1 TB/s (half of them missing 48 us, 5.5 TB/s); 16 tokens 3.2 us.
 template <class T, int V>
 __global__ void __launch_bounds__(256, 4) rows_combine_kernel(const T *__restrict__ y, int64_t ldy, int n_rows,
                                                            const int32_t *__restrict__ pos,
@@ -430,7 +430,7 @@ extern "C" int k3moe_rows_combine(const void *y, int64_t ldy, int n_rows, const 
         using Ty = decltype(t);
         constexpr int V = decltype(v)::value;
         const int nv = D / V;
-        // about four rounds of the 32 or so warps an SM holds (4096 tokens: 95 us, with one round 103)
+        // about four rounds of the 32 or so warps an SM holds (with one round 4096 tokens took 8 % longer)
         const int pieces = (nv + 31) / 32, split = (int)std::min<int64_t>(pieces, (128LL * sms + T - 1) / T);
         k3_launch(rows_combine_kernel<Ty, V>, (unsigned)std::min<int64_t>(((int64_t)T * split + 7) / 8, 1 << 20), 256, 0,
                   st, (const Ty *)y, ldy, n_rows, pos, weights, T, K, nv, split, (Ty *)z, ldz, status);
@@ -460,7 +460,7 @@ extern "C" int k3moe_rows_combine_grad(const void *dz, int64_t lddz, const void 
         using Ty = decltype(t);
         constexpr int V = decltype(v)::value;
         // few tokens: a CTA for every eight pairs (16 tokens 7.0 -> 4.0 us); many: one for all of a token's
-        // (4096 tokens 167 us against 180; three CTAs an SM by registers, 154 us, against 177 with two)
+        // (4096 tokens: 7 % less; three CTAs an SM by registers: 13 % less than two)
         const int nv = D / V, ky = T < 4 * k3_num_sms() ? std::min(65535, (K + 7) / 8) : 1;
         k3_launch(rows_combine_grad_kernel<Ty, V>, dim3(T, ky), row_threads(nv), 0, st, (const Ty *)dz, lddz, (const Ty *)y, ldy,
                   n_rows, pos, weights, T, K, nv, (Ty *)dy, lddy, dweights, status);
