@@ -416,7 +416,7 @@ int k3moe_group_mm_grad_w(const int32_t *offsets, int n_experts, int rows, int n
  * elements are multiplied by 1 / (1 - p).  0 <= p < 1; p = 0 keeps all. */
 
 /* a[r][c] = dropout(act(g, u)) with g = gu[r][c], u = gu[r][width + c].  gu [rows, 2 width], a [rows,
- * width]; act K3MOE_ACT_*, betas as in k3moe_config (<= 0: 4 and 25).  F16 or BF16.  SiLU of a gate below
+ * width]; act K3MOE_ACT_*, betas as in k3moe_config (<= 0: 4 and 25; else 2^-126 to 2^126).  F16 or BF16.  SiLU of a gate below
  * -94.2 is 0. */
 int k3moe_glu_dropout(const void *gu, int64_t ldgu, int rows, int width, int dtype, int act, float situ_beta,
                       float situ_linear_beta, double p, uint64_t seed, uint64_t offset, void *a, int64_t lda,

@@ -546,7 +546,9 @@ static int glu_run(const void *da, int64_t ldda, const void *gu, int64_t ldgu, i
     if (rows > 0 && (!gu || !out || (GRAD && !da))) return K3MOE_ERR_ARG;
     if (ldgu < 2 * (int64_t)width || ldo < (GRAD ? 2 : 1) * (int64_t)width || (GRAD && ldda < width)) return K3MOE_ERR_ARG;
     if (act != K3MOE_ACT_SILU && act != K3MOE_ACT_SITU) return K3MOE_ERR_UNSUPPORTED;
-    if (beta != beta || linear_beta != linear_beta) return K3MOE_ERR_ARG;
+    // limits (0 and below: the defaults) whose reciprocal is a finite number that is not zero; NaN is neither
+    for (const float limit : {beta, linear_beta})
+        if (!(limit <= 0.f || (limit >= 0x1p-126f && limit <= 0x1p126f))) return K3MOE_ERR_ARG;
     if (dtype != K3MOE_TYPE_BF16 && dtype != K3MOE_TYPE_F16) return K3MOE_ERR_UNSUPPORTED;
     const size_t ngu = k3_span(rows, 2 * (int64_t)width, ldgu, dtype);
     const size_t no = k3_span(rows, (GRAD ? 2 : 1) * (int64_t)width, ldo, dtype);

@@ -59,3 +59,14 @@ def test_status_reads_the_current_device_unless_told_another(monkeypatch):
     with pytest.raises(K3Error) as err:
         ex.status("cpu")
     assert err.value.code == ERR_CODE["ARG"]
+
+
+def test_soft_limits_without_a_finite_reciprocal_are_refused():
+    from latent_moe_layer_gb300 import k3moe
+    lib, far = k3moe.lib(), [1 << 40, 2 << 40, 3 << 40]                # addresses that a refused call never touches
+    inf = float("inf")
+    for b, lb in ((inf, 25.0), (4.0, inf), (1e-39, 25.0), (4.0, 1e-45), (3e38, 25.0), (float("nan"), 25.0), (4.0, float("nan"))):
+        assert lib.k3moe_glu_dropout(far[0], 64, 4, 32, 1, 1, b, lb, 0.1, 1, 2, far[1], 32, None) == ERR_CODE["ARG"]
+        assert lib.k3moe_glu_dropout_grad(far[2], 32, far[0], 64, 4, 32, 1, 1, b, lb, 0.1, 1, 2, far[1], 64, None) == ERR_CODE["ARG"]
+    for b, lb in ((0.0, -1.0), (-inf, 25.0), (2.0 ** -126, 2.0 ** 126)):
+        assert lib.k3moe_glu_dropout(None, 64, 0, 32, 1, 1, b, lb, 0.1, 1, 2, None, 32, None) == 0
