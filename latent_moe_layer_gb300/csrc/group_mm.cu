@@ -33,7 +33,7 @@ __device__ __forceinline__ void load_blocks(uint32_t (&r)[4], const void *row)
 
 // 64 x 64 outputs per CTA, 32 x 16 a warp, the contraction in steps of 32 through shared memory; the next step's
 // values are in flight meanwhile, one element a load, so any size, stride and alignment goes.  Those loads bind it:
-// 4,099 rows over 8 experts, 1001 to 2003: 267 us, 62 TFLOP/s (fp32 sums on the CUDA cores: 820); the gradients 281 and 316.
+// 4,099 rows over 8 experts, 1001 to 2003: 260 us, 63 TFLOP/s (fp32 sums on the CUDA cores: 820); the gradients 312 and 309.
 // Tile rows x are output rows (tokens' rows; n_out for grad_w), columns y the output's contiguous axis.
 template <int MODE, class T, class O>
 __global__ void __launch_bounds__(GG_THREADS, 3) group_generic_kernel(const K3Group g)
