@@ -431,6 +431,74 @@ int k3moe_glu_dropout_grad(const void *da, int64_t ldda, const void *gu, int64_t
 int k3moe_dropout(const void *x, const void *residual, int64_t n, int dtype, double p, uint64_t seed, uint64_t offset,
                   void *out, cudaStream_t stream);
 
+/* Products of 8-bit operands with a scale for each block of 128.  A code is an OCP E4M3 or E5M2 number (K3MOE_F8_*), a scale
+ * the E8M0 byte k + 127 of 2^k; the value is code * 2^k.  k is the smallest from -127 up with the block's largest finite
+ * size <= 2^k times the format's largest number (448, 57344), so nothing saturates; values are rounded to nearest even.  A
+ * value that is not finite takes no part in the scale and becomes NaN (E5M2 keeps infinities). */
+#define K3MOE_F8_E4M3 0
+#define K3MOE_F8_E5M2 1
+/* Rows x [rows, n], a scale for each 128 columns: codes [rows, n] with row stride ldc bytes, scales [rows, ceil(n / 128)]
+ * with row stride lds.  F16 or BF16. */
+int k3moe_quant8_rows(const void *x, int64_t ldx, int rows, int n, int dtype, int kind, uint8_t *codes, int64_t ldc,
+                      uint8_t *scales, int64_t lds, cudaStream_t stream);
+/* Weights w [n_experts][n_out][n_in], a scale for each 128 x 128 block: scales [n_experts][ceil(n_out / 128)][ceil(n_in / 128)],
+ * contiguous; codes [n_experts][n_out][n_in] with row stride ldc and expert stride stride_c, and, where codes_t is given, the
+ * same codes as [n_experts][n_in][n_out] (row stride ldt, expert stride stride_t), whose scales are the transposed ones. */
+int k3moe_quant8_weights(const void *w, int64_t ldw, int64_t stride_w, int n_experts, int n_out, int n_in, int dtype, int kind,
+                         uint8_t *codes, int64_t ldc, int64_t stride_c, uint8_t *codes_t, int64_t ldt, int64_t stride_t,
+                         uint8_t *scales, cudaStream_t stream);
+/* y[r] = W_e x[r] for the rows of every expert, as group_mm: x codes [rows, n_in] with scales [rows, ceil(n_in / 128)] (row
+ * stride ldxs), w codes [n_experts][n_out][n_in] with scale (e, i, j) at w_scales[e sse + i sso + j ssi] (the transposed codes
+ * and scales of quant8_weights give the gradient for the rows).  Codes start on 16-byte boundaries (pointers, row and
+ * expert strides), x scales on 4-byte ones.  out_dtype F32, F16 or BF16.  Products are exact, each block of 32 is scaled by
+ * the tensor cores and added in fp32 with truncation (errors as of the products above). */
+int k3moe_group_mm8(const int32_t *offsets, int n_experts, int rows, int n_in, int n_out, const uint8_t *x, int64_t ldx,
+                    int x_kind, const uint8_t *x_scales, int64_t ldxs, const uint8_t *w, int64_t ldw, int64_t stride_w,
+                    int w_kind, const uint8_t *w_scales, int64_t sse, int64_t sso, int64_t ssi, void *y, int64_t ldy,
+                    int out_dtype, int32_t *status, cudaStream_t stream);
+
+/* The gated block's projections and unit in one pass: a[r] = act(Wg x[r]) * (Wu x[r]) for the rows of every expert, w
+ * [n_experts][2 width][n_in] the gate rows, then the up rows; a [rows, width].  The projections stay in fp32.  act and betas
+ * as for glu_dropout. */
+int k3moe_group_glu(const int32_t *offsets, int n_experts, int rows, int n_in, int width, const void *x, int64_t ldx,
+                    const void *w, int64_t ldw, int64_t stride_w, int dtype, int act, float situ_beta, float situ_linear_beta,
+                    void *a, int64_t lda, int32_t *status, cudaStream_t stream);
+/* The projections' gradient dgu [rows, 2 width] from da [rows, width]; the projections are computed again, so nothing but x
+ * is kept for it.  group_mm_grad_x and _grad_w of dgu give the gradients for x and w. */
+int k3moe_group_glu_grad(const int32_t *offsets, int n_experts, int rows, int n_in, int width, const void *da, int64_t ldda,
+                         const void *x, int64_t ldx, const void *w, int64_t ldw, int64_t stride_w, int dtype, int act,
+                         float situ_beta, float situ_linear_beta, void *dgu, int64_t lddgu, int32_t *status,
+                         cudaStream_t stream);
+
+/* Norms around a block, rs(v) = 1 / sqrt(mean v^2 + eps) over a row of D <= 16384 (eps > 0; squares in fp32):
+ *   rms_norm        out = gain x rs(x)
+ *   norm_residual   h = residual_scale residual + gate (gain y rs(y)),  n = next_gain h rs(h)   (n NULL: h alone)
+ * F32, F16 or BF16 rows; gains [D] of that type or F32 (gain_dtype), NULL for ones; n is computed from the h that is not
+ * rounded yet.  gate by gate_kind: none (NULL), a number for each row (fp32 [rows]) or for each element ([rows, D]).  An
+ * output may be an input of its shape itself (the same pointer and leading dimension), though not another output. */
+#define K3MOE_NORM_MAX_WIDTH 16384
+#define K3MOE_GATE_NONE 0
+#define K3MOE_GATE_ROW  1
+#define K3MOE_GATE_FULL 2
+int k3moe_rms_norm(const void *x, int64_t ldx, const void *gain, int gain_dtype, float eps, int rows, int D, int dtype,
+                   void *out, int64_t ldo, cudaStream_t stream);
+int k3moe_norm_residual(const void *y, int64_t ldy, const void *residual, int64_t ldr, const void *gain, const void *next_gain,
+                        int gain_dtype, const void *gate, int64_t ldgate, int gate_kind, float residual_scale, float eps,
+                        int rows, int D, int dtype, void *h, int64_t ldh, void *n, int64_t ldn, cudaStream_t stream);
+/* Gradients.  rms_norm_grad: dx = [add +] the gradient of rms_norm for x, from dy (add may be NULL: the residual's own path).
+ * norm_residual_grad: from dh and dn (either may be NULL, not both) the gradients for y, residual and gate; h as norm_residual
+ * gave it (not read without dn).  Gains' gradients are fp32 [D] sums over the rows in an order that does not depend on timing
+ * (NULL: not wanted; dnext_gain only with dn).  workspace: k3moe_norm_grad_workspace_bytes(rows, D) bytes. */
+size_t k3moe_norm_grad_workspace_bytes(int rows, int D);
+int k3moe_rms_norm_grad(const void *dy, int64_t lddy, const void *x, int64_t ldx, const void *gain, int gain_dtype,
+                        const void *add, int64_t ldadd, float eps, int rows, int D, int dtype, void *dx, int64_t lddx,
+                        float *dgain, void *workspace, size_t workspace_bytes, cudaStream_t stream);
+int k3moe_norm_residual_grad(const void *dh, int64_t lddh, const void *dn, int64_t lddn, const void *y, int64_t ldy,
+                             const void *h, int64_t ldh, const void *gain, const void *next_gain, int gain_dtype,
+                             const void *gate, int64_t ldgate, int gate_kind, float residual_scale, float eps, int rows, int D,
+                             int dtype, void *dy, int64_t lddy, void *dresidual, int64_t lddr, void *dgate, int64_t lddgate,
+                             float *dgain, float *dnext_gain, void *workspace, size_t workspace_bytes, cudaStream_t stream);
+
 /* ------------------------------------------------------------ profiling
  * Stage timing with CUDA events recorded on the launching stream around each
  * stage of k3moe_forward (a ring of 256 forwards), plus a count of kernel

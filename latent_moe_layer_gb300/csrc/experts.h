@@ -97,8 +97,15 @@ inline bool k3_rows16(const void *p, int64_t ld, int type)
 int k3_num_sms();
 
 // One product grouped by expert.  mm: a = x, out = y; grad_x: a = dy, out = dx; grad_w: a = dy,
-// b = x, out = dw.
-enum K3GroupMode { K3_GROUP_MM = 0, K3_GROUP_GRAD_X = 1, K3_GROUP_GRAD_W = 2 };
+// b = x, out = dw; gated block: a = x, n_out = width, out = a or dgu; mm8: a = x's codes.
+enum K3GroupMode {
+    K3_GROUP_MM = 0,
+    K3_GROUP_GRAD_X = 1,
+    K3_GROUP_GRAD_W = 2,
+    K3_GROUP_GLU = 3,
+    K3_GROUP_GLU_GRAD = 4,
+    K3_GROUP_MM8 = 5
+};
 struct K3Group {
     const int32_t *offsets;
     int E, rows, n_in, n_out;
@@ -115,3 +122,5 @@ int k3_group_generic(int mode, const K3Group &g, cudaStream_t st);
 // Whether the tensor-core kernels take it (every row on a 16-byte boundary), and their launch.
 bool k3_group_tc_fits(int mode, const K3Group &g);
 int k3_group_tc(int mode, const K3Group &g, cudaStream_t st);
+// The argument checks that all products share: sizes, offsets and types; > 0: nothing to do.
+int k3_group_check(const K3Group &g, int mode);

@@ -12,7 +12,9 @@
 #include <torch/csrc/Dtype.h>
 #include <torch/csrc/autograd/python_variable.h>
 
+#include <initializer_list>
 #include <string>
+#include <vector>
 
 #include "k3moe.h"
 
@@ -36,11 +38,14 @@ PyObject *g_error = nullptr;                 // the exception class, called with
 PyObject *g_new_status = nullptr;            // callable: device index -> address of its status word
 int32_t *g_status[64] = {};
 
-enum Entry { PLAN_BYTES, PLAN, GATHER, COMBINE, COMBINE_GRAD, MM, MM_GRAD_X, MM_GRAD_W, GLU, GLU_GRAD, DROPOUT, ENTRIES };
+enum Entry { PLAN_BYTES, PLAN, GATHER, COMBINE, COMBINE_GRAD, MM, MM_GRAD_X, MM_GRAD_W, GLU, GLU_GRAD, DROPOUT, QUANT_ROWS, QUANT_WEIGHTS,
+             MM8, GROUP_GLU, GROUP_GLU_GRAD, RMS_NORM, NORM_RESIDUAL, NORM_BYTES, RMS_NORM_GRAD, NORM_RESIDUAL_GRAD, ENTRIES };
 const char *const ENTRY_NAMES[ENTRIES] = {
     "k3moe_rows_plan_workspace_bytes", "k3moe_rows_plan", "k3moe_rows_gather", "k3moe_rows_combine",
     "k3moe_rows_combine_grad", "k3moe_group_mm", "k3moe_group_mm_grad_x", "k3moe_group_mm_grad_w",
-    "k3moe_glu_dropout", "k3moe_glu_dropout_grad", "k3moe_dropout"};
+    "k3moe_glu_dropout", "k3moe_glu_dropout_grad", "k3moe_dropout", "k3moe_quant8_rows", "k3moe_quant8_weights",
+    "k3moe_group_mm8", "k3moe_group_glu", "k3moe_group_glu_grad", "k3moe_rms_norm", "k3moe_norm_residual",
+    "k3moe_norm_grad_workspace_bytes", "k3moe_rms_norm_grad", "k3moe_norm_residual_grad"};
 void *g_entry[ENTRIES] = {};
 
 template <Entry E, class F>
@@ -236,6 +241,29 @@ PyObject *written(at::Tensor t, PyObject *given)
     return wrap(std::move(t));
 }
 
+// A tuple of tensors, None where there is none.
+PyObject *tuple(std::initializer_list<PyObject *> items)
+{
+    PyObject *t = PyTuple_New((Py_ssize_t)items.size());
+    Py_ssize_t i = 0;
+    bool ok = t != nullptr;
+    for (PyObject *x : items) {
+        ok = ok && x;
+        if (ok) PyTuple_SET_ITEM(t, i, x);
+        else Py_XDECREF(x);
+        ++i;
+    }
+    if (ok) return t;
+    Py_XDECREF(t);
+    return nullptr;
+}
+
+PyObject *none()
+{
+    Py_INCREF(Py_None);
+    return Py_None;
+}
+
 PyObject *pair(PyObject *x, at::Tensor b)
 {
     PyObject *y = x ? wrap(std::move(b)) : nullptr;
@@ -426,6 +454,271 @@ PyObject *dropout(Args a)                    // x, p, seed, offset, residual, ou
     return written(std::move(out), a[5]);
 }
 
+// ---------------------------------------------------------------------------- 8-bit operands
+int kind_code(PyObject *o)
+{
+    if (PyUnicode_Check(o)) {
+        if (PyUnicode_CompareWithASCIIString(o, "e4m3") == 0) return K3MOE_F8_E4M3;
+        if (PyUnicode_CompareWithASCIIString(o, "e5m2") == 0) return K3MOE_F8_E5M2;
+    }
+    refuse("kind: e4m3 or e5m2");
+}
+
+int kind_of(at::ScalarType t, const char *what)
+{
+    if (t == at::kFloat8_e4m3fn) return K3MOE_F8_E4M3;
+    if (t == at::kFloat8_e5m2) return K3MOE_F8_E5M2;
+    refuse(std::string(what) + ": 8-bit codes (float8_e4m3fn, float8_e5m2)", K3MOE_ERR_UNSUPPORTED);
+}
+
+at::ScalarType kind_type(int kind) { return kind == K3MOE_F8_E4M3 ? at::kFloat8_e4m3fn : at::kFloat8_e5m2; }
+
+int64_t up(int64_t n, int64_t to) { return (n + to - 1) / to * to; }
+
+// [..., n] of one-byte elements whose rows start at multiples of `to` bytes.
+at::Tensor padded_rows(std::vector<int64_t> shape, int64_t to, const at::Tensor &like, at::ScalarType type)
+{
+    const int64_t n = shape.back();
+    shape.back() = up(n, to);
+    at::Tensor t = fresh(shape, like, type);
+    return shape.back() == n ? t : t.slice(-1, 0, n);
+}
+
+PyObject *quant8_rows(Args a)                // x, kind
+{
+    const at::Tensor &xt = tensor(a[0], "x");
+    const Place at(xt);
+    const Rows x(xt, at, "x");
+    const int kind = kind_code(a[1]), type = type_code(xt.scalar_type(), "x");
+    need(x.width > 0, "x: [rows, n]");
+    const int64_t blocks = (x.width + 127) / 128;
+    at::Tensor codes = padded_rows({x.n, x.width}, 16, xt, kind_type(kind)), scales = padded_rows({x.n, blocks}, 4, xt, at::kByte);
+    check(entry<QUANT_ROWS>(&k3moe_quant8_rows)(x.p, x.ld, (int)x.n, (int)x.width, type, kind,
+                                                static_cast<uint8_t *>(codes.data_ptr()), up(x.width, 16),
+                                                static_cast<uint8_t *>(scales.data_ptr()), up(blocks, 4), at.stream),
+          "quant8_rows");
+    return pair(wrap(std::move(codes)), std::move(scales));
+}
+
+PyObject *quant8_weights(Args a)             // w, kind, transposed
+{
+    const at::Tensor &wt = tensor(a[0], "w");
+    const Place at(wt);
+    const Matrices w(wt, at, "w");
+    const int kind = kind_code(a[1]), type = type_code(wt.scalar_type(), "w"), transposed = PyObject_IsTrue(a[2]);
+    if (transposed < 0) throw PythonError();
+    need(w.E > 0 && w.rows > 0 && w.cols > 0, "w: [E, n_out, n_in]");
+    at::Tensor codes = padded_rows({w.E, w.rows, w.cols}, 16, wt, kind_type(kind)), t;
+    at::Tensor scales = fresh({w.E, (w.rows + 127) / 128, (w.cols + 127) / 128}, wt, at::kByte);
+    if (transposed) t = padded_rows({w.E, w.cols, w.rows}, 16, wt, kind_type(kind));
+    const int64_t ldc = up(w.cols, 16), ldt = up(w.rows, 16);
+    check(entry<QUANT_WEIGHTS>(&k3moe_quant8_weights)(w.p, w.ld, w.stride, (int)w.E, (int)w.rows, (int)w.cols, type, kind,
+                                                      static_cast<uint8_t *>(codes.data_ptr()), ldc, w.rows * ldc,
+                                                      transposed ? static_cast<uint8_t *>(t.data_ptr()) : nullptr, ldt,
+                                                      w.cols * ldt, static_cast<uint8_t *>(scales.data_ptr()), at.stream),
+          "quant8_weights");
+    if (!transposed) return pair(wrap(std::move(codes)), std::move(scales));
+    return tuple({wrap(std::move(codes)), wrap(std::move(scales)), wrap(std::move(t))});
+}
+
+PyObject *group_mm8(Args a)                  // x, x_scales, w, w_scales, offsets, out, out_dtype
+{
+    const at::Tensor &xt = tensor(a[0], "x"), &st = tensor(a[1], "x_scales"), &wt = tensor(a[2], "w"), &vt = tensor(a[3], "w_scales");
+    const Place at(xt);
+    const Matrices w(wt, at, "w");
+    const Rows x(xt, at, "x", w.cols);
+    const int xk = kind_of(xt.scalar_type(), "x"), wk = kind_of(wt.scalar_type(), "w");
+    const int64_t blocks = (w.cols + 127) / 128, row_blocks = (w.rows + 127) / 128;
+    need(st.scalar_type() == at::kByte && vt.scalar_type() == at::kByte, "scales: uint8 exponents");
+    const Rows xs(st, at, "x_scales", blocks, x.n);
+    if (!at.has(vt) || vt.dim() != 3 || vt.size(0) != w.E || vt.size(1) != row_blocks || vt.size(2) != blocks)
+        refuse("w_scales: [E, ceil(n_out / 128), ceil(n_in / 128)] on the call's device");
+    const int32_t *off = static_cast<int32_t *>(table(tensor(a[4], "offsets"), at, "offsets", at::kInt, {w.E + 1}));
+    const at::Tensor *given = maybe(a[5], "out");
+    const at::ScalarType type = scalar_type(a[6], given ? given->scalar_type() : at::kBFloat16);
+    at::Tensor out = output(a[5], x.n, w.rows, xt, type);
+    const Rows o(out, at, "out", w.rows, x.n);
+    // a matrix of one row has no stride of its own: the next boundary
+    check(entry<MM8>(&k3moe_group_mm8)(off, (int)w.E, (int)x.n, (int)w.cols, (int)w.rows, static_cast<uint8_t *>(x.p),
+                                       x.n > 1 ? x.ld : up(x.ld, 16), xk, static_cast<uint8_t *>(xs.p),
+                                       x.n > 1 ? xs.ld : up(xs.ld, 4), static_cast<uint8_t *>(w.p),
+                                       w.rows > 1 ? w.ld : up(w.ld, 16), w.stride, wk, static_cast<uint8_t *>(vt.data_ptr()),
+                                       vt.stride(0), vt.stride(1), vt.stride(2), o.p, o.ld, type_code(type, "out"), at.status(),
+                                       at.stream),
+          "group_mm8");
+    return written(std::move(out), a[5]);
+}
+
+// ---------------------------------------------------------------------------- gated block
+template <bool GRAD>
+PyObject *gated_block(Args a)                // [da,] x, w, offsets, act, situ_beta, situ_linear_beta, out
+{
+    const at::Tensor &first = tensor(a[0], GRAD ? "da" : "x"), &xt = tensor(a[GRAD], "x"), &wt = tensor(a[GRAD + 1], "w");
+    const Place at(first);
+    const Matrices w(wt, at, "w");
+    need(w.rows > 0 && w.rows % 2 == 0, "w: [E, 2 width, n_in]");
+    const int64_t width = w.rows / 2;
+    const Rows x(xt, at, "x", w.cols);
+    need(xt.scalar_type() == wt.scalar_type(), "x, w: one type");
+    const int32_t *off = static_cast<int32_t *>(table(tensor(a[GRAD + 2], "offsets"), at, "offsets", at::kInt, {w.E + 1}));
+    const int act = act_code(a[GRAD + 3]), type = type_code(xt.scalar_type(), "x");
+    const float beta = (float)as_double(a[GRAD + 4], "situ_beta"), linear = (float)as_double(a[GRAD + 5], "situ_linear_beta");
+    at::Tensor out = output(a[GRAD + 6], x.n, GRAD ? 2 * width : width, xt, xt.scalar_type());
+    const Rows o(out, at, "out", GRAD ? 2 * width : width, x.n);
+    if constexpr (GRAD) {
+        const Rows da(first, at, "da", width, x.n);
+        need(first.scalar_type() == xt.scalar_type(), "da: x's type");
+        check(entry<GROUP_GLU_GRAD>(&k3moe_group_glu_grad)(off, (int)w.E, (int)x.n, (int)w.cols, (int)width, da.p, da.ld, x.p, x.ld,
+                                                           w.p, w.ld, w.stride, type, act, beta, linear, o.p, o.ld, at.status(),
+                                                           at.stream),
+              "group_glu_grad");
+    } else {
+        check(entry<GROUP_GLU>(&k3moe_group_glu)(off, (int)w.E, (int)x.n, (int)w.cols, (int)width, x.p, x.ld, w.p, w.ld, w.stride,
+                                                 type, act, beta, linear, o.p, o.ld, at.status(), at.stream),
+              "group_glu");
+    }
+    return written(std::move(out), a[GRAD + 6]);
+}
+
+// ---------------------------------------------------------------------------- norms
+// Gains [D] of the rows' type or fp32, both of one type; a gate by row or by element.
+struct Gains {
+    const void *p[2] = {};
+    int type;
+    Gains(PyObject *const (&o)[2], const Place &at, const at::Tensor &rows, int64_t D)
+    {
+        at::ScalarType t = rows.scalar_type();
+        for (int i = 0; i < 2; ++i)
+            if (const at::Tensor *g = maybe(o[i], i ? "next_gain" : "gain")) {
+                if (!p[0] && !p[1]) t = g->scalar_type();
+                if (t != at::kFloat && t != rows.scalar_type()) refuse("gains: fp32 or the rows' type");
+                p[i] = table(*g, at, i ? "next_gain" : "gain", t, {D});
+            }
+        type = type_code(t, "gain");
+    }
+};
+
+struct Gate {
+    int kind = K3MOE_GATE_NONE;
+    void *p = nullptr;
+    int64_t ld = 0;
+    Gate(const at::Tensor *t, const Place &at, const at::Tensor &rows, int64_t n, int64_t D)
+    {
+        if (!t) return;
+        if (t->dim() == 1) {
+            kind = K3MOE_GATE_ROW;
+            p = table(*t, at, "gate", at::kFloat, {n});
+        } else {
+            kind = K3MOE_GATE_FULL;
+            const Rows m(*t, at, "gate", D, n);
+            need(t->scalar_type() == rows.scalar_type(), "gate: [rows, D] of the rows' type, or fp32 [rows]");
+            p = m.p;
+            ld = m.ld;
+        }
+    }
+};
+
+PyObject *rms_norm(Args a)                   // x, gain, eps, out
+{
+    const at::Tensor &xt = tensor(a[0], "x");
+    const Place at(xt);
+    const Rows x(xt, at, "x");
+    const Gains g({Py_None, a[1]}, at, xt, x.width);
+    const float eps = (float)as_double(a[2], "eps");
+    at::Tensor out = output(a[3], x.n, x.width, xt, xt.scalar_type());
+    const Rows o(out, at, "out", x.width, x.n);
+    check(entry<RMS_NORM>(&k3moe_rms_norm)(x.p, x.ld, g.p[1], g.type, eps, (int)x.n, (int)x.width,
+                                           type_code(xt.scalar_type(), "x"), o.p, o.ld, at.stream),
+          "rms_norm");
+    return written(std::move(out), a[3]);
+}
+
+PyObject *norm_residual(Args a)              // y, residual, gain, gate, residual_scale, next_gain, eps, out
+{
+    const at::Tensor &yt = tensor(a[0], "y"), &rt = tensor(a[1], "residual");
+    const Place at(yt);
+    const Rows y(yt, at, "y"), r(rt, at, "residual", y.width, y.n);
+    need(rt.scalar_type() == yt.scalar_type(), "residual: y's type");
+    const Gains g({a[2], a[5]}, at, yt, y.width);
+    const Gate gate(maybe(a[3], "gate"), at, yt, y.n, y.width);
+    const float scale = (float)as_double(a[4], "residual_scale"), eps = (float)as_double(a[6], "eps");
+    at::Tensor h = output(a[7], y.n, y.width, yt, yt.scalar_type()), n;
+    const Rows o(h, at, "out", y.width, y.n);
+    if (g.p[1]) n = fresh({y.n, y.width}, yt, yt.scalar_type());
+    check(entry<NORM_RESIDUAL>(&k3moe_norm_residual)(y.p, y.ld, r.p, r.ld, g.p[0], g.p[1], g.type, gate.p, gate.ld, gate.kind, scale,
+                                                     eps, (int)y.n, (int)y.width, type_code(yt.scalar_type(), "y"), o.p, o.ld,
+                                                     g.p[1] ? n.data_ptr() : nullptr, y.width, at.stream),
+          "norm_residual");
+    return tuple({written(std::move(h), a[7]), g.p[1] ? wrap(std::move(n)) : none()});
+}
+
+size_t norm_bytes(const Rows &x)
+{
+    return entry<NORM_BYTES>(&k3moe_norm_grad_workspace_bytes)((int)x.n, (int)x.width);
+}
+
+PyObject *rms_norm_grad(Args a)              // dy, x, gain, eps, add, out
+{
+    const at::Tensor &dt = tensor(a[0], "dy"), &xt = tensor(a[1], "x");
+    const Place at(dt);
+    const Rows x(xt, at, "x"), dy(dt, at, "dy", x.width, x.n);
+    need(dt.scalar_type() == xt.scalar_type(), "dy: x's type");
+    const Gains g({Py_None, a[2]}, at, xt, x.width);
+    const float eps = (float)as_double(a[3], "eps");
+    const at::Tensor *add = maybe(a[4], "add");
+    need(!add || add->scalar_type() == xt.scalar_type(), "add: x's type");
+    const Rows more(add ? *add : xt, at, "add", x.width, x.n);
+    at::Tensor out = output(a[5], x.n, x.width, xt, xt.scalar_type());
+    const Rows o(out, at, "out", x.width, x.n);
+    at::Tensor dgain;
+    if (g.p[1]) dgain = fresh({x.width}, xt, at::kFloat);
+    const size_t nb = norm_bytes(x);
+    const at::Tensor ws = fresh({(int64_t)(nb / 4)}, xt, at::kFloat);
+    check(entry<RMS_NORM_GRAD>(&k3moe_rms_norm_grad)(dy.p, dy.ld, x.p, x.ld, g.p[1], g.type, add ? more.p : nullptr, more.ld, eps,
+                                                     (int)x.n, (int)x.width, type_code(xt.scalar_type(), "x"), o.p, o.ld,
+                                                     g.p[1] ? static_cast<float *>(dgain.data_ptr()) : nullptr, ws.data_ptr(), nb,
+                                                     at.stream),
+          "rms_norm_grad");
+    return tuple({written(std::move(out), a[5]), g.p[1] ? wrap(std::move(dgain)) : none()});
+}
+
+PyObject *norm_residual_grad(Args a)         // dh, dn, y, h, gain, gate, residual_scale, next_gain, eps
+{
+    const at::Tensor &yt = tensor(a[2], "y");
+    const at::Tensor *dht = maybe(a[0], "dh"), *dnt = maybe(a[1], "dn"), *ht = maybe(a[3], "h");
+    const Place at(yt);
+    const Rows y(yt, at, "y");
+    need(dht || dnt, "dh or dn is needed");
+    need(!dnt || ht, "h: needed with dn");
+    for (const at::Tensor *t : {dht, dnt, ht}) need(!t || t->scalar_type() == yt.scalar_type(), "dh, dn, h: y's type");
+    const Rows dh(dht ? *dht : yt, at, "dh", y.width, y.n), dn(dnt ? *dnt : yt, at, "dn", y.width, y.n),
+        h(ht ? *ht : yt, at, "h", y.width, y.n);
+    const Gains g({a[4], a[7]}, at, yt, y.width);
+    const Gate gate(maybe(a[5], "gate"), at, yt, y.n, y.width);
+    const float scale = (float)as_double(a[6], "residual_scale"), eps = (float)as_double(a[8], "eps");
+    need(dnt || !g.p[1], "next_gain: with dn alone");
+    const at::ScalarType type = yt.scalar_type();
+    at::Tensor dy = fresh({y.n, y.width}, yt, type), dres = fresh({y.n, y.width}, yt, type), dgate, dgain, dnext;
+    if (gate.kind == K3MOE_GATE_ROW) dgate = fresh({y.n}, yt, at::kFloat);
+    if (gate.kind == K3MOE_GATE_FULL) dgate = fresh({y.n, y.width}, yt, type);
+    if (g.p[0]) dgain = fresh({y.width}, yt, at::kFloat);
+    if (g.p[1]) dnext = fresh({y.width}, yt, at::kFloat);
+    const size_t nb = norm_bytes(y);
+    const at::Tensor ws = fresh({(int64_t)(nb / 4)}, yt, at::kFloat);
+    check(entry<NORM_RESIDUAL_GRAD>(&k3moe_norm_residual_grad)(
+              dht ? dh.p : nullptr, dh.ld, dnt ? dn.p : nullptr, dn.ld, y.p, y.ld, ht ? h.p : nullptr, h.ld, g.p[0], g.p[1], g.type,
+              gate.p, gate.ld, gate.kind, scale, eps, (int)y.n, (int)y.width, type_code(type, "y"), dy.data_ptr(), y.width,
+              dres.data_ptr(), y.width, gate.p || gate.kind != K3MOE_GATE_NONE ? dgate.data_ptr() : nullptr, y.width,
+              g.p[0] ? static_cast<float *>(dgain.data_ptr()) : nullptr, g.p[1] ? static_cast<float *>(dnext.data_ptr()) : nullptr,
+              ws.data_ptr(), nb, at.stream),
+          "norm_residual_grad");
+    return tuple({wrap(std::move(dy)), wrap(std::move(dres)), g.p[0] ? wrap(std::move(dgain)) : none(),
+                  gate.kind != K3MOE_GATE_NONE ? wrap(std::move(dgate)) : none(), g.p[1] ? wrap(std::move(dnext)) : none()});
+}
+
+PyObject *group_glu(Args a) { return gated_block<false>(a); }
+PyObject *group_glu_grad(Args a) { return gated_block<true>(a); }
+
 // No C++ exception leaves a call: refusals become the error class, others a RuntimeError.
 template <PyObject *(*F)(Args), int N>
 PyObject *call(PyObject *, PyObject *const *args, Py_ssize_t n)
@@ -485,6 +778,15 @@ PyMethodDef methods[] = {{"setup", (PyCFunction)(void (*)(void))setup, METH_FAST
                          CALL(glu_dropout, 8),
                          CALL(glu_dropout_grad, 9),
                          CALL(dropout, 6),
+                         CALL(quant8_rows, 2),
+                         CALL(quant8_weights, 3),
+                         CALL(group_mm8, 7),
+                         CALL(group_glu, 7),
+                         CALL(group_glu_grad, 8),
+                         CALL(rms_norm, 4),
+                         CALL(norm_residual, 8),
+                         CALL(rms_norm_grad, 6),
+                         CALL(norm_residual_grad, 9),
                          {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_experts", "Binding of the expert training operators.", -1, methods};
 

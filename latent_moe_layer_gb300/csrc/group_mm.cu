@@ -1,6 +1,6 @@
 // Products grouped by expert (k3moe_group_mm, _grad_x, _grad_w): argument checks, and the kernel of shapes
 // and strides that the copy engine, which feeds the main kernel (group_tc.cu), cannot address.
-#include "experts.h"
+#include "glu.cuh"
 #include "group_sched.cuh"
 
 namespace k3 {
@@ -34,25 +34,28 @@ __device__ __forceinline__ void load_blocks(uint32_t (&r)[4], const void *row)
 // 64 x 64 outputs per CTA, 32 x 16 a warp, the contraction in steps of 32 through shared memory; the next step's
 // values are in flight meanwhile, one element a load, so any size, stride and alignment goes.  Those loads bind it:
 // 4,099 rows over 8 experts, 1001 to 2003: 260 us, 63 TFLOP/s (fp32 sums on the CUDA cores: 820); the gradients 312 and 309.
-// Tile rows x are output rows (tokens' rows; n_out for grad_w), columns y the output's contiguous axis.
+// Tile rows x are output rows (tokens' rows; n_out for grad_w), columns y the output's contiguous axis.  The gated block's
+// 64 columns are eight gate and the same eight up rows of the weights in turn, so that a thread's two accumulator pieces of a
+// warp tile are both projections of the same elements.
 template <int MODE, class T, class O>
-__global__ void __launch_bounds__(GG_THREADS, 3) group_generic_kernel(const K3Group g)
+__global__ void __launch_bounds__(GG_THREADS, 3) group_generic_kernel(const K3Group g, const K3GroupGlu unit)
 {
     griddep_enter();
-    constexpr bool W = MODE == K3_GROUP_GRAD_W;
-    constexpr bool X_K = !W, Y_K = MODE == K3_GROUP_MM;                  // operands contiguous along the contraction
+    constexpr bool W = MODE == K3_GROUP_GRAD_W, GLU = MODE == K3_GROUP_GLU || MODE == K3_GROUP_GLU_GRAD;
+    constexpr bool X_K = !W, Y_K = MODE == K3_GROUP_MM || GLU;           // operands contiguous along the contraction
+    constexpr int Y_TILE = GLU ? GG_TILE / 2 : GG_TILE;                  // output columns of a tile
     constexpr int LOADS = GG_TILE * GG_K / GG_THREADS;
     __shared__ __align__(16) uint16_t sx[2][GG_TILE][GG_ROW], sy[2][GG_TILE][GG_ROW];
     __shared__ int s_off[K3MOE_TRAIN_MAX_EXPERTS + 1], s_tile[K3MOE_TRAIN_MAX_EXPERTS + 1], s_tmp[GG_THREADS / 32];
     if (!group_tiles<GG_THREADS, GG_TILE>(g.offsets, g.E, g.rows, s_off, s_tile, s_tmp, g.status)) return;
     const uint16_t *A = static_cast<const uint16_t *>(g.a), *B = static_cast<const uint16_t *>(g.b);
     O *out = static_cast<O *>(g.out);
-    const int NY = MODE == K3_GROUP_MM ? g.n_out : g.n_in;
-    const int y_blocks = (NY + GG_TILE - 1) / GG_TILE, x_blocks = W ? (g.n_out + GG_TILE - 1) / GG_TILE : 1;
+    const int NY = MODE == K3_GROUP_MM || GLU ? g.n_out : g.n_in;
+    const int y_blocks = (NY + Y_TILE - 1) / Y_TILE, x_blocks = W ? (g.n_out + GG_TILE - 1) / GG_TILE : 1;
     const long long jobs = (W ? (long long)g.E * x_blocks : (long long)s_tile[g.E]) * y_blocks;
     const int lane = threadIdx.x & 31, wx = (threadIdx.x >> 5 & 1) * 32, wy = (threadIdx.x >> 6) * 16;
     for (long long job = blockIdx.x; job < jobs; job += gridDim.x) {
-        const int y0 = (int)(job % y_blocks) * GG_TILE, t = (int)(job / y_blocks);
+        const int y0 = (int)(job % y_blocks) * Y_TILE, t = (int)(job / y_blocks);
         int e, x0, x1, k1;                       // tile rows [x0, x1), contraction [0, k1)
         long long r0 = 0;
         if (W) {
@@ -65,7 +68,7 @@ __global__ void __launch_bounds__(GG_THREADS, 3) group_generic_kernel(const K3Gr
             e = group_find(s_tile, g.E, t);
             x0 = s_off[e] + (t - s_tile[e]) * GG_TILE;
             x1 = s_off[e + 1];
-            k1 = MODE == K3_GROUP_MM ? g.n_in : g.n_out;
+            k1 = MODE == K3_GROUP_MM || GLU ? g.n_in : g.n_out;
         }
         const uint16_t *Be = B + (W ? r0 * g.ldb : e * g.stride_b), *Ae = A + (W ? r0 * g.lda : 0);
         uint16_t vx[LOADS], vy[LOADS];
@@ -75,9 +78,10 @@ __global__ void __launch_bounds__(GG_THREADS, 3) group_generic_kernel(const K3Gr
                 // consecutive threads along the operand's contiguous axis
                 const int at = threadIdx.x + i * GG_THREADS;
                 const int kx = k0 + (X_K ? at % GG_K : at / GG_TILE), x = x0 + (X_K ? at / GG_K : at % GG_TILE);
-                const int ky = k0 + (Y_K ? at % GG_K : at / GG_TILE), y = y0 + (Y_K ? at / GG_K : at % GG_TILE);
+                const int ky = k0 + (Y_K ? at % GG_K : at / GG_TILE), iy = Y_K ? at / GG_K : at % GG_TILE;
+                const int y = y0 + (GLU ? iy / 16 * 8 + iy % 8 : iy), up = GLU && (iy & 8) ? NY : 0;
                 vx[i] = kx < k1 && x < x1 ? Ae[X_K ? x * g.lda + kx : kx * g.lda + x] : (uint16_t)0;
-                vy[i] = ky < k1 && y < NY ? Be[Y_K ? y * g.ldb + ky : ky * g.ldb + y] : (uint16_t)0;
+                vy[i] = ky < k1 && y < NY ? Be[Y_K ? (y + up) * g.ldb + ky : ky * g.ldb + y] : (uint16_t)0;
             }
         };
         float acc[2][2][4] = {}, sum[2][2][4] = {};
@@ -114,24 +118,50 @@ __global__ void __launch_bounds__(GG_THREADS, 3) group_generic_kernel(const K3Gr
             }
         }
         __syncthreads();                         // the next job writes the buffers
+        if constexpr (GLU) {
+            constexpr bool GRAD = MODE == K3_GROUP_GLU_GRAD;
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-            const int x = x0 + wx + (i >> 3) * 16 + (lane >> 2) + (i >> 1 & 1) * 8;
-            const int y = y0 + wy + (i >> 2 & 1) * 8 + (lane & 3) * 2 + (i & 1);
-            if (x >= x1 || y >= NY) continue;
-            O *o = out + (W ? e * g.stride_o : 0) + x * g.ldo + y;
-            const float v = (&sum[0][0][0])[i];
-            *o = from_f32<O>(W && g.accumulate ? to_f32(*o) + v : v);
+            for (int i = 0; i < 4; ++i) {        // two elements of a row at a time
+                const int x = x0 + wx + (i >> 1) * 16 + (lane >> 2) + (i & 1) * 8, y = y0 + wy / 2 + (lane & 3) * 2;
+                if (x >= x1 || y >= NY) continue;
+                const float *gs = &sum[i >> 1][0][2 * (i & 1)], *us = &sum[i >> 1][1][2 * (i & 1)];
+                const F2 gv = {gs[0], gs[1]}, uv = {us[0], us[1]};
+                F2 t = f2(unit.situ ? 1.0f : SILU_UNIT), o0, o1;
+                const bool two = y + 1 < NY;
+                if (GRAD) {
+                    const T *d = static_cast<const T *>(unit.da) + x * unit.ldda + y;
+                    t = mul2(t, {to_f32(d[0]), two ? to_f32(d[1]) : 0.f});
+                }
+                if (unit.situ) glu_two<K3MOE_ACT_SITU, GRAD, false>(gv, uv, t, unit.c, o0, o1);
+                else glu_two<K3MOE_ACT_SILU, GRAD, false>(gv, uv, t, unit.c, o0, o1);
+                O *o = out + x * g.ldo + y;
+                o[0] = from_f32<O>(o0.x);
+                if (two) o[1] = from_f32<O>(o0.y);
+                if (GRAD) {
+                    o[NY] = from_f32<O>(o1.x);
+                    if (two) o[NY + 1] = from_f32<O>(o1.y);
+                }
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                const int x = x0 + wx + (i >> 3) * 16 + (lane >> 2) + (i >> 1 & 1) * 8;
+                const int y = y0 + wy + (i >> 2 & 1) * 8 + (lane & 3) * 2 + (i & 1);
+                if (x >= x1 || y >= NY) continue;
+                O *o = out + (W ? e * g.stride_o : 0) + x * g.ldo + y;
+                const float v = (&sum[0][0][0])[i];
+                *o = from_f32<O>(W && g.accumulate ? to_f32(*o) + v : v);
+            }
         }
     }
 }
 
 template <int MODE, class T, class O>
-static int launch_generic(const K3Group &g, cudaStream_t st)
+static int launch_generic(const K3Group &g, cudaStream_t st, const K3GroupGlu &unit = {})
 {
     const int sms = k3_num_sms();
     if (!sms) return K3MOE_ERR_CUDA;
-    k3_launch(group_generic_kernel<MODE, T, O>, 3 * sms, GG_THREADS, 0, st, g);
+    k3_launch(group_generic_kernel<MODE, T, O>, 3 * sms, GG_THREADS, 0, st, g, unit);
     k3_note_launch();
     return cudaGetLastError() == cudaSuccess ? K3MOE_OK : K3MOE_ERR_CUDA;
 }
@@ -169,8 +199,15 @@ int k3_group_generic(int mode, const K3Group &g, cudaStream_t st)
     }
 }
 
-// Checks shared by the three products; > 0: nothing to do.
-static int group_check(const K3Group &g, int mode)
+int k3_group_glu_generic(const K3Group &g, const K3GroupGlu &u, cudaStream_t st)
+{
+    if (g.dtype == K3MOE_TYPE_BF16)
+        return u.da ? launch_generic<K3_GROUP_GLU_GRAD, __nv_bfloat16, __nv_bfloat16>(g, st, u)
+                    : launch_generic<K3_GROUP_GLU, __nv_bfloat16, __nv_bfloat16>(g, st, u);
+    return u.da ? launch_generic<K3_GROUP_GLU_GRAD, __half, __half>(g, st, u) : launch_generic<K3_GROUP_GLU, __half, __half>(g, st, u);
+}
+
+int k3_group_check(const K3Group &g, int mode)
 {
     if (g.E < 1 || g.rows < 0 || g.n_in < 1 || g.n_out < 1 || !g.offsets || !g.status) return K3MOE_ERR_ARG;
     if (g.E > K3MOE_TRAIN_MAX_EXPERTS) return K3MOE_ERR_SHAPE;
@@ -203,7 +240,7 @@ static int group_check(const K3Group &g, int mode)
 
 static int group_run(const K3Group &g, int mode, cudaStream_t st)
 {
-    const int rc = group_check(g, mode);
+    const int rc = k3_group_check(g, mode);
     if (rc) return rc > 0 ? K3MOE_OK : rc;
     return k3_group_tc_fits(mode, g) ? k3_group_tc(mode, g, st) : k3_group_generic(mode, g, st);
 }

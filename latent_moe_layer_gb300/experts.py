@@ -1,6 +1,6 @@
-"""Training step of the routed experts on 16-bit weights (the k3moe_rows_*, k3moe_group_*, k3moe_glu_*
-and k3moe_dropout calls of include/k3moe.h): tensors in, tensors out, argument marshalling only (in
-csrc/experts_py.cpp).
+"""Training step of the routed experts on 16-bit weights (the k3moe_rows_*, k3moe_group_*, k3moe_glu_*,
+k3moe_quant8_*, k3moe_*norm* and k3moe_dropout calls of include/k3moe.h): tensors in, tensors out, argument
+marshalling only (in csrc/experts_py.cpp).
 
 Tensors live on one CUDA device; matrices have contiguous rows (any row stride).  Work is enqueued on
 `stream` (default: the current stream), and results are allocated there.  Nothing is recorded for autograd: a
@@ -128,6 +128,80 @@ def group_mm_grad_w(dy, x, offsets, out=None, out_dtype=None, accumulate=False, 
     fp32 by default (or `out`'s / `out_dtype`'s type: x's).  accumulate adds to an fp32 `out`; otherwise an
     expert without rows gets zeros."""
     return _call("group_mm_grad_w", stream, dy, x, offsets, out, out_dtype, accumulate)
+
+
+# ------------------------------------------------------------------------------------------ gated block
+def group_glu(x, w, offsets, act="silu", situ_beta=4.0, situ_linear_beta=25.0, out=None, stream=None):
+    """a[r] = act(Wg x[r]) (Wu x[r]) for every expert's rows: both projections and the unit in one pass.
+
+    x [rows, n_in], w [E, 2 width, n_in] = gate rows then up rows, of one 16-bit type -> a [rows, width].  The
+    projections are not rounded on the way (group_mm then glu_dropout rounds them, and draws a dropout mask)."""
+    return _call("group_glu", stream, x, w, offsets, act, situ_beta, situ_linear_beta, out)
+
+
+def group_glu_grad(da, x, w, offsets, act="silu", situ_beta=4.0, situ_linear_beta=25.0, out=None, stream=None):
+    """Gradient of group_glu for its projections, which are computed again -> dgu [rows, 2 width].
+
+    The gradients for x and w are group_mm_grad_x(dgu, w, offsets) and group_mm_grad_w(dgu, x, offsets)."""
+    return _call("group_glu_grad", stream, da, x, w, offsets, act, situ_beta, situ_linear_beta, out)
+
+
+# ------------------------------------------------------------------------------------------ 8-bit operands
+def quant8_rows(x, kind="e4m3", stream=None):
+    """x [rows, n], 16-bit -> (codes [rows, n] float8_e4m3fn or, for kind "e5m2", float8_e5m2, scales [rows,
+    ceil(n / 128)] uint8): a value is code 2^(scale - 127), a scale for each 128 columns of a row.
+
+    The scale is the smallest power of two under which nothing saturates; a value that is not finite takes no part in
+    it and becomes NaN (e5m2 keeps infinities).  Rows of the results start on 16- and 4-byte boundaries."""
+    return _call("quant8_rows", stream, x, kind)
+
+
+def quant8_weights(w, kind="e4m3", transposed=False, stream=None):
+    """w [E, n_out, n_in], 16-bit -> (codes [E, n_out, n_in], scales [E, ceil(n_out / 128), ceil(n_in / 128)] uint8):
+    a scale for each 128 x 128 block, as in quant8_rows.
+
+    transposed: a third result, the same codes as [E, n_in, n_out], whose scales are scales.transpose(1, 2)."""
+    return _call("quant8_weights", stream, w, kind, transposed)
+
+
+def group_mm8(x, x_scales, w, w_scales, offsets, out=None, out_dtype=None, stream=None):
+    """y[r] = w[e] x[r] on 8-bit operands (quant8_rows, quant8_weights) -> [rows, n_out], bf16 (or `out`'s / `out_dtype`'s
+    type: f16, fp32).
+
+    The gradient for the rows is the same call on the quantised dy with the transposed codes and scales.  Codes of rows
+    that are not on 16-byte boundaries are refused."""
+    return _call("group_mm8", stream, x, x_scales, w, w_scales, offsets, out, out_dtype)
+
+
+# ------------------------------------------------------------------------------------------ norms
+def rms_norm(x, gain=None, eps=1e-6, out=None, stream=None):
+    """gain x / sqrt(mean x^2 + eps) over each row; x [rows, D <= 16384], fp32 or 16-bit, gain [D] of x's type or fp32.
+    `out` may be x."""
+    return _call("rms_norm", stream, x, gain, eps, out)
+
+
+def rms_norm_grad(dy, x, gain=None, eps=1e-6, add=None, out=None, stream=None):
+    """Gradient of rms_norm: (dx [+ add], dgain [D] fp32 or None without a gain).  `out` may be dy, x or add."""
+    return _call("rms_norm_grad", stream, dy, x, gain, eps, add, out)
+
+
+def norm_residual(y, residual, gain=None, gate=None, residual_scale=1.0, next_gain=None, eps=1e-6, out=None, stream=None):
+    """The norm after a block, its gate, the residual and the norm before the next block: (h, n) with
+    h = residual_scale residual + gate (gain y rs(y)), n = next_gain h rs(h), rs(v) = 1 / sqrt(mean v^2 + eps).
+
+    gate: None, fp32 [rows], or [rows, D] of y's type.  Without next_gain n is None.  `out` (for h) may be y, residual or
+    gate; n comes from the h that is not rounded yet."""
+    return _call("norm_residual", stream, y, residual, gain, gate, residual_scale, next_gain, eps, out)
+
+
+def norm_residual_grad(dh, dn, y, h, gain=None, gate=None, residual_scale=1.0, next_gain=None, eps=1e-6, stream=None):
+    """Gradient of norm_residual: (dy, dresidual, dgain, dgate, dnext_gain), None for what was not there.
+
+    dh and dn are the gradients for h and n (either may be None, not both); h is norm_residual's (may be None without
+    dn).  dgain and dnext_gain are fp32 [D], dgate of the gate's shape and type."""
+    if stream is not None and y.device != stream.device:         # dh may be None
+        raise K3Error(ERR_CODE["ARG"], "stream: one of the tensors' device")
+    return _call("norm_residual_grad", stream, dh, dn, y, h, gain, gate, residual_scale, next_gain, eps)
 
 
 # ------------------------------------------------------------------------------------------ gated unit, dropout

@@ -31,7 +31,10 @@ EXPORTS = ["k3moe_create", "k3moe_persistent_bytes", "k3moe_load_weights", "k3mo
            "k3moe_route_static", "k3moe_mma_peak",
            "k3moe_rows_plan_workspace_bytes", "k3moe_rows_plan", "k3moe_rows_gather", "k3moe_rows_combine",
            "k3moe_rows_combine_grad", "k3moe_group_mm", "k3moe_group_mm_grad_x", "k3moe_group_mm_grad_w",
-           "k3moe_glu_dropout", "k3moe_glu_dropout_grad", "k3moe_dropout"]
+           "k3moe_glu_dropout", "k3moe_glu_dropout_grad", "k3moe_dropout",
+           "k3moe_quant8_rows", "k3moe_quant8_weights", "k3moe_group_mm8", "k3moe_group_glu", "k3moe_group_glu_grad",
+           "k3moe_rms_norm", "k3moe_norm_residual", "k3moe_norm_grad_workspace_bytes", "k3moe_rms_norm_grad",
+           "k3moe_norm_residual_grad"]
 STAGES = ["router", "down_proj", "topk", "permute", "gate_up", "expert_down", "combine_norm",
           "up_proj", "shared", "finish", "prep", "shared_down"]
 
@@ -122,6 +125,18 @@ def lib():
         L.k3moe_glu_dropout.argtypes = [vp, l, i, i, i, i, f, f, d, u, u, vp, l, vp]
         L.k3moe_glu_dropout_grad.argtypes = [vp, l, vp, l, i, i, i, i, f, f, d, u, u, vp, l, vp]
         L.k3moe_dropout.argtypes = [vp, vp, l, i, d, u, u, vp, vp]
+        L.k3moe_quant8_rows.argtypes = [vp, l, i, i, i, i, vp, l, vp, l, vp]
+        L.k3moe_quant8_weights.argtypes = [vp, l, l, i, i, i, i, i, vp, l, l, vp, l, l, vp, vp]
+        L.k3moe_group_mm8.argtypes = [vp, i, i, i, i, vp, l, i, vp, l, vp, l, l, i, vp, l, l, l, vp, l, i, vp, vp]
+        L.k3moe_group_glu.argtypes = [vp, i, i, i, i, vp, l, vp, l, l, i, i, f, f, vp, l, vp, vp]
+        L.k3moe_group_glu_grad.argtypes = [vp, i, i, i, i, vp, l, vp, l, vp, l, l, i, i, f, f, vp, l, vp, vp]
+        L.k3moe_rms_norm.argtypes = [vp, l, vp, i, f, i, i, i, vp, l, vp]
+        L.k3moe_norm_residual.argtypes = [vp, l, vp, l, vp, vp, i, vp, l, i, f, f, i, i, i, vp, l, vp, l, vp]
+        L.k3moe_norm_grad_workspace_bytes.argtypes = [i, i]
+        L.k3moe_norm_grad_workspace_bytes.restype = sz
+        L.k3moe_rms_norm_grad.argtypes = [vp, l, vp, l, vp, i, vp, l, f, i, i, i, vp, l, vp, vp, sz, vp]
+        L.k3moe_norm_residual_grad.argtypes = [vp, l, vp, l, vp, l, vp, l, vp, vp, i, vp, l, i, f, f, i, i, i, vp, l, vp, l,
+                                               vp, l, vp, vp, vp, sz, vp]
         for name in EXPORTS:
             getattr(L, name)
         _lib = L

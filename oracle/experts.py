@@ -106,3 +106,99 @@ def group_mm_grad_x(dy, w, offsets):
 def group_mm_grad_w(dy, x, offsets):
     dy, x = np.asarray(dy, dtype=np.float64), np.asarray(x, dtype=np.float64)
     return np.stack([dy[a:b].T @ x[a:b] for a, b in zip(offsets[:-1], offsets[1:])])
+
+
+# ------------------------------------------------------------------------------------------ gated block
+def group_glu(x, w, offsets, act="silu", beta=4.0, linear_beta=25.0):
+    """Rows of no expert give zeros, as in group_mm."""
+    return glu_dropout(group_mm(x, w, offsets), 0.0, 0, 0, act, beta, linear_beta)
+
+
+def group_glu_grad(da, x, w, offsets, act="silu", beta=4.0, linear_beta=25.0):
+    return glu_dropout_grad(da, group_mm(x, w, offsets), 0.0, 0, 0, act, beta, linear_beta)
+
+
+# ------------------------------------------------------------------------------------------ 8-bit operands
+F8 = {"e4m3": (3, -6, 448.0), "e5m2": (2, -14, 57344.0)}      # mantissa bits, least normal exponent, largest value
+
+
+def round8(v, kind):
+    """To the format's nearest value, ties to even; |v| is at most the largest value, or not finite."""
+    mantissa, least, _ = F8[kind]
+    v = np.asarray(v, dtype=np.float64)
+    with np.errstate(invalid="ignore"):
+        e = np.maximum(np.frexp(np.where(np.isfinite(v), v, 1.0))[1] - 1, least)
+        out = np.ldexp(np.rint(np.ldexp(v, mantissa - e)), e - mantissa)
+    if kind == "e4m3":
+        out = np.where(np.isinf(v), np.nan, out)
+    return out
+
+
+def scale_exponent(amax, kind):
+    """The smallest k >= -127 with amax <= 2^k largest."""
+    k = -127
+    while amax > F8[kind][2] * 2.0 ** k:
+        k += 1
+    return k
+
+
+def quant8(x, kind, rows=1, cols=128):
+    """x [..., n, m] -> (codes' values, scale bytes k + 127) with a scale for each block of rows x cols."""
+    x = np.asarray(x, dtype=np.float64)
+    n, m = x.shape[-2:]
+    codes = np.empty_like(x)
+    scales = np.empty(x.shape[:-2] + (-(-n // rows), -(-m // cols)), dtype=np.uint8)
+    for i in np.ndindex(*scales.shape):
+        at = i[:-2] + (slice(i[-2] * rows, (i[-2] + 1) * rows), slice(i[-1] * cols, (i[-1] + 1) * cols))
+        v = x[at]
+        k = scale_exponent(np.max(np.abs(v[np.isfinite(v)]), initial=0.0), kind)
+        scales[i] = k + 127
+        codes[at] = round8(np.ldexp(v, -k), kind)
+    return codes, scales
+
+
+def dequant8(codes, scales, rows=1, cols=128):
+    k = np.repeat(np.repeat(np.asarray(scales, dtype=np.int64) - 127, rows, -2), cols, -1)
+    codes = np.asarray(codes, dtype=np.float64)
+    return np.ldexp(codes, k[..., :codes.shape[-2], :codes.shape[-1]])
+
+
+def group_mm8(x, x_scales, w, w_scales, offsets):
+    return group_mm(dequant8(x, x_scales), dequant8(w, w_scales, 128), offsets)
+
+
+# ------------------------------------------------------------------------------------------ norms
+def rms_norm(x, gain=None, eps=1e-6):
+    x = np.asarray(x, dtype=np.float64)
+    n = x / np.sqrt(np.mean(x * x, 1, keepdims=True) + eps)
+    return n if gain is None else n * gain
+
+
+def rms_norm_grad(dy, x, gain=None, eps=1e-6, add=None):
+    """(dx, dgain): dgain also without a gain."""
+    dy, x = np.asarray(dy, dtype=np.float64), np.asarray(x, dtype=np.float64)
+    r = 1.0 / np.sqrt(np.mean(x * x, 1, keepdims=True) + eps)
+    v = dy if gain is None else dy * gain
+    dx = r * v - x * r ** 3 * np.mean(v * x, 1, keepdims=True)
+    return dx if add is None else dx + add, (dy * x * r).sum(0)
+
+
+def _gate(gate):
+    return 1.0 if gate is None else np.asarray(gate, dtype=np.float64).reshape(len(gate), -1)
+
+
+def norm_residual(y, residual, gain=None, gate=None, residual_scale=1.0, next_gain=None, eps=1e-6):
+    h = residual_scale * np.asarray(residual, dtype=np.float64) + _gate(gate) * rms_norm(y, gain, eps)
+    return h, rms_norm(h, next_gain, eps)
+
+
+def norm_residual_grad(dh, dn, y, h, gain=None, gate=None, residual_scale=1.0, next_gain=None, eps=1e-6):
+    """(dy, dresidual, dgain, dgate, dnext_gain); dgate for each element and (rows) summed where the gate is by row."""
+    t = 0.0 if dh is None else np.asarray(dh, dtype=np.float64)
+    dnext = None
+    if dn is not None:
+        t, dnext = rms_norm_grad(dn, h, next_gain, eps, add=t)
+    b = rms_norm(y, gain, eps)
+    dgate = None if gate is None else (t * b if np.ndim(gate) == 2 else (t * b).sum(1))
+    dy, dgain = rms_norm_grad(t * _gate(gate), y, gain, eps)
+    return dy, residual_scale * t, dgain, dgate, dnext
