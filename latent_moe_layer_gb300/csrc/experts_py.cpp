@@ -492,10 +492,10 @@ PyObject *quant8_rows(Args a)                // x, kind
     const int kind = kind_code(a[1]), type = type_code(xt.scalar_type(), "x");
     need(x.width > 0, "x: [rows, n]");
     const int64_t blocks = (x.width + 127) / 128;
-    at::Tensor codes = padded_rows({x.n, x.width}, 16, xt, kind_type(kind)), scales = padded_rows({x.n, blocks}, 4, xt, at::kByte);
+    at::Tensor codes = padded_rows({x.n, x.width}, 16, xt, kind_type(kind)), scales = padded_rows({x.n, blocks}, 16, xt, at::kByte);
     check(entry<QUANT_ROWS>(&k3moe_quant8_rows)(x.p, x.ld, (int)x.n, (int)x.width, type, kind,
                                                 static_cast<uint8_t *>(codes.data_ptr()), up(x.width, 16),
-                                                static_cast<uint8_t *>(scales.data_ptr()), up(blocks, 4), at.stream),
+                                                static_cast<uint8_t *>(scales.data_ptr()), up(blocks, 16), at.stream),
           "quant8_rows");
     return pair(wrap(std::move(codes)), std::move(scales));
 }
@@ -541,7 +541,7 @@ PyObject *group_mm8(Args a)                  // x, x_scales, w, w_scales, offset
     // a matrix of one row has no stride of its own: the next boundary
     check(entry<MM8>(&k3moe_group_mm8)(off, (int)w.E, (int)x.n, (int)w.cols, (int)w.rows, static_cast<uint8_t *>(x.p),
                                        x.n > 1 ? x.ld : up(x.ld, 16), xk, static_cast<uint8_t *>(xs.p),
-                                       x.n > 1 ? xs.ld : up(xs.ld, 4), static_cast<uint8_t *>(w.p),
+                                       x.n > 1 ? xs.ld : up(xs.ld, 16), static_cast<uint8_t *>(w.p),
                                        w.rows > 1 ? w.ld : up(w.ld, 16), w.stride, wk, static_cast<uint8_t *>(vt.data_ptr()),
                                        vt.stride(0), vt.stride(1), vt.stride(2), o.p, o.ld, type_code(type, "out"), at.status(),
                                        at.stream),

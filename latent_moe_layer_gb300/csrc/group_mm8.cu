@@ -45,6 +45,7 @@ extern "C" int k3moe_group_mm8(const int32_t *offsets, int n_experts, int rows, 
     a.status = status;
     a.xs = x_scales;
     a.ldxs = ldxs;
+    a.xs16 = (((uintptr_t)x_scales | (uint64_t)ldxs) & 15) == 0;
     a.ws = w_scales;
     a.sse = E > 1 ? sse : 0;
     a.sso = sso;

@@ -59,9 +59,9 @@ constexpr int64_t GT_L2_ROWS = 32 << 20;
 // bytes of a box of 16 rows of 16 16-bit values, the second eight rows 32 bytes further so that both halves' stores miss
 // each other's banks
 constexpr int GT_BOX16 = 16 * 32 + 32;
-// 8-bit products: scale words (four blocks of the contraction) of 128 rows of A and of 256 of B; slots of them in shared
-// memory and in tensor memory (4 and 8 columns)
-constexpr int GT_SF_BYTES = 512 + 1024, GT_SF_SLOTS = 2, GT_SF_COL = 2 * 240, GT_SF_COLS = 16;
+// 8-bit products: scale words (four blocks of the contraction) of 128 rows of A and of 256 of B: four slots in shared memory,
+// two in tensor memory (4 and 8 columns each)
+constexpr int GT_SF_BYTES = 512 + 1024, GT_SF_SLOTS = 4, GT_SF_COL = 2 * 240, GT_SF_COLS = 16;
 
 template <int MODE, bool FOLD>
 struct GroupSmem {
@@ -116,7 +116,7 @@ struct GroupTcArgs {
     // 8-bit products: scales of x [rows, blocks] (row stride ldxs) and of w (expert, row block, block); types of the codes
     const uint8_t *xs, *ws;
     int64_t ldxs, sse, sso, ssi;
-    int blocks, a_type, b_type;
+    int blocks, xs16, a_type, b_type;
 };
 
 struct GroupJob {
@@ -607,6 +607,7 @@ __global__ void __launch_bounds__(GroupSmem<MODE, FOLD>::THREADS, 1)
         RingPos<NS> p;
         RingPos<2> acc;
         RingPos<GT_SF_SLOTS> sf;
+        uint32_t words = 0;
         bool ok = true;
         for (GroupWalk<MODE> walk(args, s_off, s_tile, mb, cb, jobs); walk.valid() && ok; walk.next()) {
             const GroupJob j = walk.get();
@@ -623,7 +624,12 @@ __global__ void __launch_bounds__(GroupSmem<MODE, FOLD>::THREADS, 1)
                 // a scale word covers four stages
                 const bool sf_begin = F8 && (s == s0 || (s & 3) == 0), sf_end = F8 && (s == s1 - 1 || (s & 3) == 3);
                 if constexpr (F8)
-                    if (sf_begin) ok = ok && pair_wait(smem_u32(sfull + sf.slot), sf.phase, abort_flag, args.status, 67);
+                    if (sf_begin) {
+                        ok = ok && pair_wait(smem_u32(sfull + sf.slot), sf.phase, abort_flag, args.status, 67);
+                        // its slot in tensor memory: the MMAs of the word two before have read it
+                        const uint32_t two = (sf.slot + 2) % GT_SF_SLOTS, p2 = sf.slot < 2 ? sf.phase ^ 1 : sf.phase;
+                        if (words++ >= 2) ok = ok && pair_wait(smem_u32(sempty + two), p2, abort_flag, args.status, 70);
+                    }
                 ok = ok && pair_wait(smem_u32(full + p.slot), p.phase, abort_flag, args.status, 64);
                 if (!ok) break;
                 if constexpr (F8)
@@ -634,7 +640,7 @@ __global__ void __launch_bounds__(GroupSmem<MODE, FOLD>::THREADS, 1)
                 const uint32_t d = tmem + acc.slot * TILE_N;
                 const uint64_t ad = ad0 + p.slot * (GT_STAGE / 16), bd = bd0 + p.slot * (GT_STAGE / 16);
                 const int kk_n = last ? (j.last + STEP - 1) / STEP : 4;
-                const uint32_t sfa = tmem + GT_SF_COL + sf.slot * GT_SF_COLS, sfb = sfa + 4;
+                const uint32_t sfa = tmem + GT_SF_COL + (sf.slot & 1) * GT_SF_COLS, sfb = sfa + 4;
                 const uint32_t sf_id = (uint32_t)(s & 3) << 29 | (uint32_t)(s & 3) << 4;
                 if (one) {
                     if constexpr (F8)
@@ -688,43 +694,75 @@ __global__ void __launch_bounds__(GroupSmem<MODE, FOLD>::THREADS, 1)
         // ------------------------------------------------------------ scales (each CTA its A rows and all of B's)
         // A word holds a row's scales of four blocks of the contraction, the MMA picks the byte.  In shared memory word i of
         // row 32 i + l of 128 is lane l's i-th; A's rows of a CTA lie in one block of the weights and share one word.
+        // 16 blocks are loaded at a time, while the 16 before them are handed on: an arrival that releases to the cluster
+        // waits for all of the thread's loads (with a load for every word, 8192^3 took 443 us).
         const uint32_t sfull0 = cluster_addr(smem_u32(sfull), lead);
         RingPos<GT_SF_SLOTS> sf;
         uint32_t used = 0;
         bool ok = true;
         const int m_blocks = (args.M + 127) / 128;
-        for (GroupWalk<MODE> walk(args, s_off, s_tile, mb, cb, jobs); walk.valid() && ok; walk.next()) {
-            const GroupJob j = walk.get();
-            const int s0 = first_stage(j), s1 = end_stage(j), m_block = j.m0 / 128 + (int)rank;
-            const uint8_t *ws = args.ws + walk.e * args.sse + m_block * args.sso;
-            if (s0 >= s1) continue;
-            for (int g = s0 >> 2; g <= (s1 - 1) >> 2; ++g, ++used, sf.next()) {
-                const int b = 4 * g, nb = min(4, args.blocks - b);
-                uint32_t w = 0, x[8];
-                if (lane < nb) w = (m_block < m_blocks ? (uint32_t)ws[(int64_t)(b + lane) * args.ssi] : 127u) << (8 * lane);
-                w = __reduce_or_sync(0xffffffffu, w);
+        GroupWalk<MODE> walk(args, s_off, s_tile, mb, cb, jobs);
+        GroupJob j;
+        int g = 0, g_end = -1;                               // the first of the next 16 blocks' words, the job's last word
+        uint32_t next_w = 0;                                 // the lane's block of A's 16
+        uint4 next_x[8];                                     // 16 blocks of rows lane + 32 i of B
+        auto load = [&]() {
+            if (g > g_end && walk.valid()) {
+                j = walk.get();
+                g = first_stage(j) >> 2;
+                g_end = (end_stage(j) - 1) >> 2;
+            }
+            if (g > g_end) return;
+            const int b = 16 * (g >> 2), nb = min(16, args.blocks - b), m_block = j.m0 / 128 + (int)rank;
+            next_w = 127u;
+            if (lane < nb && m_block < m_blocks) next_w = args.ws[walk.e * args.sse + m_block * args.sso + (b + lane) * args.ssi];
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    x[i] = 0;
-                    if (lane + 32 * i >= j.n) continue;
-                    const uint8_t *p = args.xs + (int64_t)(j.c0 + lane + 32 * i) * args.ldxs + b;
-                    if (nb == 4) {
-                        x[i] = *reinterpret_cast<const uint32_t *>(p);
-                    } else {
-                        for (int k = 0; k < nb; ++k) x[i] |= (uint32_t)p[k] << (8 * k);
-                    }
+            for (int i = 0; i < 8; ++i) {
+                next_x[i] = make_uint4(0, 0, 0, 0);
+                if (lane + 32 * i >= j.n) continue;
+                const uint8_t *p = args.xs + (int64_t)(j.c0 + lane + 32 * i) * args.ldxs + b;
+                if (args.xs16 && nb == 16) {
+                    next_x[i] = *reinterpret_cast<const uint4 *>(p);
+                    continue;
                 }
+                uint32_t x[4] = {};
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    if (4 * k + 4 <= nb) x[k] = *reinterpret_cast<const uint32_t *>(p + 4 * k);
+                    else
+                        for (int q = 4 * k; q < nb; ++q) x[k] |= (uint32_t)p[q] << (8 * (q & 3));
+                }
+                next_x[i] = make_uint4(x[0], x[1], x[2], x[3]);
+            }
+        };
+        load();
+        while (g <= g_end && ok) {
+            const uint32_t aw = next_w << (8 * (lane & 3));
+            const int from = g & 3, to = min(3, g_end - (g & ~3));
+            uint4 x[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) x[i] = next_x[i];
+            g = (g | 3) + 1;
+            if (g > g_end) walk.next();
+            load();
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                if (k < from || k > to) continue;
+                const uint32_t w = __reduce_or_sync(0xffffffffu, (lane >> 2) == k ? aw : 0u);
                 if (!pair_wait(smem_u32(sempty + sf.slot), sf.phase ^ 1, abort_flag, args.status, 68)) {
                     ok = false;
                     break;
                 }
+                auto word = [&](int i) { return k == 0 ? x[i].x : k == 1 ? x[i].y : k == 2 ? x[i].z : x[i].w; };
                 uint4 *at = reinterpret_cast<uint4 *>(smem + SM::OFF_SF + sf.slot * GT_SF_BYTES) + lane;
                 at[0] = make_uint4(w, w, w, w);
-                at[32] = make_uint4(x[0], x[1], x[2], x[3]);
-                at[64] = make_uint4(x[4], x[5], x[6], x[7]);
+                at[32] = make_uint4(word(0), word(1), word(2), word(3));
+                at[64] = make_uint4(word(4), word(5), word(6), word(7));
                 fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0) mbar_arrive_cluster(sfull0 + sf.slot * 8);
+                ++used;
+                sf.next();
             }
         }
         // the last releases of this CTA's slots land before it may exit

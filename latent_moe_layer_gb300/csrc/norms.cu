@@ -9,7 +9,7 @@
 //   dy    = rs(y) (gain s - y' mean(gain s y'))
 // The means are computed again from y and h, which the gradient reads anyway: nothing is kept for it but h.  rms_norm
 // is the second half alone (h = x given).
-#include "experts.h"
+#include "glu.cuh"
 
 namespace k3 {
 
@@ -34,34 +34,40 @@ __device__ __forceinline__ void norm_cp16(void *dst, const void *src)
                  : "memory");
 }
 
-// V gains from element i.
+// Gains of the pairs j, j + 1 of V elements from element i (V = 1: the element and nothing).
 template <class T, int V>
-__device__ __forceinline__ void load_gain(const void *p, int f32, int i, float (&g)[V])
+__device__ __forceinline__ void load_gain(const void *p, int f32, int i, F2 (&g)[(V + 1) / 2])
 {
     if (!p) {
 #pragma unroll
-        for (int j = 0; j < V; ++j) g[j] = 1.0f;
+        for (int j = 0; j < (V + 1) / 2; ++j) g[j] = f2(1.0f);
     } else if (f32) {
         const float *q = static_cast<const float *>(p) + i;
         if constexpr (V % 4 == 0) {
 #pragma unroll
             for (int j = 0; j < V; j += 4) {
                 const float4 x = __ldg(reinterpret_cast<const float4 *>(q + j));
-                g[j] = x.x, g[j + 1] = x.y, g[j + 2] = x.z, g[j + 3] = x.w;
+                g[j / 2] = {x.x, x.y}, g[j / 2 + 1] = {x.z, x.w};
             }
         } else {
-            g[0] = __ldg(q);
+            g[0] = {__ldg(q), 0.0f};
         }
     } else {
         const Vec<T, V> x = *reinterpret_cast<const Vec<T, V> *>(static_cast<const T *>(p) + i);
 #pragma unroll
         for (int j = 0; j < V; j += 2) {
             const float2 e = x.get2(j);
-            g[j] = e.x;
-            if (V > 1) g[(j + 1) % V] = e.y;
+            g[j / 2] = {e.x, e.y};
         }
     }
 }
+template <class T, int V>
+__device__ __forceinline__ F2 pair_of(const Vec<T, V> &v, int j)
+{
+    const float2 e = v.get2(j);
+    return {e.x, e.y};
+}
+__device__ __forceinline__ F2 neg2(F2 a) { return {-a.x, -a.y}; }
 
 // Sums over the threads of a row (its warps of the CTA, all of them in the same order: every thread gets the same bits).
 // Two buffers in turn, so that one barrier a sum is enough.
@@ -88,123 +94,141 @@ __device__ __forceinline__ void row_sum(float (&v)[N], int group, float *buf, in
         for (int i = 0; i < N; ++i) v[i] += __shfl_xor_sync(0xffffffffu, v[i], o);
 }
 
-// Whether the next row's pieces fit in shared memory (not those of the widest fp32 rows).
-template <int V, int SLOTS>
-constexpr bool norm_ring() { return V > 1 && SLOTS * 16 + 1024 <= kMaxSmem; }
+// The inputs in the order of their slots, NULL where there is none: read from the arguments (constant memory) where they are
+// used, as registers are what a gradient is short of.
+template <bool GRAD>
+__device__ __forceinline__ const void *norm_src(const NormArgs &a, int k)
+{
+    if (GRAD) return k == 0 ? a.dn : k == 1 ? a.hin : k == 2 ? a.dh : k == 3 ? a.y : a.gate_kind == NORM_GATE_FULL ? a.gate : nullptr;
+    return k == 0 ? a.y : k == 1 ? a.res : a.gate_kind == NORM_GATE_FULL ? a.gate : nullptr;
+}
+template <bool GRAD>
+__device__ __forceinline__ int64_t norm_ld(const NormArgs &a, int k)
+{
+    if (GRAD) return k == 0 ? a.ld_dn : k == 1 ? a.ld_hin : k == 2 ? a.ld_dh : k == 3 ? a.ld_y : a.ld_gate;
+    return k == 0 ? a.ld_y : k == 1 ? a.ld_res : a.ld_gate;
+}
+
+// Rows' pieces that a thread keeps in flight in shared memory: two rows where they fit, else one or none (wide fp32 rows).
+template <int V, int BYTES>
+constexpr int norm_slots() { return V == 1 ? 0 : std::min(2, (kMaxSmem - 1024) / BYTES); }
 
 // A group of threads holds a row in registers, P pieces of V elements a thread, and walks over the rows.  With 16-byte
-// pieces every thread copies its pieces of the next row into shared memory (its own slots: nothing is synchronised) as
-// soon as all of this row's are in registers.
+// pieces every thread copies its pieces of the next row into shared memory (its own slots: nothing is synchronised): with
+// two slots while this row is worked on, with one as soon as this row is in registers.
 template <class T, int V, int P, bool GRAD, bool POST, int MAXT, int CTAS>
 __global__ void __launch_bounds__(MAXT, CTAS) norm_kernel(const NormArgs a)
 {
     griddep_enter();
-    constexpr int NIN = GRAD ? (POST ? 5 : 3) : (POST ? 3 : 1);
-    constexpr bool RING = norm_ring<V, NIN * P * MAXT>();
+    constexpr int NIN = GRAD ? (POST ? 5 : 3) : (POST ? 3 : 1), H = (V + 1) / 2;
+    constexpr int SLOTS = norm_slots<V, NIN * P * MAXT * 16>();
     extern __shared__ uint4 ring[];
     __shared__ float buf[2 * 32 * 3];
     const int group = a.group, g = (int)threadIdx.x / group, t = (int)threadIdx.x - g * group;
     const int per = (int)blockDim.x / group, pieces = a.D / V;
     int turn = 0;
-    // the inputs in the order of their slots, NULL where there is none
-    const void *src[NIN];
-    int64_t ld[NIN];
-    if constexpr (GRAD) {
-        src[0] = a.dn, ld[0] = a.ld_dn;
-        src[1] = a.hin, ld[1] = a.ld_hin;
-        src[2] = a.dh, ld[2] = a.ld_dh;
-        if constexpr (POST) {
-            src[3] = a.y, ld[3] = a.ld_y;
-            src[4] = a.gate_kind == NORM_GATE_FULL ? a.gate : nullptr, ld[4] = a.ld_gate;
-        }
-    } else {
-        src[0] = a.y, ld[0] = a.ld_y;
-        if constexpr (POST) {
-            src[1] = a.res, ld[1] = a.ld_res;
-            src[2] = a.gate_kind == NORM_GATE_FULL ? a.gate : nullptr, ld[2] = a.ld_gate;
-        }
-    }
     auto piece = [&](int p) { return p * group + t; };
-    auto slot = [&](int k, int p) { return ring + (k * P + p) * blockDim.x + threadIdx.x; };
-    auto fetch = [&](int64_t row) {
-        if constexpr (RING) {
-            if (row < a.rows) {
+    auto slot = [&](int s, int k, int p) { return ring + ((s * NIN + k) * P + p) * blockDim.x + threadIdx.x; };
+    auto fetch = [&](int64_t row, int s) {
+        if (row < a.rows) {
 #pragma unroll
-                for (int k = 0; k < NIN; ++k)
-                    if (src[k])
+            for (int k = 0; k < NIN; ++k)
+                if (norm_src<GRAD>(a, k))
 #pragma unroll
-                        for (int p = 0; p < P; ++p)
-                            if (piece(p) < pieces) norm_cp16(slot(k, p), static_cast<const T *>(src[k]) + row * ld[k] + piece(p) * V);
-            }
-            asm volatile("cp.async.commit_group;" ::: "memory");
+                    for (int p = 0; p < P; ++p)
+                        if (piece(p) < pieces) norm_cp16(slot(s, k, p), static_cast<const T *>(norm_src<GRAD>(a, k)) + row * norm_ld<GRAD>(a, k) + piece(p) * V);
         }
+        asm volatile("cp.async.commit_group;" ::: "memory");
     };
-    float acc[GRAD ? 2 : 1][GRAD ? P * V : 1] = {};
+    F2 acc[GRAD ? 2 : 1][GRAD ? P : 1][H] = {};
     const int64_t step = (int64_t)gridDim.x * per;
-    fetch((int64_t)blockIdx.x * per + g);
+    int at = 0;                                              // the slot of this row
+    if (SLOTS > 0) fetch((int64_t)blockIdx.x * per + g, 0);
     for (int64_t base = (int64_t)blockIdx.x * per; base < a.rows; base += step) {
         const int64_t row = base + g;
         const bool on = row < a.rows;
-        Vec<T, V> in[NIN][P] = {};
-        if constexpr (RING) asm volatile("cp.async.wait_group 0;" ::: "memory");
+        // the row's pieces: in their slot while the next row's are copied into the other, else in registers
+        constexpr bool HELD = SLOTS != 2;
+        Vec<T, V> held[HELD ? NIN : 1][HELD ? P : 1] = {};
+        if constexpr (SLOTS == 2) {
+            fetch(row + step, at ^ 1);
+            asm volatile("cp.async.wait_group 1;" ::: "memory");
+        } else if constexpr (SLOTS == 1) {
+            asm volatile("cp.async.wait_group 0;" ::: "memory");
+        }
+        if constexpr (HELD) {
 #pragma unroll
-        for (int k = 0; k < NIN; ++k)
-            if (src[k] && on)
+            for (int k = 0; k < NIN; ++k)
+                if (norm_src<GRAD>(a, k) && on)
 #pragma unroll
-                for (int p = 0; p < P; ++p)
-                    if (piece(p) < pieces) {
-                        if constexpr (RING) in[k][p] = *reinterpret_cast<const Vec<T, V> *>(slot(k, p));
-                        else in[k][p] = *reinterpret_cast<const Vec<T, V> *>(static_cast<const T *>(src[k]) + row * ld[k] + piece(p) * V);
-                    }
+                    for (int p = 0; p < P; ++p)
+                        if (piece(p) < pieces) {
+                            if constexpr (SLOTS > 0) held[k][p] = *reinterpret_cast<const Vec<T, V> *>(slot(0, k, p));
+                            else held[k][p] = *reinterpret_cast<const Vec<T, V> *>(static_cast<const T *>(norm_src<GRAD>(a, k)) + row * norm_ld<GRAD>(a, k) + piece(p) * V);
+                        }
+        }
+        auto in = [&](int k, int p) {
+            if constexpr (HELD) {
+                return held[k][p];
+            } else {
+                Vec<T, V> v = {};
+                if (norm_src<GRAD>(a, k) && on && piece(p) < pieces) v = *reinterpret_cast<const Vec<T, V> *>(slot(at, k, p));
+                return v;
+            }
+        };
+        const bool full = POST && a.gate_kind == NORM_GATE_FULL;
         const float row_gate = POST && a.gate_kind == NORM_GATE_ROW && on ? static_cast<const float *>(a.gate)[row] : 1.0f;
         auto put = [&](void *out, int64_t ldo, int p, const Vec<T, V> &v) {
             if (on && piece(p) < pieces) *reinterpret_cast<Vec<T, V> *>(static_cast<T *>(out) + row * ldo + piece(p) * V) = v;
         };
+        // Sums are of pairs; a pair's second half is 0 where V is 1.  Pieces past the row's end are zeros.
         if constexpr (!GRAD) {
-            float ss[1] = {};
+            F2 sq = f2(0.0f);
 #pragma unroll
-            for (int p = 0; p < P; ++p)
+            for (int p = 0; p < P; ++p) {
+                const Vec<T, V> yv = in(0, p);
 #pragma unroll
-                for (int j = 0; j < V; j += 2) {
-                    const float2 y = in[0][p].get2(j);
-                    ss[0] = fmaf(y.x, y.x, fmaf(y.y, y.y, ss[0]));
+                for (int j = 0; j < H; ++j) {
+                    const F2 y = pair_of(yv, 2 * j);
+                    sq = fma2(y, y, sq);
                 }
+            }
+            float ss[1] = {sq.x + sq.y};
             row_sum(ss, group, buf, turn);
-            fetch(row + step);
-            float r = rsqrtf(fmaf(ss[0], a.inv_d, a.eps));
+            if (SLOTS == 1) fetch(row + step, 0);
+            F2 r = f2(rsqrtf(fmaf(ss[0], a.inv_d, a.eps)));
             if constexpr (POST) {
-                float h[P][V];
-                float s2[1] = {};
+                F2 h[P][H], s2 = f2(0.0f);
+                const F2 scale = f2(a.scale), rg = f2(row_gate);
 #pragma unroll
                 for (int p = 0; p < P; ++p) {
-                    float gain[V];
+                    F2 gain[H] = {};
                     if (piece(p) < pieces) load_gain<T, V>(a.gain, a.gain_f32, piece(p) * V, gain);
+                    const Vec<T, V> yv = in(0, p), xv = in(1, p), mv = in(2, p);
                     Vec<T, V> o;
 #pragma unroll
-                    for (int j = 0; j < V; j += 2) {
-                        const int k = V == 1 ? 0 : j + 1;
-                        const float2 y = in[0][p].get2(j), x = in[1][p].get2(j), m = in[2][p].get2(j);
-                        const bool full = a.gate_kind == NORM_GATE_FULL;
-                        const float h1 = fmaf(a.scale, x.y, (full ? m.y : row_gate) * (y.y * r * gain[k]));
-                        h[p][k] = h1;
-                        h[p][j] = fmaf(a.scale, x.x, (full ? m.x : row_gate) * (y.x * r * gain[j]));
-                        o.set2(j, h[p][j], h1);
-                        if (piece(p) < pieces) s2[0] = fmaf(h[p][j], h[p][j], V > 1 ? fmaf(h1, h1, s2[0]) : s2[0]);
+                    for (int j = 0; j < H; ++j) {
+                        const F2 n = mul2(mul2(pair_of(yv, 2 * j), r), gain[j]);
+                        const F2 m = full ? pair_of(mv, 2 * j) : rg;
+                        h[p][j] = fma2(m, n, mul2(scale, pair_of(xv, 2 * j)));
+                        o.set2(2 * j, h[p][j].x, h[p][j].y);
+                        s2 = fma2(h[p][j], h[p][j], s2);
                     }
                     put(a.h, a.ld_h, p, o);
                 }
                 if (a.next) {
-                    row_sum(s2, group, buf, turn);
-                    r = rsqrtf(fmaf(s2[0], a.inv_d, a.eps));
+                    float s[1] = {s2.x + s2.y};
+                    row_sum(s, group, buf, turn);
+                    r = f2(rsqrtf(fmaf(s[0], a.inv_d, a.eps)));
 #pragma unroll
                     for (int p = 0; p < P; ++p) {
-                        float gain[V];
+                        F2 gain[H] = {};
                         if (piece(p) < pieces) load_gain<T, V>(a.next_gain, a.gain_f32, piece(p) * V, gain);
                         Vec<T, V> o;
 #pragma unroll
-                        for (int j = 0; j < V; j += 2) {
-                            const int k = V == 1 ? 0 : j + 1;
-                            o.set2(j, h[p][j] * r * gain[j], h[p][k] * r * gain[k]);
+                        for (int j = 0; j < H; ++j) {
+                            const F2 n = mul2(mul2(h[p][j], r), gain[j]);
+                            o.set2(2 * j, n.x, n.y);
                         }
                         put(a.n, a.ld_n, p, o);
                     }
@@ -212,103 +236,116 @@ __global__ void __launch_bounds__(MAXT, CTAS) norm_kernel(const NormArgs a)
             } else {
 #pragma unroll
                 for (int p = 0; p < P; ++p) {
-                    float gain[V];
+                    F2 gain[H] = {};
                     if (piece(p) < pieces) load_gain<T, V>(a.next_gain, a.gain_f32, piece(p) * V, gain);
+                    const Vec<T, V> xv = in(0, p);
                     Vec<T, V> o;
 #pragma unroll
-                    for (int j = 0; j < V; j += 2) {
-                        const int k = V == 1 ? 0 : j + 1;
-                        const float2 x = in[0][p].get2(j);
-                        o.set2(j, x.x * r * gain[j], x.y * r * gain[k]);
+                    for (int j = 0; j < H; ++j) {
+                        const F2 n = mul2(mul2(pair_of(xv, 2 * j), r), gain[j]);
+                        o.set2(2 * j, n.x, n.y);
                     }
                     put(a.n, a.ld_n, p, o);
                 }
             }
         } else {
             // mean squares of h and y, and <next_gain dn, h>
-            float s[3] = {};
+            F2 hh = f2(0.0f), dh = f2(0.0f), yy = f2(0.0f);
 #pragma unroll
             for (int p = 0; p < P; ++p) {
                 if (a.next) {
-                    float gain[V];
+                    F2 gain[H] = {};
                     if (piece(p) < pieces) load_gain<T, V>(a.next_gain, a.gain_f32, piece(p) * V, gain);
+                    const Vec<T, V> dv = in(0, p), hv = in(1, p);
 #pragma unroll
-                    for (int j = 0; j < V; j += 2) {
-                        const float2 d = in[0][p].get2(j), h = in[1][p].get2(j);
-                        s[0] = fmaf(h.x, h.x, fmaf(h.y, h.y, s[0]));
-                        if (piece(p) < pieces) s[1] = fmaf(d.x * gain[j], h.x, V > 1 ? fmaf(d.y * gain[(j + 1) % V], h.y, s[1]) : s[1]);
+                    for (int j = 0; j < H; ++j) {
+                        const F2 h = pair_of(hv, 2 * j);
+                        hh = fma2(h, h, hh);
+                        dh = fma2(mul2(pair_of(dv, 2 * j), gain[j]), h, dh);
                     }
                 }
-                if constexpr (POST)
+                if constexpr (POST) {
+                    const Vec<T, V> yv = in(3, p);
 #pragma unroll
-                    for (int j = 0; j < V; j += 2) {
-                        const float2 y = in[3][p].get2(j);
-                        s[2] = fmaf(y.x, y.x, fmaf(y.y, y.y, s[2]));
+                    for (int j = 0; j < H; ++j) {
+                        const F2 y = pair_of(yv, 2 * j);
+                        yy = fma2(y, y, yy);
                     }
+                }
             }
+            float s[3] = {hh.x + hh.y, dh.x + dh.y, yy.x + yy.y};
             row_sum(s, group, buf, turn);
-            fetch(row + step);
-            const float rh = a.next ? rsqrtf(fmaf(s[0], a.inv_d, a.eps)) : 0.0f, mh = s[1] * a.inv_d * rh * rh;
+            if (SLOTS == 1) fetch(row + step, 0);
+            const float rh = a.next ? rsqrtf(fmaf(s[0], a.inv_d, a.eps)) : 0.0f;
             const float ry = POST ? rsqrtf(fmaf(s[2], a.inv_d, a.eps)) : 0.0f;
-            float u[1] = {};
-            float gt[POST ? P : 1][V];                   // gain t, before the gate
+            const F2 rh2 = f2(rh), ry2 = f2(ry), mh = f2(-s[1] * a.inv_d * rh * rh), scale = f2(a.scale), rg = f2(row_gate);
+            F2 us = f2(0.0f), gt[POST ? P : 1][H];               // gain gate t (a gate by row comes in at the end)
 #pragma unroll
             for (int p = 0; p < P; ++p) {
-                float gain[V], post[V];
-                if (a.next && piece(p) < pieces) load_gain<T, V>(a.next_gain, a.gain_f32, piece(p) * V, gain);
-                if (POST && piece(p) < pieces) load_gain<T, V>(a.gain, a.gain_f32, piece(p) * V, post);
-                Vec<T, V> o, og;
+                F2 v[H];
+                const Vec<T, V> ev = in(2, p);
 #pragma unroll
-                for (int j = 0; j < V; j += 2) {
-                    float w[2], wg[2] = {};
-                    const float2 d = in[0][p].get2(j), h = in[1][p].get2(j), e = in[2][p].get2(j);
+                for (int j = 0; j < H; ++j) v[j] = pair_of(ev, 2 * j);
+                if (a.next) {
+                    F2 gain[H] = {};
+                    if (piece(p) < pieces) load_gain<T, V>(a.next_gain, a.gain_f32, piece(p) * V, gain);
+                    const Vec<T, V> dv = in(0, p), hv = in(1, p);
 #pragma unroll
-                    for (int i = 0; i < (V == 1 ? 1 : 2); ++i) {
-                        float v = i ? e.y : e.x;
-                        if (a.next) {
-                            const float dn = i ? d.y : d.x, hv = i ? h.y : h.x;
-                            v += rh * fmaf(-hv, mh, dn * gain[j + i]);
-                            acc[1][p * V + j + i] = fmaf(dn, hv * rh, acc[1][p * V + j + i]);
-                        }
-                        if constexpr (POST) {
-                            const float2 yy = in[3][p].get2(j), mm = in[4][p].get2(j);
-                            const float yh = (i ? yy.y : yy.x) * ry, m = a.gate_kind == NORM_GATE_FULL ? (i ? mm.y : mm.x) : row_gate;
-                            w[i] = a.scale * v;
-                            acc[0][p * V + j + i] = fmaf(m * v, yh, acc[0][p * V + j + i]);
-                            if (piece(p) < pieces) {
-                                const float q = post[j + i] * v;
-                                wg[i] = q * yh;
-                                const float c = a.gate_kind == NORM_GATE_FULL ? m * q : q;
-                                gt[p][j + i] = c;
-                                u[0] = fmaf(c, yh, u[0]);
-                            }
-                        } else {
-                            w[i] = v;
-                        }
+                    for (int j = 0; j < H; ++j) {
+                        const F2 dn = pair_of(dv, 2 * j), h = pair_of(hv, 2 * j);
+                        v[j] = fma2(rh2, fma2(h, mh, mul2(dn, gain[j])), v[j]);
+                        acc[1][p][j] = fma2(dn, mul2(h, rh2), acc[1][p][j]);
                     }
-                    o.set2(j, w[0], V == 1 ? 0.0f : w[1 % (V == 1 ? 1 : 2)]);
-                    if (POST) og.set2(j, wg[0], wg[1]);
+                }
+                Vec<T, V> o;
+                if constexpr (POST) {
+                    // what follows is loaded after that is done, for its registers
+                    asm volatile("" ::: "memory");
+                    F2 gain[H] = {};
+                    if (piece(p) < pieces) load_gain<T, V>(a.gain, a.gain_f32, piece(p) * V, gain);
+                    const Vec<T, V> yv = in(3, p), mv = in(4, p);
+                    Vec<T, V> og;
+#pragma unroll
+                    for (int j = 0; j < H; ++j) {
+                        const F2 yh = mul2(pair_of(yv, 2 * j), ry2), w = mul2(scale, v[j]), q = mul2(gain[j], v[j]);
+                        o.set2(2 * j, w.x, w.y);
+                        if (full) {
+                            const F2 m = pair_of(mv, 2 * j), wg = mul2(q, yh);
+                            og.set2(2 * j, wg.x, wg.y);
+                            acc[0][p][j] = fma2(mul2(m, v[j]), yh, acc[0][p][j]);
+                            gt[p][j] = mul2(m, q);
+                        } else {
+                            acc[0][p][j] = fma2(mul2(rg, v[j]), yh, acc[0][p][j]);
+                            gt[p][j] = q;
+                        }
+                        us = fma2(gt[p][j], yh, us);
+                    }
+                    if (full) put(a.dgate, a.ld_dgate, p, og);
+                } else {
+#pragma unroll
+                    for (int j = 0; j < H; ++j) o.set2(2 * j, v[j].x, v[j].y);
                 }
                 put(a.n, a.ld_n, p, o);
-                if (POST && a.gate_kind == NORM_GATE_FULL) put(a.dgate, a.ld_dgate, p, og);
             }
             if constexpr (POST) {
+                float u[1] = {us.x + us.y};
                 row_sum(u, group, buf, turn);
                 if (a.gate_kind == NORM_GATE_ROW && t == 0 && on) static_cast<float *>(a.dgate)[row] = u[0];
-                const float m = u[0] * a.inv_d * ry, f = a.gate_kind == NORM_GATE_ROW ? row_gate * ry : ry;
+                const F2 m = f2(-u[0] * a.inv_d * ry), f = f2(row_gate * ry);
 #pragma unroll
                 for (int p = 0; p < P; ++p) {
+                    const Vec<T, V> yv = in(3, p);
                     Vec<T, V> o;
 #pragma unroll
-                    for (int j = 0; j < V; j += 2) {
-                        const int k = V == 1 ? 0 : j + 1;
-                        const float2 y = in[3][p].get2(j);
-                        o.set2(j, f * fmaf(-y.x, m, gt[p][j]), f * fmaf(-y.y, m, gt[p][k]));
+                    for (int j = 0; j < H; ++j) {
+                        const F2 d = mul2(f, fma2(pair_of(yv, 2 * j), m, gt[p][j]));
+                        o.set2(2 * j, d.x, d.y);
                     }
                     put(a.h, a.ld_h, p, o);
                 }
             }
         }
+        if (SLOTS == 2) at ^= 1;
     }
     if constexpr (GRAD) {
         // rows that are not there added nothing
@@ -321,7 +358,10 @@ __global__ void __launch_bounds__(MAXT, CTAS) norm_kernel(const NormArgs a)
                 if (piece(p) >= pieces) continue;
                 float *o = a.part + (k * groups + mine) * a.D + piece(p) * V;
 #pragma unroll
-                for (int j = 0; j < V; ++j) o[j] = acc[k][p * V + j];
+                for (int j = 0; j < H; ++j) {
+                    o[2 * j] = acc[k][p][j].x;
+                    if (V > 1) o[2 * j + 1] = acc[k][p][j].y;
+                }
             }
         }
     }
@@ -347,30 +387,26 @@ __global__ void __launch_bounds__(512) norm_gain_kernel(const float *part, int g
     }
 }
 
-// Threads a row and rows a CTA: 16 elements a thread (a warp where a row has at most 512).
-constexpr int NORM_ELEMS = 16;
-static int norm_group(int D) { return std::max(32, (int)(((int64_t)D + 32 * NORM_ELEMS - 1) / (32 * NORM_ELEMS)) * 32); }
+// Elements a thread: 16 forwards; 8 for the gradients' up to 8192 columns, which keep five inputs, sums of two gains and twice
+// the gains in registers (7168 columns, 8 a thread: 896 threads of 72 registers).  Where pieces are single elements, 16.
+static int norm_group(int D, int elems) { return std::max(32, (D + 32 * elems - 1) / (32 * elems) * 32); }
 static int norm_rows(int group) { return group >= 128 ? 1 : 256 / group; }
-// Row groups of a gradient's grid at most, each with sums of its own.
-static int64_t norm_groups(int64_t rows, int D)
-{
-    const int per = norm_rows(norm_group(D));
-    return std::min<int64_t>((rows + per - 1) / per, per > 1 ? 304 : 608) * per;
-}
+// Row groups of a gradient's grid at most, each with sums of its own; a CTA has at most 8.
+static int64_t norm_groups(int64_t rows) { return std::min<int64_t>((rows + 7) / 8 * 8, 8 * 304); }
 
-template <class T, int V, bool GRAD, bool POST, int MAXT>
+template <class T, int V, int ELEMS, bool GRAD, bool POST, int MAXT, int CTAS>
 static int launch_norm(NormArgs a, float *dgain, float *dnext, cudaStream_t st)
 {
-    constexpr int P = NORM_ELEMS / V;
+    constexpr int P = ELEMS / V;
     constexpr int NIN = GRAD ? (POST ? 5 : 3) : (POST ? 3 : 1);
-    constexpr int CTAS = GRAD || MAXT > 512 ? 1 : 2;
+    constexpr int SLOTS = norm_slots<V, NIN * P * MAXT * 16>();
     auto kern = norm_kernel<T, V, P, GRAD, POST, MAXT, CTAS>;
+    a.group = norm_group(a.D, ELEMS);
     const int per = norm_rows(a.group), threads = a.group * per, sms = k3_num_sms();
     if (!sms) return K3MOE_ERR_CUDA;
-    constexpr bool RING = norm_ring<V, NIN * P * MAXT>();
-    const int smem = RING ? NIN * P * threads * 16 : 0;
+    const int smem = SLOTS * NIN * P * threads * 16;
     static unsigned long long attr_set = 0;
-    if (RING && !k3_smem_attr(kern, NIN * P * MAXT * 16, attr_set)) return K3MOE_ERR_CUDA;
+    if (SLOTS && !k3_smem_attr(kern, SLOTS * NIN * P * MAXT * 16, attr_set)) return K3MOE_ERR_CUDA;
     static int fits[33] = {};                            // CTAs an SM by warps a row
     int fit = fits[a.group / 32];
     if (!fit) {
@@ -378,7 +414,7 @@ static int launch_norm(NormArgs a, float *dgain, float *dnext, cudaStream_t st)
         fits[a.group / 32] = fit;
     }
     int64_t grid = std::min<int64_t>(((int64_t)a.rows + per - 1) / per, (int64_t)fit * sms);
-    if (GRAD) grid = std::min<int64_t>(grid, norm_groups(a.rows, a.D) / per);
+    if (GRAD) grid = std::min<int64_t>(grid, norm_groups(a.rows) / per);
     if (grid > 0) {
         k3_launch(kern, dim3((unsigned)grid), threads, smem, st, a);
         k3_note_launch();
@@ -391,26 +427,35 @@ static int launch_norm(NormArgs a, float *dgain, float *dnext, cudaStream_t st)
     return cudaGetLastError() == cudaSuccess ? K3MOE_OK : K3MOE_ERR_CUDA;
 }
 
-template <class T, int V, bool GRAD>
-static int launch_sized(const NormArgs &a, bool post, float *dgain, float *dnext, cudaStream_t st)
+template <class T, int V, bool GRAD, bool POST>
+static int launch_sized(const NormArgs &a, float *dgain, float *dnext, cudaStream_t st)
 {
-    if constexpr (V > 1)
-        if (a.group <= 512)
-            return post ? launch_norm<T, V, GRAD, true, 512>(a, dgain, dnext, st) : launch_norm<T, V, GRAD, false, 512>(a, dgain, dnext, st);
-    return post ? launch_norm<T, V, GRAD, true, 1024>(a, dgain, dnext, st) : launch_norm<T, V, GRAD, false, 1024>(a, dgain, dnext, st);
+    if constexpr (V > 1 && GRAD) {
+        if (a.D <= 3584) return launch_norm<T, V, 8, true, POST, 448, 2>(a, dgain, dnext, st);
+        if (a.D <= 7168) return launch_norm<T, V, 8, true, POST, 896, 1>(a, dgain, dnext, st);
+        if (a.D <= 8192) return launch_norm<T, V, 8, true, POST, 1024, 1>(a, dgain, dnext, st);
+    } else if constexpr (V > 1) {
+        if (a.D <= 8192) return launch_norm<T, V, 16, false, POST, 512, 2>(a, dgain, dnext, st);
+    }
+    return launch_norm<T, V, 16, GRAD, POST, 1024, 1>(a, dgain, dnext, st);
+}
+
+template <class T, int V, bool GRAD>
+static int launch_post(const NormArgs &a, bool post, float *dgain, float *dnext, cudaStream_t st)
+{
+    return post ? launch_sized<T, V, GRAD, true>(a, dgain, dnext, st) : launch_sized<T, V, GRAD, false>(a, dgain, dnext, st);
 }
 
 template <bool GRAD>
 static int launch_typed(NormArgs a, bool post, int dtype, bool vec, float *dgain, float *dnext, cudaStream_t st)
 {
-    a.group = norm_group(a.D);
     a.inv_d = 1.0f / (float)a.D;
     if (dtype == K3MOE_TYPE_F32)
-        return vec ? launch_sized<float, 4, GRAD>(a, post, dgain, dnext, st) : launch_sized<float, 1, GRAD>(a, post, dgain, dnext, st);
+        return vec ? launch_post<float, 4, GRAD>(a, post, dgain, dnext, st) : launch_post<float, 1, GRAD>(a, post, dgain, dnext, st);
     if (dtype == K3MOE_TYPE_BF16)
-        return vec ? launch_sized<__nv_bfloat16, 8, GRAD>(a, post, dgain, dnext, st)
-                   : launch_sized<__nv_bfloat16, 1, GRAD>(a, post, dgain, dnext, st);
-    return vec ? launch_sized<__half, 8, GRAD>(a, post, dgain, dnext, st) : launch_sized<__half, 1, GRAD>(a, post, dgain, dnext, st);
+        return vec ? launch_post<__nv_bfloat16, 8, GRAD>(a, post, dgain, dnext, st)
+                   : launch_post<__nv_bfloat16, 1, GRAD>(a, post, dgain, dnext, st);
+    return vec ? launch_post<__half, 8, GRAD>(a, post, dgain, dnext, st) : launch_post<__half, 1, GRAD>(a, post, dgain, dnext, st);
 }
 
 // Checks shared by the calls.
@@ -513,7 +558,7 @@ extern "C" int k3moe_norm_residual(const void *y, int64_t ldy, const void *resid
 
 extern "C" size_t k3moe_norm_grad_workspace_bytes(int rows, int D)
 {
-    return rows < 0 || D < 1 || D > K3MOE_NORM_MAX_WIDTH ? 0 : (size_t)std::max<int64_t>(1, norm_groups(rows, D)) * D * 2 * sizeof(float);
+    return rows < 0 || D < 1 || D > K3MOE_NORM_MAX_WIDTH ? 0 : (size_t)std::max<int64_t>(1, norm_groups(rows)) * D * 2 * sizeof(float);
 }
 
 extern "C" int k3moe_rms_norm_grad(const void *dy, int64_t lddy, const void *x, int64_t ldx, const void *gain, int gain_dtype,

@@ -6,7 +6,7 @@
 // where m is above 0.75: bits of amax, no logarithm.  x 2^-k is exact, so a code is rounded once.
 #include <cuda_fp8.h>
 
-#include "experts.h"
+#include "glu.cuh"
 
 namespace k3 {
 
@@ -14,16 +14,25 @@ template <int KIND> constexpr int F8_TOP = KIND == K3MOE_F8_E4M3 ? 9 : 16;
 
 template <class T> constexpr uint32_t INF16 = std::is_same<T, __half>::value ? 0x7C00u : 0x7F80u;
 
-// The largest finite size of eight values, two a word, as bits of T.
+// The largest finite size of eight values, as bits of T, and whether an infinity is among them.  The packed maximum passes
+// over NaN; where it is infinite (or all of a place's values are NaN) the values are looked at one by one.
 template <class T>
-__device__ __forceinline__ uint32_t amax_bits(const Vec<T, 8> &v)
+__device__ __forceinline__ uint32_t amax_bits(const Vec<T, 8> &v, bool &infinite)
 {
-    uint32_t m = 0;
+    using T2 = std::conditional_t<std::is_same<T, __half>::value, __half2, __nv_bfloat162>;
+    const T2 *p = reinterpret_cast<const T2 *>(v.w);
+    const T2 m2 = __hmax2(__hmax2(__habs2(p[0]), __habs2(p[1])), __hmax2(__habs2(p[2]), __habs2(p[3])));
+    const uint32_t w = *reinterpret_cast<const uint32_t *>(&m2);
+    uint32_t m = max(w & 0x7FFFu, w >> 16 & 0x7FFFu);
+    infinite = m >= INF16<T>;
+    if (infinite) {
+        m = 0;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const uint32_t lo = v.w[i] & 0x7FFFu, hi = v.w[i] >> 16 & 0x7FFFu;
-        m = max(m, lo < INF16<T> ? lo : 0u);
-        m = max(m, hi < INF16<T> ? hi : 0u);
+        for (int i = 0; i < 4; ++i) {
+            const uint32_t lo = v.w[i] & 0x7FFFu, hi = v.w[i] >> 16 & 0x7FFFu;
+            m = max(m, lo < INF16<T> ? lo : 0u);
+            m = max(m, hi < INF16<T> ? hi : 0u);
+        }
     }
     return m;
 }
@@ -44,25 +53,24 @@ __device__ __forceinline__ uint32_t scale_byte(float amax)
 // 2^-k; byte <= 247
 __device__ __forceinline__ float unscale(uint32_t byte) { return __uint_as_float((254u - byte) << 23); }
 
-// Two codes, the first in the low byte.  The conversion gives infinities the largest finite code: they become NaN (E4M3) or
-// stay infinite (E5M2).
-template <int KIND>
-__device__ __forceinline__ uint32_t code2(float x, float y)
-{
-    uint32_t c = (uint32_t)__nv_cvt_float2_to_fp8x2(make_float2(x, y), __NV_SATFINITE, KIND == K3MOE_F8_E4M3 ? __NV_E4M3 : __NV_E5M2);
-    if (fabsf(x) == __int_as_float(0x7F800000)) c = (c & 0xFF80u) | (KIND == K3MOE_F8_E4M3 ? 0x7Fu : 0x7Cu);
-    if (fabsf(y) == __int_as_float(0x7F800000)) c = (c & 0x80FFu) | (KIND == K3MOE_F8_E4M3 ? 0x7F00u : 0x7C00u);
-    return c;
-}
-
+// Eight codes.  The conversion gives infinities the largest finite code: they become NaN (E4M3) or stay infinite (E5M2).
 template <class T, int KIND>
-__device__ __forceinline__ uint2 codes8(const Vec<T, 8> &v, float f)
+__device__ __forceinline__ uint2 codes8(const Vec<T, 8> &v, float f, bool infinite)
 {
     uint32_t c[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         const float2 e = v.get2(2 * i);
-        c[i] = code2<KIND>(e.x * f, e.y * f);
+        const F2 x = mul2({e.x, e.y}, f2(f));
+        c[i] = (uint32_t)__nv_cvt_float2_to_fp8x2(make_float2(x.x, x.y), __NV_SATFINITE, KIND == K3MOE_F8_E4M3 ? __NV_E4M3 : __NV_E5M2);
+    }
+    if (infinite) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const uint32_t lo = v.w[i] & 0x7FFFu, hi = v.w[i] >> 16 & 0x7FFFu;
+            if (lo == INF16<T>) c[i] = (c[i] & 0xFF80u) | (KIND == K3MOE_F8_E4M3 ? 0x7Fu : 0x7Cu);
+            if (hi == INF16<T>) c[i] = (c[i] & 0x80FFu) | (KIND == K3MOE_F8_E4M3 ? 0x7F00u : 0x7C00u);
+        }
     }
     return make_uint2(c[0] | c[1] << 16, c[2] | c[3] << 16);
 }
@@ -97,40 +105,46 @@ struct QuantRows {
     int rows, n, blocks;
     uint8_t *codes, *scales;
     int vec_x, vec_c;
+    int64_t row_step;                                    // from a half-warp's block to its next: row_step rows and block_step
+    int block_step;                                      // blocks on, a row more where that is past the row's end
 };
 
-// Half a warp a block of 128, eight elements a lane, QR_UNROLL blocks in flight a half-warp.
-constexpr int QR_THREADS = 256, QR_UNROLL = 4;
+// Half a warp a block of 128, eight elements a lane, QR_UNROLL blocks in flight a half-warp.  The blocks are walked without a
+// division (with one a block, 65,536 x 3584 took 208 us).
+constexpr int QR_THREADS = 256, QR_UNROLL = 4, QR_CTAS = 5;
 template <class T, int KIND>
-__global__ void __launch_bounds__(QR_THREADS) quant_rows_kernel(const QuantRows a)
+__global__ void __launch_bounds__(QR_THREADS, QR_CTAS) quant_rows_kernel(const QuantRows a)
 {
     griddep_enter();
     const int lane = threadIdx.x & 15;
-    const int64_t total = (int64_t)a.rows * a.blocks;
-    const int64_t halves = (int64_t)gridDim.x * (QR_THREADS / 16);
-    const int64_t first = (int64_t)blockIdx.x * (QR_THREADS / 16) + (threadIdx.x >> 4);
+    const uint32_t first = blockIdx.x * (QR_THREADS / 16) + (threadIdx.x >> 4);
+    int64_t at = first / (uint32_t)a.blocks;             // the next block's row
+    int block = (int)(first - (uint32_t)at * (uint32_t)a.blocks);
     // whole warps take part in every round: a half without a block works on zeros
-    for (int64_t i0 = first; i0 - (first & 1) < total; i0 += halves * QR_UNROLL) {
+    while (__any_sync(0xffffffffu, at < a.rows)) {
         Vec<T, 8> v[QR_UNROLL];
         int64_t row[QR_UNROLL];
-        int block[QR_UNROLL], n[QR_UNROLL];
+        int col[QR_UNROLL], n[QR_UNROLL];
 #pragma unroll
         for (int u = 0; u < QR_UNROLL; ++u) {
-            const int64_t i = i0 + u * halves;
-            row[u] = i / a.blocks;
-            block[u] = (int)(i - row[u] * a.blocks);
-            n[u] = i < total ? max(0, min(8, a.n - block[u] * 128 - lane * 8)) : 0;
-            v[u] = load8<T>(static_cast<const T *>(a.x) + (n[u] > 0 ? row[u] * a.ldx + block[u] * 128 + lane * 8 : 0), n[u], a.vec_x);
+            row[u] = at;
+            col[u] = block * 128 + lane * 8;
+            n[u] = at < a.rows ? a.n - col[u] : 0;
+            v[u] = load8<T>(static_cast<const T *>(a.x) + (n[u] > 0 ? at * a.ldx + col[u] : 0), n[u], a.vec_x);
+            at += a.row_step;
+            block += a.block_step;
+            if (block >= a.blocks) block -= a.blocks, ++at;
         }
 #pragma unroll
         for (int u = 0; u < QR_UNROLL; ++u) {
-            uint32_t m = amax_bits<T>(v[u]);
+            bool infinite;
+            uint32_t m = amax_bits<T>(v[u], infinite);
 #pragma unroll
             for (int o = 8; o; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
             const uint32_t s = scale_byte<KIND>(from_bits<T>(m));
             if (n[u] > 0) {
-                store8(a.codes + row[u] * a.ldc + block[u] * 128 + lane * 8, codes8<T, KIND>(v[u], unscale(s)), n[u], a.vec_c);
-                if (lane == 0) a.scales[row[u] * a.lds + block[u]] = (uint8_t)s;
+                store8(a.codes + row[u] * a.ldc + col[u], codes8<T, KIND>(v[u], unscale(s), infinite), n[u], a.vec_c);
+                if (lane == 0) a.scales[row[u] * a.lds + (col[u] >> 7)] = (uint8_t)s;
             }
         }
     }
@@ -163,6 +177,7 @@ __global__ void __launch_bounds__(QW_THREADS) quant_weights_kernel(const QuantWe
     const int cols = max(0, min(8, a.K - k0 - cp * 8));
     Vec<T, 8> v[2][4];
     uint32_t m = 0;
+    bool infinite = false;
 #pragma unroll
     for (int h = 0; h < 2; ++h)
 #pragma unroll
@@ -173,7 +188,11 @@ __global__ void __launch_bounds__(QW_THREADS) quant_weights_kernel(const QuantWe
 #pragma unroll
     for (int h = 0; h < 2; ++h)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) m = max(m, amax_bits<T>(v[h][i]));
+        for (int i = 0; i < 4; ++i) {
+            bool inf;
+            m = max(m, amax_bits<T>(v[h][i], inf));
+            infinite |= inf;
+        }
     m = __reduce_max_sync(0xffffffffu, m);
     if ((threadIdx.x & 31) == 0) s_max[threadIdx.x >> 5] = m;
     __syncthreads();
@@ -188,7 +207,7 @@ __global__ void __launch_bounds__(QW_THREADS) quant_weights_kernel(const QuantWe
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const int r = n0 + 4 * (rg + 16 * h) + i;
-            c[i] = codes8<T, KIND>(v[h][i], f);
+            c[i] = codes8<T, KIND>(v[h][i], f, infinite);
             if (r < a.N && cols > 0) store8(a.codes + e * a.stride_c + r * a.ldc + k0 + cp * 8, c[i], cols, a.vec_c);
         }
         if (a.codes_t)
@@ -262,9 +281,11 @@ extern "C" int k3moe_quant8_rows(const void *x, int64_t ldx, int rows, int n, in
     if (rows == 0) return K3MOE_OK;
     const int sms = k3_num_sms();
     if (!sms) return K3MOE_ERR_CUDA;
-    const QuantRows a = {x, ldx, ldc, lds, rows, n, blocks, codes, scales, k3_rows16(x, ldx, dtype), bytes_by(codes, ldc, 0, 8)};
     const int64_t ctas = ((int64_t)rows * blocks + QR_THREADS / 16 - 1) / (QR_THREADS / 16);
-    const unsigned grid = (unsigned)std::min<int64_t>(ctas, 6 * (int64_t)sms);
+    const unsigned grid = (unsigned)std::min<int64_t>(ctas, QR_CTAS * (int64_t)sms);
+    const int64_t step = (int64_t)grid * (QR_THREADS / 16);
+    const QuantRows a = {x, ldx, ldc, lds, rows, n, blocks, codes, scales, k3_rows16(x, ldx, dtype), bytes_by(codes, ldc, 0, 8),
+                         step / blocks, (int)(step % blocks)};
     return by_type(dtype, kind, [&](auto t, auto k) {
         k3_launch(quant_rows_kernel<decltype(t), decltype(k)::value>, grid, QR_THREADS, 0, stream, a);
     });

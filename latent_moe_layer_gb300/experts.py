@@ -152,7 +152,7 @@ def quant8_rows(x, kind="e4m3", stream=None):
     ceil(n / 128)] uint8): a value is code 2^(scale - 127), a scale for each 128 columns of a row.
 
     The scale is the smallest power of two under which nothing saturates; a value that is not finite takes no part in
-    it and becomes NaN (e5m2 keeps infinities).  Rows of the results start on 16- and 4-byte boundaries."""
+    it and becomes NaN (e5m2 keeps infinities).  Rows of both results start on 16-byte boundaries."""
     return _call("quant8_rows", stream, x, kind)
 
 
