@@ -25,7 +25,7 @@ struct NormArgs {
     int rows, D, group;                                  // group: threads a row
     void *h, *n, *dgate;                                 // gradient: h = dy, n = dres (without POST: n = dx)
     int64_t ld_h, ld_n, ld_dgate;
-    float *part;                                         // [dgain, dnext_gain][row groups of the grid][D]
+    float *part;                                         // [dgain, dnext_gain][CTAs][D]
 };
 
 __device__ __forceinline__ void norm_cp16(void *dst, const void *src)
@@ -69,29 +69,65 @@ __device__ __forceinline__ F2 pair_of(const Vec<T, V> &v, int j)
 }
 __device__ __forceinline__ F2 neg2(F2 a) { return {-a.x, -a.y}; }
 
-// Sums over the threads of a row (its warps of the CTA, all of them in the same order: every thread gets the same bits).
-// Two buffers in turn, so that one barrier a sum is enough.
+// Sums of N values over a warp, all of them at once: the lanes split over the values as they halve (6 shuffles for four
+// values instead of 20).  Value i is left in lanes 8 i .. 8 i + 7 (N = 1: in all).
 template <int N>
-__device__ __forceinline__ void row_sum(float (&v)[N], int group, float *buf, int &turn)
+__device__ __forceinline__ float warp_sums(const float (&v)[N], int lane)
+{
+    float k;
+    if constexpr (N == 1) {
+        k = v[0];
+        k += __shfl_xor_sync(0xffffffffu, k, 16);
+        k += __shfl_xor_sync(0xffffffffu, k, 8);
+    } else {
+        const float v2 = N > 2 ? v[N > 2 ? 2 : 0] : 0.0f, v3 = N > 3 ? v[N > 3 ? 3 : 0] : 0.0f;
+        const bool high = lane & 16, odd = lane & 8;
+        const float k0 = (high ? v2 : v[0]) + __shfl_xor_sync(0xffffffffu, high ? v[0] : v2, 16);
+        const float k1 = (high ? v3 : v[1]) + __shfl_xor_sync(0xffffffffu, high ? v[1] : v3, 16);
+        k = (odd ? k1 : k0) + __shfl_xor_sync(0xffffffffu, odd ? k0 : k1, 8);
+    }
+    k += __shfl_xor_sync(0xffffffffu, k, 4);
+    k += __shfl_xor_sync(0xffffffffu, k, 2);
+    k += __shfl_xor_sync(0xffffffffu, k, 1);
+    return k;
+}
+template <int N>
+__device__ __forceinline__ void spread_sums(float k, float (&v)[N])
 {
 #pragma unroll
-    for (int o = 16; o; o >>= 1)
+    for (int i = 0; i < N; ++i) v[i] = N == 1 ? k : __shfl_sync(0xffffffffu, k, 8 * i);
+}
+
+// Sums over the threads of a row (its warps of the CTA, all of them in the same order: every thread gets the same bits).
+// Two buffers in turn, so that one barrier a sum is enough.
+template <bool ONE, int N>
+__device__ __forceinline__ void row_sum(float (&v)[N], int group, float4 *buf, int &turn)
+{
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    if (!ONE && group < 32) {
+        for (int o = group >> 1; o; o >>= 1)
 #pragma unroll
-        for (int i = 0; i < N; ++i) v[i] += __shfl_xor_sync(0xffffffffu, v[i], o);
-    if (group == 32) return;
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = group >> 5, first = (int)threadIdx.x / group * warps;
-    float *b = buf + turn * 32 * 3;
-    turn ^= 1;
-    if (lane == 0)
-#pragma unroll
-        for (int i = 0; i < N; ++i) b[warp * 3 + i] = v[i];
-    __syncthreads();
-#pragma unroll
-    for (int i = 0; i < N; ++i) v[i] = lane < warps ? b[(first + lane) * 3 + i] : 0.0f;
-#pragma unroll
-    for (int o = 16; o; o >>= 1)
-#pragma unroll
-        for (int i = 0; i < N; ++i) v[i] += __shfl_xor_sync(0xffffffffu, v[i], o);
+            for (int i = 0; i < N; ++i) v[i] += __shfl_xor_sync(0xffffffffu, v[i], o);
+        return;
+    }
+    float k = warp_sums(v, lane);
+    if (ONE || group > 32) {
+        const int warps = group >> 5, first = ONE ? 0 : (int)threadIdx.x / group * warps;
+        float4 *b = buf + turn * 32;
+        turn ^= 1;
+        if (N == 1 ? lane == 0 : (lane & 7) == 0) reinterpret_cast<float *>(b + warp)[N == 1 ? 0 : lane >> 3] = k;
+        __syncthreads();
+        float w[N] = {};
+        if (lane < warps) {
+            const float4 q = b[first + lane];
+            w[0] = q.x;
+            if constexpr (N > 1) w[1] = q.y;
+            if constexpr (N > 2) w[2] = q.z;
+            if constexpr (N > 3) w[3] = q.w;
+        }
+        k = warp_sums(w, lane);
+    }
+    spread_sums(k, v);
 }
 
 // The inputs in the order of their slots, NULL where there is none: read from the arguments (constant memory) where they are
@@ -109,25 +145,49 @@ __device__ __forceinline__ int64_t norm_ld(const NormArgs &a, int k)
     return k == 0 ? a.ld_y : k == 1 ? a.ld_res : a.ld_gate;
 }
 
+// Whether the rows of a call follow each other through steps of their own (see the gradient's loop); its gains are kept in
+// shared memory, as the two rows' pieces leave the L1 too little room for them (`slots`, `gains`: bytes of either).
+constexpr bool norm_piped(bool grad, bool post, bool one, int slots, int gains)
+{
+    return grad && post && one && 2 * slots + gains + 1024 <= kMaxSmem;
+}
 // Rows' pieces that a thread keeps in flight in shared memory: two rows where they fit, else one or none (wide fp32 rows).
 template <int V, int BYTES>
 constexpr int norm_slots() { return V == 1 ? 0 : std::min(2, (kMaxSmem - 1024) / BYTES); }
 
-// A group of threads holds a row in registers, P pieces of V elements a thread, and walks over the rows.  With 16-byte
-// pieces every thread copies its pieces of the next row into shared memory (its own slots: nothing is synchronised): with
-// two slots while this row is worked on, with one as soon as this row is in registers.
-template <class T, int V, int P, bool GRAD, bool POST, int MAXT, int CTAS>
+// A group of threads holds a row, P pieces of V elements a thread, and walks over the rows (ONE: the group is the CTA, so that
+// rows' addresses are the same for all its threads).  With 16-byte pieces every thread copies its pieces of the next row into
+// shared memory (its own slots: nothing is synchronised): with two slots while this row is worked on, with one as soon as
+// this row is in registers.
+template <class T, int V, int P, bool GRAD, bool POST, int MAXT, int CTAS, bool ONE>
 __global__ void __launch_bounds__(MAXT, CTAS) norm_kernel(const NormArgs a)
 {
     griddep_enter();
     constexpr int NIN = GRAD ? (POST ? 5 : 3) : (POST ? 3 : 1), H = (V + 1) / 2;
     constexpr int SLOTS = norm_slots<V, NIN * P * MAXT * 16>();
+    constexpr bool PIPED = V > 1 && norm_piped(GRAD, POST, ONE, NIN * P * MAXT * 16, 2 * P * V * MAXT * 4);
     extern __shared__ uint4 ring[];
-    __shared__ float buf[2 * 32 * 3];
-    const int group = a.group, g = (int)threadIdx.x / group, t = (int)threadIdx.x - g * group;
-    const int per = (int)blockDim.x / group, pieces = a.D / V;
+    __shared__ float4 buf[2 * 32];
+    const int group = ONE ? (int)blockDim.x : a.group, g = ONE ? 0 : (int)threadIdx.x / group, t = (int)threadIdx.x - g * group;
+    const int per = ONE ? 1 : (int)blockDim.x / group, pieces = a.D / V;
     int turn = 0;
     auto piece = [&](int p) { return p * group + t; };
+    auto gain_at = [&](int p) { return min(piece(p), pieces - 1) * V; };         // any gain where the elements are zeros
+    // PIPED: this thread's gains (0: gain, 1: next_gain), after the slots
+    auto gain_slot = [&](int k, int p, int q) {
+        return reinterpret_cast<float4 *>(ring + 2 * NIN * P * blockDim.x) + ((k * P + p) * (V / 4) + q) * blockDim.x + threadIdx.x;
+    };
+    auto gains = [&](int k, int p, F2 (&g)[H]) {
+        if constexpr (PIPED) {
+#pragma unroll
+            for (int q = 0; q < V / 4; ++q) {
+                const float4 x = *gain_slot(k, p, q);
+                g[2 * q] = {x.x, x.y}, g[2 * q + 1] = {x.z, x.w};
+            }
+        } else {
+            load_gain<T, V>(k ? a.next_gain : a.gain, a.gain_f32, gain_at(p), g);
+        }
+    };
     auto slot = [&](int s, int k, int p) { return ring + ((s * NIN + k) * P + p) * blockDim.x + threadIdx.x; };
     auto fetch = [&](int64_t row, int s) {
         if (row < a.rows) {
@@ -142,221 +202,305 @@ __global__ void __launch_bounds__(MAXT, CTAS) norm_kernel(const NormArgs a)
     };
     F2 acc[GRAD ? 2 : 1][GRAD ? P : 1][H] = {};
     const int64_t step = (int64_t)gridDim.x * per;
-    int at = 0;                                              // the slot of this row
-    if (SLOTS > 0) fetch((int64_t)blockIdx.x * per + g, 0);
-    for (int64_t base = (int64_t)blockIdx.x * per; base < a.rows; base += step) {
-        const int64_t row = base + g;
-        const bool on = row < a.rows;
-        // the row's pieces: in their slot while the next row's are copied into the other, else in registers
-        constexpr bool HELD = SLOTS != 2;
-        Vec<T, V> held[HELD ? NIN : 1][HELD ? P : 1] = {};
-        if constexpr (SLOTS == 2) {
-            fetch(row + step, at ^ 1);
-            asm volatile("cp.async.wait_group 1;" ::: "memory");
-        } else if constexpr (SLOTS == 1) {
-            asm volatile("cp.async.wait_group 0;" ::: "memory");
-        }
-        if constexpr (HELD) {
+    const bool full = POST && a.gate_kind == NORM_GATE_FULL;
+    auto put = [&](bool on, int64_t row, void *out, int64_t ldo, int p, const Vec<T, V> &v) {
+        if (on && piece(p) < pieces) *reinterpret_cast<Vec<T, V> *>(static_cast<T *>(out) + row * ldo + piece(p) * V) = v;
+    };
+    auto gate_of = [&](int64_t row, bool on) {
+        return POST && a.gate_kind == NORM_GATE_ROW && on ? static_cast<const float *>(a.gate)[row] : 1.0f;
+    };
+    // The gradient's steps on a row whose pieces in(k, p) gives.  Sums are of pairs; a pair's second half is 0 where V is 1, and
+    // pieces past the row's end are zeros.
+    // 1: mean squares of h and y, and <next_gain dn, h>
+    auto grad_sums = [&](auto in, float &s0, float &s1, float &s2) {
+        F2 hh = f2(0.0f), dh = f2(0.0f), yy = f2(0.0f);
 #pragma unroll
-            for (int k = 0; k < NIN; ++k)
-                if (norm_src<GRAD>(a, k) && on)
+        for (int p = 0; p < P; ++p) {
+            if (a.next) {
+                F2 gain[H];
+                gains(1, p, gain);
+                const Vec<T, V> dv = in(0, p), hv = in(1, p);
 #pragma unroll
-                    for (int p = 0; p < P; ++p)
-                        if (piece(p) < pieces) {
-                            if constexpr (SLOTS > 0) held[k][p] = *reinterpret_cast<const Vec<T, V> *>(slot(0, k, p));
-                            else held[k][p] = *reinterpret_cast<const Vec<T, V> *>(static_cast<const T *>(norm_src<GRAD>(a, k)) + row * norm_ld<GRAD>(a, k) + piece(p) * V);
-                        }
-        }
-        auto in = [&](int k, int p) {
-            if constexpr (HELD) {
-                return held[k][p];
-            } else {
-                Vec<T, V> v = {};
-                if (norm_src<GRAD>(a, k) && on && piece(p) < pieces) v = *reinterpret_cast<const Vec<T, V> *>(slot(at, k, p));
-                return v;
+                for (int j = 0; j < H; ++j) {
+                    const F2 h = pair_of(hv, 2 * j);
+                    hh = fma2(h, h, hh);
+                    dh = fma2(mul2(pair_of(dv, 2 * j), gain[j]), h, dh);
+                }
             }
-        };
-        const bool full = POST && a.gate_kind == NORM_GATE_FULL;
-        const float row_gate = POST && a.gate_kind == NORM_GATE_ROW && on ? static_cast<const float *>(a.gate)[row] : 1.0f;
-        auto put = [&](void *out, int64_t ldo, int p, const Vec<T, V> &v) {
-            if (on && piece(p) < pieces) *reinterpret_cast<Vec<T, V> *>(static_cast<T *>(out) + row * ldo + piece(p) * V) = v;
-        };
-        // Sums are of pairs; a pair's second half is 0 where V is 1.  Pieces past the row's end are zeros.
-        if constexpr (!GRAD) {
-            F2 sq = f2(0.0f);
-#pragma unroll
-            for (int p = 0; p < P; ++p) {
-                const Vec<T, V> yv = in(0, p);
+            if constexpr (POST) {
+                const Vec<T, V> yv = in(3, p);
 #pragma unroll
                 for (int j = 0; j < H; ++j) {
                     const F2 y = pair_of(yv, 2 * j);
-                    sq = fma2(y, y, sq);
+                    yy = fma2(y, y, yy);
                 }
             }
-            float ss[1] = {sq.x + sq.y};
-            row_sum(ss, group, buf, turn);
-            if (SLOTS == 1) fetch(row + step, 0);
-            F2 r = f2(rsqrtf(fmaf(ss[0], a.inv_d, a.eps)));
-            if constexpr (POST) {
-                F2 h[P][H], s2 = f2(0.0f);
-                const F2 scale = f2(a.scale), rg = f2(row_gate);
+        }
+        s0 = hh.x + hh.y, s1 = dh.x + dh.y, s2 = yy.x + yy.y;
+    };
+    // 2: t, dresidual and dgate (or dx), the gains' sums; gt = gain gate t (a gate by row comes in at the end) and <gt, y'>
+    auto grad_middle = [&](auto in, bool on, int64_t row, float rh, float mean, float ry, float row_gate, auto &gt) {
+        const F2 rh2 = f2(rh), ry2 = f2(ry), mh = f2(-mean * rh * rh), scale = f2(a.scale), rg = f2(row_gate);
+        F2 us = f2(0.0f);
 #pragma unroll
-                for (int p = 0; p < P; ++p) {
-                    F2 gain[H] = {};
-                    if (piece(p) < pieces) load_gain<T, V>(a.gain, a.gain_f32, piece(p) * V, gain);
-                    const Vec<T, V> yv = in(0, p), xv = in(1, p), mv = in(2, p);
-                    Vec<T, V> o;
+        for (int p = 0; p < P; ++p) {
+            F2 v[H];
+            const Vec<T, V> ev = in(2, p);
+#pragma unroll
+            for (int j = 0; j < H; ++j) v[j] = pair_of(ev, 2 * j);
+            if (a.next) {
+                F2 gain[H];
+                gains(1, p, gain);
+                const Vec<T, V> dv = in(0, p), hv = in(1, p);
+#pragma unroll
+                for (int j = 0; j < H; ++j) {
+                    const F2 dn = pair_of(dv, 2 * j), h = pair_of(hv, 2 * j);
+                    v[j] = fma2(rh2, fma2(h, mh, mul2(dn, gain[j])), v[j]);
+                    acc[1][p][j] = fma2(dn, mul2(h, rh2), acc[1][p][j]);
+                }
+            }
+            Vec<T, V> o;
+            if constexpr (POST) {
+                // what follows is loaded after that is done, for its registers
+                asm volatile("" ::: "memory");
+#pragma unroll
+                for (int j = 0; j < H; ++j) {
+                    const F2 w = mul2(scale, v[j]);
+                    o.set2(2 * j, w.x, w.y);
+                }
+                put(on, row, a.n, a.ld_n, p, o);
+                F2 gain[H];
+                gains(0, p, gain);
+                const Vec<T, V> yv = in(3, p);
+                // (one test a piece: inside the loop both sides would run)
+                if (full) {
+                    const Vec<T, V> mv = in(4, p);
+                    Vec<T, V> og;
 #pragma unroll
                     for (int j = 0; j < H; ++j) {
-                        const F2 n = mul2(mul2(pair_of(yv, 2 * j), r), gain[j]);
-                        const F2 m = full ? pair_of(mv, 2 * j) : rg;
-                        h[p][j] = fma2(m, n, mul2(scale, pair_of(xv, 2 * j)));
-                        o.set2(2 * j, h[p][j].x, h[p][j].y);
-                        s2 = fma2(h[p][j], h[p][j], s2);
+                        const F2 yh = mul2(pair_of(yv, 2 * j), ry2), q = mul2(gain[j], v[j]), m = pair_of(mv, 2 * j);
+                        const F2 wg = mul2(q, yh), mv2 = mul2(m, v[j]);
+                        og.set2(2 * j, wg.x, wg.y);
+                        acc[0][p][j] = fma2(mv2, yh, acc[0][p][j]);
+                        gt[p][j] = mul2(m, q);
+                        us = fma2(m, wg, us);
                     }
-                    put(a.h, a.ld_h, p, o);
-                }
-                if (a.next) {
-                    float s[1] = {s2.x + s2.y};
-                    row_sum(s, group, buf, turn);
-                    r = f2(rsqrtf(fmaf(s[0], a.inv_d, a.eps)));
+                    put(on, row, a.dgate, a.ld_dgate, p, og);
+                } else {
 #pragma unroll
-                    for (int p = 0; p < P; ++p) {
-                        F2 gain[H] = {};
-                        if (piece(p) < pieces) load_gain<T, V>(a.next_gain, a.gain_f32, piece(p) * V, gain);
-                        Vec<T, V> o;
-#pragma unroll
-                        for (int j = 0; j < H; ++j) {
-                            const F2 n = mul2(mul2(h[p][j], r), gain[j]);
-                            o.set2(2 * j, n.x, n.y);
-                        }
-                        put(a.n, a.ld_n, p, o);
+                    for (int j = 0; j < H; ++j) {
+                        const F2 yh = mul2(pair_of(yv, 2 * j), ry2);
+                        acc[0][p][j] = fma2(mul2(rg, v[j]), yh, acc[0][p][j]);
+                        gt[p][j] = mul2(gain[j], v[j]);
+                        us = fma2(gt[p][j], yh, us);
                     }
                 }
             } else {
 #pragma unroll
-                for (int p = 0; p < P; ++p) {
-                    F2 gain[H] = {};
-                    if (piece(p) < pieces) load_gain<T, V>(a.next_gain, a.gain_f32, piece(p) * V, gain);
-                    const Vec<T, V> xv = in(0, p);
-                    Vec<T, V> o;
-#pragma unroll
-                    for (int j = 0; j < H; ++j) {
-                        const F2 n = mul2(mul2(pair_of(xv, 2 * j), r), gain[j]);
-                        o.set2(2 * j, n.x, n.y);
-                    }
-                    put(a.n, a.ld_n, p, o);
-                }
+                for (int j = 0; j < H; ++j) o.set2(2 * j, v[j].x, v[j].y);
+                put(on, row, a.n, a.ld_n, p, o);
             }
-        } else {
-            // mean squares of h and y, and <next_gain dn, h>
-            F2 hh = f2(0.0f), dh = f2(0.0f), yy = f2(0.0f);
+        }
+        return us.x + us.y;
+    };
+    // 3: dy, and a row's dgate
+    auto grad_last = [&](auto in, bool on, int64_t row, float u, float ry, float row_gate, auto &gt) {
+        if (a.gate_kind == NORM_GATE_ROW && t == 0 && on) static_cast<float *>(a.dgate)[row] = u;
+        const F2 m = f2(-u * a.inv_d * ry), f = f2(row_gate * ry);
+#pragma unroll
+        for (int p = 0; p < P; ++p) {
+            const Vec<T, V> yv = in(3, p);
+            Vec<T, V> o;
+#pragma unroll
+            for (int j = 0; j < H; ++j) {
+                const F2 d = mul2(f, fma2(pair_of(yv, 2 * j), m, gt[p][j]));
+                o.set2(2 * j, d.x, d.y);
+            }
+            put(on, row, a.h, a.ld_h, p, o);
+        }
+    };
+    F2 gt[GRAD && POST ? P : 1][H];
+    if constexpr (SLOTS == 2) {
+        // what no copy will write is read as zeros
+#pragma unroll
+        for (int s = 0; s < SLOTS; ++s)
+#pragma unroll
+            for (int k = 0; k < NIN; ++k)
+#pragma unroll
+                for (int p = 0; p < P; ++p)
+                    if (!norm_src<GRAD>(a, k) || piece(p) >= pieces) *slot(s, k, p) = make_uint4(0, 0, 0, 0);
+    }
+    if constexpr (PIPED) {
+#pragma unroll
+        for (int k = 0; k < 2; ++k)
 #pragma unroll
             for (int p = 0; p < P; ++p) {
-                if (a.next) {
-                    F2 gain[H] = {};
-                    if (piece(p) < pieces) load_gain<T, V>(a.next_gain, a.gain_f32, piece(p) * V, gain);
-                    const Vec<T, V> dv = in(0, p), hv = in(1, p);
+                F2 g[H];
+                load_gain<T, V>(k ? a.next_gain : a.gain, a.gain_f32, gain_at(p), g);
 #pragma unroll
-                    for (int j = 0; j < H; ++j) {
-                        const F2 h = pair_of(hv, 2 * j);
-                        hh = fma2(h, h, hh);
-                        dh = fma2(mul2(pair_of(dv, 2 * j), gain[j]), h, dh);
-                    }
+                for (int q = 0; q < V / 4; ++q) *gain_slot(k, p, q) = make_float4(g[2 * q].x, g[2 * q].y, g[2 * q + 1].x, g[2 * q + 1].y);
+            }
+        // Step 1 of the next row goes with step 2 of this one, so that a row costs one barrier and one reduction of all sums.
+        auto rows_of = [&](int s) {
+            return [&, s](int k, int p) { return *reinterpret_cast<const Vec<T, V> *>(slot(s, k, p)); };
+        };
+        int64_t row = blockIdx.x;
+#pragma unroll
+        for (int s = 0; s < SLOTS; ++s) fetch(row + s * step, s);
+        asm volatile("cp.async.wait_group 1;" ::: "memory");
+        float s[3];
+        grad_sums(rows_of(0), s[0], s[1], s[2]);
+        row_sum<ONE>(s, group, buf, turn);
+        for (int at = 0; row < a.rows; row += step) {
+            const float rh = a.next ? rsqrtf(fmaf(s[0], a.inv_d, a.eps)) : 0.0f, ry = rsqrtf(fmaf(s[2], a.inv_d, a.eps));
+            const float row_gate = gate_of(row, true);
+            const int next = at ^ 1;
+            float w[4];
+            w[0] = grad_middle(rows_of(at), true, row, rh, s[1] * a.inv_d, ry, row_gate, gt);
+            asm volatile("cp.async.wait_group 0;" ::: "memory");
+            grad_sums(rows_of(next), w[1], w[2], w[3]);              // past the last row: whatever the slot holds, unused
+            row_sum<ONE>(w, group, buf, turn);
+            grad_last(rows_of(at), true, row, w[0], ry, row_gate, gt);
+            fetch(row + SLOTS * step, at);
+            s[0] = w[1], s[1] = w[2], s[2] = w[3];
+            at = next;
+        }
+    } else {
+        int at = 0;                                              // the slot of this row
+        if (SLOTS > 0) fetch((int64_t)blockIdx.x * per + g, 0);
+        for (int64_t base = (int64_t)blockIdx.x * per; base < a.rows; base += step) {
+            const int64_t row = base + g;
+            const bool on = ONE || row < a.rows;
+            // the row's pieces: in their slot while the next row's are copied into the other, else in registers
+            constexpr bool HELD = SLOTS != 2;
+            Vec<T, V> held[HELD ? NIN : 1][HELD ? P : 1] = {};
+            if constexpr (SLOTS == 2) {
+                fetch(row + step, at ^ 1);
+                asm volatile("cp.async.wait_group 1;" ::: "memory");
+            } else if constexpr (SLOTS == 1) {
+                asm volatile("cp.async.wait_group 0;" ::: "memory");
+            }
+            if constexpr (HELD) {
+#pragma unroll
+                for (int k = 0; k < NIN; ++k)
+                    if (norm_src<GRAD>(a, k) && on)
+#pragma unroll
+                        for (int p = 0; p < P; ++p)
+                            if (piece(p) < pieces) {
+                                if constexpr (SLOTS > 0) held[k][p] = *reinterpret_cast<const Vec<T, V> *>(slot(0, k, p));
+                                else held[k][p] = *reinterpret_cast<const Vec<T, V> *>(static_cast<const T *>(norm_src<GRAD>(a, k)) + row * norm_ld<GRAD>(a, k) + piece(p) * V);
+                            }
+            }
+            auto in = [&](int k, int p) {
+                if constexpr (HELD) {
+                    return held[k][p];
+                } else {
+                    Vec<T, V> v = {};
+                    if (on) v = *reinterpret_cast<const Vec<T, V> *>(slot(at, k, p));
+                    return v;
                 }
-                if constexpr (POST) {
-                    const Vec<T, V> yv = in(3, p);
+            };
+            const float row_gate = gate_of(row, on);
+            if constexpr (!GRAD) {
+                F2 sq = f2(0.0f);
+#pragma unroll
+                for (int p = 0; p < P; ++p) {
+                    const Vec<T, V> yv = in(0, p);
 #pragma unroll
                     for (int j = 0; j < H; ++j) {
                         const F2 y = pair_of(yv, 2 * j);
-                        yy = fma2(y, y, yy);
+                        sq = fma2(y, y, sq);
                     }
                 }
-            }
-            float s[3] = {hh.x + hh.y, dh.x + dh.y, yy.x + yy.y};
-            row_sum(s, group, buf, turn);
-            if (SLOTS == 1) fetch(row + step, 0);
-            const float rh = a.next ? rsqrtf(fmaf(s[0], a.inv_d, a.eps)) : 0.0f;
-            const float ry = POST ? rsqrtf(fmaf(s[2], a.inv_d, a.eps)) : 0.0f;
-            const F2 rh2 = f2(rh), ry2 = f2(ry), mh = f2(-s[1] * a.inv_d * rh * rh), scale = f2(a.scale), rg = f2(row_gate);
-            F2 us = f2(0.0f), gt[POST ? P : 1][H];               // gain gate t (a gate by row comes in at the end)
-#pragma unroll
-            for (int p = 0; p < P; ++p) {
-                F2 v[H];
-                const Vec<T, V> ev = in(2, p);
-#pragma unroll
-                for (int j = 0; j < H; ++j) v[j] = pair_of(ev, 2 * j);
-                if (a.next) {
-                    F2 gain[H] = {};
-                    if (piece(p) < pieces) load_gain<T, V>(a.next_gain, a.gain_f32, piece(p) * V, gain);
-                    const Vec<T, V> dv = in(0, p), hv = in(1, p);
-#pragma unroll
-                    for (int j = 0; j < H; ++j) {
-                        const F2 dn = pair_of(dv, 2 * j), h = pair_of(hv, 2 * j);
-                        v[j] = fma2(rh2, fma2(h, mh, mul2(dn, gain[j])), v[j]);
-                        acc[1][p][j] = fma2(dn, mul2(h, rh2), acc[1][p][j]);
-                    }
-                }
-                Vec<T, V> o;
+                float ss[1] = {sq.x + sq.y};
+                row_sum<ONE>(ss, group, buf, turn);
+                if (SLOTS == 1) fetch(row + step, 0);
+                float r = rsqrtf(fmaf(ss[0], a.inv_d, a.eps));
                 if constexpr (POST) {
-                    // what follows is loaded after that is done, for its registers
-                    asm volatile("" ::: "memory");
-                    F2 gain[H] = {};
-                    if (piece(p) < pieces) load_gain<T, V>(a.gain, a.gain_f32, piece(p) * V, gain);
-                    const Vec<T, V> yv = in(3, p), mv = in(4, p);
-                    Vec<T, V> og;
+                    F2 h[P][H], s2 = f2(0.0f);
+                    const F2 scale = f2(a.scale);
+                    r *= row_gate;
 #pragma unroll
-                    for (int j = 0; j < H; ++j) {
-                        const F2 yh = mul2(pair_of(yv, 2 * j), ry2), w = mul2(scale, v[j]), q = mul2(gain[j], v[j]);
-                        o.set2(2 * j, w.x, w.y);
+                    for (int p = 0; p < P; ++p) {
+                        F2 gain[H];
+                        gains(0, p, gain);
+                        const Vec<T, V> yv = in(0, p), xv = in(1, p);
+                        // (one test a piece: inside the loop both sides would run)
+#pragma unroll
+                        for (int j = 0; j < H; ++j) gain[j] = mul2(gain[j], f2(r));
                         if (full) {
-                            const F2 m = pair_of(mv, 2 * j), wg = mul2(q, yh);
-                            og.set2(2 * j, wg.x, wg.y);
-                            acc[0][p][j] = fma2(mul2(m, v[j]), yh, acc[0][p][j]);
-                            gt[p][j] = mul2(m, q);
-                        } else {
-                            acc[0][p][j] = fma2(mul2(rg, v[j]), yh, acc[0][p][j]);
-                            gt[p][j] = q;
+                            const Vec<T, V> mv = in(2, p);
+#pragma unroll
+                            for (int j = 0; j < H; ++j) gain[j] = mul2(gain[j], pair_of(mv, 2 * j));
                         }
-                        us = fma2(gt[p][j], yh, us);
+                        Vec<T, V> o;
+#pragma unroll
+                        for (int j = 0; j < H; ++j) {
+                            h[p][j] = fma2(pair_of(yv, 2 * j), gain[j], mul2(scale, pair_of(xv, 2 * j)));
+                            o.set2(2 * j, h[p][j].x, h[p][j].y);
+                            s2 = fma2(h[p][j], h[p][j], s2);
+                        }
+                        put(on, row, a.h, a.ld_h, p, o);
                     }
-                    if (full) put(a.dgate, a.ld_dgate, p, og);
+                    if (a.next) {
+                        float s[1] = {s2.x + s2.y};
+                        row_sum<ONE>(s, group, buf, turn);
+                        r = rsqrtf(fmaf(s[0], a.inv_d, a.eps));
+#pragma unroll
+                        for (int p = 0; p < P; ++p) {
+                            F2 gain[H];
+                            gains(1, p, gain);
+                            Vec<T, V> o;
+#pragma unroll
+                            for (int j = 0; j < H; ++j) {
+                                const F2 n = mul2(mul2(h[p][j], f2(r)), gain[j]);
+                                o.set2(2 * j, n.x, n.y);
+                            }
+                            put(on, row, a.n, a.ld_n, p, o);
+                        }
+                    }
                 } else {
 #pragma unroll
-                    for (int j = 0; j < H; ++j) o.set2(2 * j, v[j].x, v[j].y);
-                }
-                put(a.n, a.ld_n, p, o);
-            }
-            if constexpr (POST) {
-                float u[1] = {us.x + us.y};
-                row_sum(u, group, buf, turn);
-                if (a.gate_kind == NORM_GATE_ROW && t == 0 && on) static_cast<float *>(a.dgate)[row] = u[0];
-                const F2 m = f2(-u[0] * a.inv_d * ry), f = f2(row_gate * ry);
+                    for (int p = 0; p < P; ++p) {
+                        F2 gain[H];
+                        gains(1, p, gain);
+                        const Vec<T, V> xv = in(0, p);
+                        Vec<T, V> o;
 #pragma unroll
-                for (int p = 0; p < P; ++p) {
-                    const Vec<T, V> yv = in(3, p);
-                    Vec<T, V> o;
-#pragma unroll
-                    for (int j = 0; j < H; ++j) {
-                        const F2 d = mul2(f, fma2(pair_of(yv, 2 * j), m, gt[p][j]));
-                        o.set2(2 * j, d.x, d.y);
+                        for (int j = 0; j < H; ++j) {
+                            const F2 n = mul2(mul2(pair_of(xv, 2 * j), f2(r)), gain[j]);
+                            o.set2(2 * j, n.x, n.y);
+                        }
+                        put(on, row, a.n, a.ld_n, p, o);
                     }
-                    put(a.h, a.ld_h, p, o);
+                }
+            } else {
+                float s[3];
+                grad_sums(in, s[0], s[1], s[2]);
+                row_sum<ONE>(s, group, buf, turn);
+                if (SLOTS == 1) fetch(row + step, 0);
+                const float rh = a.next ? rsqrtf(fmaf(s[0], a.inv_d, a.eps)) : 0.0f;
+                const float ry = POST ? rsqrtf(fmaf(s[2], a.inv_d, a.eps)) : 0.0f;
+                float u[1] = {grad_middle(in, on, row, rh, s[1] * a.inv_d, ry, row_gate, gt)};
+                if constexpr (POST) {
+                    row_sum<ONE>(u, group, buf, turn);
+                    grad_last(in, on, row, u[0], ry, row_gate, gt);
                 }
             }
+            if (SLOTS == 2) at ^= 1;
         }
-        if (SLOTS == 2) at ^= 1;
     }
     if constexpr (GRAD) {
-        // rows that are not there added nothing
-        const int64_t groups = (int64_t)gridDim.x * per, mine = (int64_t)blockIdx.x * per + g;
+        // rows that are not there added nothing; a CTA's groups are added up before its sums leave it
+        float *all = reinterpret_cast<float *>(ring);
+        if constexpr (!ONE) __syncthreads();
 #pragma unroll
         for (int k = POST ? 0 : 1; k < 2; ++k) {
             if (k == 1 && !a.next) break;
 #pragma unroll
             for (int p = 0; p < P; ++p) {
                 if (piece(p) >= pieces) continue;
-                float *o = a.part + (k * groups + mine) * a.D + piece(p) * V;
+                float *o = (ONE ? a.part + (k * (int64_t)gridDim.x + blockIdx.x) * a.D : all + (k * per + g) * a.D) + piece(p) * V;
 #pragma unroll
                 for (int j = 0; j < H; ++j) {
                     o[2 * j] = acc[k][p][j].x;
@@ -364,10 +508,20 @@ __global__ void __launch_bounds__(MAXT, CTAS) norm_kernel(const NormArgs a)
                 }
             }
         }
+        if constexpr (!ONE) {
+            __syncthreads();
+            for (int i = threadIdx.x; i < 2 * a.D; i += blockDim.x) {
+                const int k = i >= a.D, c = i - k * a.D;
+                if (k ? !a.next : !POST) continue;
+                float sum = 0.0f;
+                for (int q = 0; q < per; ++q) sum += all[(k * per + q) * a.D + c];
+                a.part[(k * (int64_t)gridDim.x + blockIdx.x) * a.D + c] = sum;
+            }
+        }
     }
 }
 
-// Column sums of the row groups' parts, in a fixed order: 32 columns a CTA, 16 rows of threads.
+// Column sums of the CTAs' parts, in a fixed order: 32 columns a CTA, 16 rows of threads.
 __global__ void __launch_bounds__(512) norm_gain_kernel(const float *part, int groups, int D, float *dgain, float *dnext)
 {
     griddep_enter();
@@ -387,41 +541,51 @@ __global__ void __launch_bounds__(512) norm_gain_kernel(const float *part, int g
     }
 }
 
-// Elements a thread: 16 forwards; 8 for the gradients' up to 8192 columns, which keep five inputs, sums of two gains and twice
-// the gains in registers (7168 columns, 8 a thread: 896 threads of 72 registers).  Where pieces are single elements, 16.
-static int norm_group(int D, int elems) { return std::max(32, (D + 32 * elems - 1) / (32 * elems) * 32); }
-static int norm_rows(int group) { return group >= 128 ? 1 : 256 / group; }
-// Row groups of a gradient's grid at most, each with sums of its own; a CTA has at most 8.
-static int64_t norm_groups(int64_t rows) { return std::min<int64_t>((rows + 7) / 8 * 8, 8 * 304); }
+// Elements a thread: 16; 8 for norm_residual's gradient up to 8192 columns, which keeps the sums of two gains and more in
+// registers (7168 columns: 896 threads of 72 registers).
+static int norm_group(int D, int elems)
+{
+    int n = (D + elems - 1) / elems;
+    if (n > 16) return (n + 31) / 32 * 32;
+    int group = 4;                                       // a part of a warp
+    while (group < n) group *= 2;
+    return group;
+}
+constexpr int NORM_NARROW = 96;                          // threads a row at most where a CTA has several rows
+static int norm_rows(int group) { return group > NORM_NARROW ? 1 : 256 / group; }
+// CTAs of a gradient's grid at most, each with sums of its own.
+static int64_t norm_parts(int64_t rows) { return std::min<int64_t>(rows, 608); }
 
-template <class T, int V, int ELEMS, bool GRAD, bool POST, int MAXT, int CTAS>
+template <class T, int V, int ELEMS, bool GRAD, bool POST, int MAXT, int CTAS, bool ONE>
 static int launch_norm(NormArgs a, float *dgain, float *dnext, cudaStream_t st)
 {
     constexpr int P = ELEMS / V;
     constexpr int NIN = GRAD ? (POST ? 5 : 3) : (POST ? 3 : 1);
     constexpr int SLOTS = norm_slots<V, NIN * P * MAXT * 16>();
-    auto kern = norm_kernel<T, V, P, GRAD, POST, MAXT, CTAS>;
     a.group = norm_group(a.D, ELEMS);
-    const int per = norm_rows(a.group), threads = a.group * per, sms = k3_num_sms();
+    const int per = ONE ? 1 : norm_rows(a.group), threads = a.group * per, sms = k3_num_sms();
+    auto kern = norm_kernel<T, V, P, GRAD, POST, MAXT, CTAS, ONE>;
     if (!sms) return K3MOE_ERR_CUDA;
-    const int smem = SLOTS * NIN * P * threads * 16;
+    constexpr bool PIPED = V > 1 && norm_piped(GRAD, POST, ONE, NIN * P * MAXT * 16, 2 * P * V * MAXT * 4);
+    constexpr int PER_THREAD = SLOTS * NIN * P * 16 + (PIPED ? 2 * P * V * 4 : 0);
+    const int smem = std::max(PER_THREAD * threads, GRAD && !ONE ? 2 * per * a.D * 4 : 0);
     static unsigned long long attr_set = 0;
-    if (SLOTS && !k3_smem_attr(kern, SLOTS * NIN * P * MAXT * 16, attr_set)) return K3MOE_ERR_CUDA;
-    static int fits[33] = {};                            // CTAs an SM by warps a row
-    int fit = fits[a.group / 32];
+    if (SLOTS && !k3_smem_attr(kern, PER_THREAD * MAXT, attr_set)) return K3MOE_ERR_CUDA;
+    static int fits[33] = {};                            // CTAs an SM by warps of a CTA
+    int fit = fits[threads / 32];
     if (!fit) {
         if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&fit, kern, threads, smem) != cudaSuccess || fit < 1) return K3MOE_ERR_CUDA;
-        fits[a.group / 32] = fit;
+        fits[threads / 32] = fit;
     }
     int64_t grid = std::min<int64_t>(((int64_t)a.rows + per - 1) / per, (int64_t)fit * sms);
-    if (GRAD) grid = std::min<int64_t>(grid, norm_groups(a.rows) / per);
+    if (GRAD) grid = std::min<int64_t>(grid, norm_parts(a.rows));
     if (grid > 0) {
         k3_launch(kern, dim3((unsigned)grid), threads, smem, st, a);
         k3_note_launch();
     }
     if (GRAD && ((POST && dgain) || (a.next && dnext))) {
         k3_launch(norm_gain_kernel, dim3((unsigned)((a.D + 31) / 32), 2), 512, 0, st, (const float *)a.part,
-                  (int)(grid * per), a.D, POST ? dgain : nullptr, a.next ? dnext : nullptr);
+                  (int)grid, a.D, POST ? dgain : nullptr, a.next ? dnext : nullptr);
         k3_note_launch();
     }
     return cudaGetLastError() == cudaSuccess ? K3MOE_OK : K3MOE_ERR_CUDA;
@@ -430,14 +594,27 @@ static int launch_norm(NormArgs a, float *dgain, float *dnext, cudaStream_t st)
 template <class T, int V, bool GRAD, bool POST>
 static int launch_sized(const NormArgs &a, float *dgain, float *dnext, cudaStream_t st)
 {
-    if constexpr (V > 1 && GRAD) {
-        if (a.D <= 3584) return launch_norm<T, V, 8, true, POST, 448, 2>(a, dgain, dnext, st);
-        if (a.D <= 7168) return launch_norm<T, V, 8, true, POST, 896, 1>(a, dgain, dnext, st);
-        if (a.D <= 8192) return launch_norm<T, V, 8, true, POST, 1024, 1>(a, dgain, dnext, st);
-    } else if constexpr (V > 1) {
-        if (a.D <= 8192) return launch_norm<T, V, 16, false, POST, 512, 2>(a, dgain, dnext, st);
+    if constexpr (V == 1) {
+        if (a.D <= 256) return launch_norm<T, V, 8, GRAD, POST, 256, 1, false>(a, dgain, dnext, st);
+        if (a.D <= NORM_NARROW * 16) return launch_norm<T, V, 16, GRAD, POST, 256, 1, false>(a, dgain, dnext, st);
+        if (a.D <= 8192) return launch_norm<T, V, 16, GRAD, POST, 512, 1, true>(a, dgain, dnext, st);
+    } else if constexpr (GRAD) {
+        if constexpr (POST) {
+            if (a.D <= NORM_NARROW * 8) return launch_norm<T, V, 8, true, true, 256, 3, false>(a, dgain, dnext, st);
+            if (a.D <= 3584) return launch_norm<T, V, 8, true, true, 448, 2, true>(a, dgain, dnext, st);
+            if (a.D <= 7168) return launch_norm<T, V, 8, true, true, 896, 1, true>(a, dgain, dnext, st);
+            if (a.D <= 8192) return launch_norm<T, V, 8, true, true, 1024, 1, true>(a, dgain, dnext, st);
+        } else {
+            if (a.D <= NORM_NARROW * 8) return launch_norm<T, V, 8, true, false, 256, 3, false>(a, dgain, dnext, st);
+            if (a.D <= NORM_NARROW * 16) return launch_norm<T, V, 16, true, false, 256, 3, false>(a, dgain, dnext, st);
+            if (a.D <= 8192) return launch_norm<T, V, 16, true, false, 512, 2, true>(a, dgain, dnext, st);
+        }
+    } else {
+        if (a.D <= 256) return launch_norm<T, V, 8, false, POST, 256, 4, false>(a, dgain, dnext, st);
+        if (a.D <= NORM_NARROW * 16) return launch_norm<T, V, 16, false, POST, 256, 4, false>(a, dgain, dnext, st);
+        if (a.D <= 8192) return launch_norm<T, V, 16, false, POST, 512, 2, true>(a, dgain, dnext, st);
     }
-    return launch_norm<T, V, 16, GRAD, POST, 1024, 1>(a, dgain, dnext, st);
+    return launch_norm<T, V, 16, GRAD, POST, 1024, 1, true>(a, dgain, dnext, st);
 }
 
 template <class T, int V, bool GRAD>
@@ -558,7 +735,7 @@ extern "C" int k3moe_norm_residual(const void *y, int64_t ldy, const void *resid
 
 extern "C" size_t k3moe_norm_grad_workspace_bytes(int rows, int D)
 {
-    return rows < 0 || D < 1 || D > K3MOE_NORM_MAX_WIDTH ? 0 : (size_t)std::max<int64_t>(1, norm_groups(rows)) * D * 2 * sizeof(float);
+    return rows < 0 || D < 1 || D > K3MOE_NORM_MAX_WIDTH ? 0 : (size_t)std::max<int64_t>(1, norm_parts(rows)) * D * 2 * sizeof(float);
 }
 
 extern "C" int k3moe_rms_norm_grad(const void *dy, int64_t lddy, const void *x, int64_t ldx, const void *gain, int gain_dtype,
