@@ -34,26 +34,57 @@ __device__ __forceinline__ void norm_cp16(void *dst, const void *src)
                  : "memory");
 }
 
-// Gains of the pairs j, j + 1 of V elements from element i (V = 1: the element and nothing).
-template <class T, int V>
-__device__ __forceinline__ void load_gain(const void *p, int f32, int i, F2 (&g)[(V + 1) / 2])
+// V elements from column c of a row of D.  LOOSE: element by element, zeros past the row's end.
+template <class T, int V, bool LOOSE>
+__device__ __forceinline__ Vec<T, V> load_piece(const T *row, int c, int D)
+{
+    if constexpr (!LOOSE) return *reinterpret_cast<const Vec<T, V> *>(row + c);
+    Vec<T, V> v = {};
+#pragma unroll
+    for (int j = 0; j < V; j += 2) {
+        const float x = c + j < D ? to_f32(row[c + j]) : 0.0f, y = c + j + 1 < D ? to_f32(row[c + j + 1]) : 0.0f;
+        v.set2(j, x, y);                                     // (exact: the type's own values)
+    }
+    return v;
+}
+template <class T, int V, bool LOOSE>
+__device__ __forceinline__ void store_piece(T *row, int c, int D, const Vec<T, V> &v)
+{
+    if constexpr (!LOOSE) {
+        *reinterpret_cast<Vec<T, V> *>(row + c) = v;
+    } else {
+#pragma unroll
+        for (int j = 0; j < V; j += 2) {
+            const float2 e = v.get2(j);
+            if (c + j < D) row[c + j] = from_f32<T>(e.x);
+            if (c + j + 1 < D) row[c + j + 1] = from_f32<T>(e.y);
+        }
+    }
+}
+
+// V gains from column c; any gain past the last.
+template <class T, int V, bool LOOSE>
+__device__ __forceinline__ void load_gain(const void *p, int f32, int c, int D, F2 (&g)[V / 2])
 {
     if (!p) {
 #pragma unroll
-        for (int j = 0; j < (V + 1) / 2; ++j) g[j] = f2(1.0f);
-    } else if (f32) {
-        const float *q = static_cast<const float *>(p) + i;
-        if constexpr (V % 4 == 0) {
+        for (int j = 0; j < V / 2; ++j) g[j] = f2(1.0f);
+    } else if (LOOSE) {
+        auto at = [&](int i) {
+            i = min(i, D - 1);
+            return f32 ? static_cast<const float *>(p)[i] : to_f32(static_cast<const T *>(p)[i]);
+        };
 #pragma unroll
-            for (int j = 0; j < V; j += 4) {
-                const float4 x = __ldg(reinterpret_cast<const float4 *>(q + j));
-                g[j / 2] = {x.x, x.y}, g[j / 2 + 1] = {x.z, x.w};
-            }
-        } else {
-            g[0] = {__ldg(q), 0.0f};
+        for (int j = 0; j < V / 2; ++j) g[j] = {at(c + 2 * j), at(c + 2 * j + 1)};
+    } else if (f32) {
+        const float *q = static_cast<const float *>(p) + c;
+#pragma unroll
+        for (int j = 0; j < V; j += 4) {
+            const float4 x = __ldg(reinterpret_cast<const float4 *>(q + j));
+            g[j / 2] = {x.x, x.y}, g[j / 2 + 1] = {x.z, x.w};
         }
     } else {
-        const Vec<T, V> x = *reinterpret_cast<const Vec<T, V> *>(static_cast<const T *>(p) + i);
+        const Vec<T, V> x = *reinterpret_cast<const Vec<T, V> *>(static_cast<const T *>(p) + c);
 #pragma unroll
         for (int j = 0; j < V; j += 2) {
             const float2 e = x.get2(j);
@@ -152,24 +183,24 @@ constexpr bool norm_piped(bool grad, bool post, bool one, int slots, int gains)
     return grad && post && one && 2 * slots + gains + 1024 <= kMaxSmem;
 }
 // Rows' pieces that a thread keeps in flight in shared memory: two rows where they fit, else one or none (wide fp32 rows).
-template <int V, int BYTES>
-constexpr int norm_slots() { return V == 1 ? 0 : std::min(2, (kMaxSmem - 1024) / BYTES); }
+template <bool LOOSE, int BYTES>
+constexpr int norm_slots() { return LOOSE ? 0 : std::min(2, (kMaxSmem - 1024) / BYTES); }
 
 // A group of threads holds a row, P pieces of V elements a thread, and walks over the rows (ONE: the group is the CTA, so that
 // rows' addresses are the same for all its threads).  With 16-byte pieces every thread copies its pieces of the next row into
 // shared memory (its own slots: nothing is synchronised): with two slots while this row is worked on, with one as soon as
 // this row is in registers.
-template <class T, int V, int P, bool GRAD, bool POST, int MAXT, int CTAS, bool ONE>
+template <class T, int V, int P, bool GRAD, bool POST, int MAXT, int CTAS, bool ONE, bool LOOSE>
 __global__ void __launch_bounds__(MAXT, CTAS) norm_kernel(const NormArgs a)
 {
     griddep_enter();
-    constexpr int NIN = GRAD ? (POST ? 5 : 3) : (POST ? 3 : 1), H = (V + 1) / 2;
-    constexpr int SLOTS = norm_slots<V, NIN * P * MAXT * 16>();
-    constexpr bool PIPED = V > 1 && norm_piped(GRAD, POST, ONE, NIN * P * MAXT * 16, 2 * P * V * MAXT * 4);
+    constexpr int NIN = GRAD ? (POST ? 5 : 3) : (POST ? 3 : 1), H = V / 2;
+    constexpr int SLOTS = norm_slots<LOOSE, NIN * P * MAXT * 16>();
+    constexpr bool PIPED = !LOOSE && norm_piped(GRAD, POST, ONE, NIN * P * MAXT * 16, 2 * P * V * MAXT * 4);
     extern __shared__ uint4 ring[];
     __shared__ float4 buf[2 * 32];
     const int group = ONE ? (int)blockDim.x : a.group, g = ONE ? 0 : (int)threadIdx.x / group, t = (int)threadIdx.x - g * group;
-    const int per = ONE ? 1 : (int)blockDim.x / group, pieces = a.D / V;
+    const int per = ONE ? 1 : (int)blockDim.x / group, pieces = (a.D + V - 1) / V;
     int turn = 0;
     auto piece = [&](int p) { return p * group + t; };
     auto gain_at = [&](int p) { return min(piece(p), pieces - 1) * V; };         // any gain where the elements are zeros
@@ -185,7 +216,7 @@ __global__ void __launch_bounds__(MAXT, CTAS) norm_kernel(const NormArgs a)
                 g[2 * q] = {x.x, x.y}, g[2 * q + 1] = {x.z, x.w};
             }
         } else {
-            load_gain<T, V>(k ? a.next_gain : a.gain, a.gain_f32, gain_at(p), g);
+            load_gain<T, V, LOOSE>(k ? a.next_gain : a.gain, a.gain_f32, gain_at(p), a.D, g);
         }
     };
     auto slot = [&](int s, int k, int p) { return ring + ((s * NIN + k) * P + p) * blockDim.x + threadIdx.x; };
@@ -204,13 +235,12 @@ __global__ void __launch_bounds__(MAXT, CTAS) norm_kernel(const NormArgs a)
     const int64_t step = (int64_t)gridDim.x * per;
     const bool full = POST && a.gate_kind == NORM_GATE_FULL;
     auto put = [&](bool on, int64_t row, void *out, int64_t ldo, int p, const Vec<T, V> &v) {
-        if (on && piece(p) < pieces) *reinterpret_cast<Vec<T, V> *>(static_cast<T *>(out) + row * ldo + piece(p) * V) = v;
+        if (on && piece(p) < pieces) store_piece<T, V, LOOSE>(static_cast<T *>(out) + row * ldo, piece(p) * V, a.D, v);
     };
     auto gate_of = [&](int64_t row, bool on) {
         return POST && a.gate_kind == NORM_GATE_ROW && on ? static_cast<const float *>(a.gate)[row] : 1.0f;
     };
-    // The gradient's steps on a row whose pieces in(k, p) gives.  Sums are of pairs; a pair's second half is 0 where V is 1, and
-    // pieces past the row's end are zeros.
+    // The gradient's steps on a row whose pieces in(k, p) gives.  Pieces past the row's end are zeros.
     // 1: mean squares of h and y, and <next_gain dn, h>
     auto grad_sums = [&](auto in, float &s0, float &s1, float &s2) {
         F2 hh = f2(0.0f), dh = f2(0.0f), yy = f2(0.0f);
@@ -336,7 +366,7 @@ __global__ void __launch_bounds__(MAXT, CTAS) norm_kernel(const NormArgs a)
 #pragma unroll
             for (int p = 0; p < P; ++p) {
                 F2 g[H];
-                load_gain<T, V>(k ? a.next_gain : a.gain, a.gain_f32, gain_at(p), g);
+                load_gain<T, V, LOOSE>(k ? a.next_gain : a.gain, a.gain_f32, gain_at(p), a.D, g);
 #pragma unroll
                 for (int q = 0; q < V / 4; ++q) *gain_slot(k, p, q) = make_float4(g[2 * q].x, g[2 * q].y, g[2 * q + 1].x, g[2 * q + 1].y);
             }
@@ -388,7 +418,7 @@ __global__ void __launch_bounds__(MAXT, CTAS) norm_kernel(const NormArgs a)
                         for (int p = 0; p < P; ++p)
                             if (piece(p) < pieces) {
                                 if constexpr (SLOTS > 0) held[k][p] = *reinterpret_cast<const Vec<T, V> *>(slot(0, k, p));
-                                else held[k][p] = *reinterpret_cast<const Vec<T, V> *>(static_cast<const T *>(norm_src<GRAD>(a, k)) + row * norm_ld<GRAD>(a, k) + piece(p) * V);
+                                else held[k][p] = load_piece<T, V, LOOSE>(static_cast<const T *>(norm_src<GRAD>(a, k)) + row * norm_ld<GRAD>(a, k), piece(p) * V, a.D);
                             }
             }
             auto in = [&](int k, int p) {
@@ -503,8 +533,8 @@ __global__ void __launch_bounds__(MAXT, CTAS) norm_kernel(const NormArgs a)
                 float *o = (ONE ? a.part + (k * (int64_t)gridDim.x + blockIdx.x) * a.D : all + (k * per + g) * a.D) + piece(p) * V;
 #pragma unroll
                 for (int j = 0; j < H; ++j) {
-                    o[2 * j] = acc[k][p][j].x;
-                    if (V > 1) o[2 * j + 1] = acc[k][p][j].y;
+                    if (!LOOSE || piece(p) * V + 2 * j < a.D) o[2 * j] = acc[k][p][j].x;
+                    if (!LOOSE || piece(p) * V + 2 * j + 1 < a.D) o[2 * j + 1] = acc[k][p][j].y;
                 }
             }
         }
@@ -556,17 +586,17 @@ static int norm_rows(int group) { return group > NORM_NARROW ? 1 : 256 / group; 
 // CTAs of a gradient's grid at most, each with sums of its own.
 static int64_t norm_parts(int64_t rows) { return std::min<int64_t>(rows, 608); }
 
-template <class T, int V, int ELEMS, bool GRAD, bool POST, int MAXT, int CTAS, bool ONE>
+template <class T, int V, int ELEMS, bool GRAD, bool POST, int MAXT, int CTAS, bool ONE, bool LOOSE>
 static int launch_norm(NormArgs a, float *dgain, float *dnext, cudaStream_t st)
 {
     constexpr int P = ELEMS / V;
     constexpr int NIN = GRAD ? (POST ? 5 : 3) : (POST ? 3 : 1);
-    constexpr int SLOTS = norm_slots<V, NIN * P * MAXT * 16>();
+    constexpr int SLOTS = norm_slots<LOOSE, NIN * P * MAXT * 16>();
     a.group = norm_group(a.D, ELEMS);
     const int per = ONE ? 1 : norm_rows(a.group), threads = a.group * per, sms = k3_num_sms();
-    auto kern = norm_kernel<T, V, P, GRAD, POST, MAXT, CTAS, ONE>;
+    auto kern = norm_kernel<T, V, P, GRAD, POST, MAXT, CTAS, ONE, LOOSE>;
     if (!sms) return K3MOE_ERR_CUDA;
-    constexpr bool PIPED = V > 1 && norm_piped(GRAD, POST, ONE, NIN * P * MAXT * 16, 2 * P * V * MAXT * 4);
+    constexpr bool PIPED = !LOOSE && norm_piped(GRAD, POST, ONE, NIN * P * MAXT * 16, 2 * P * V * MAXT * 4);
     constexpr int PER_THREAD = SLOTS * NIN * P * 16 + (PIPED ? 2 * P * V * 4 : 0);
     const int smem = std::max(PER_THREAD * threads, GRAD && !ONE ? 2 * per * a.D * 4 : 0);
     static unsigned long long attr_set = 0;
@@ -591,48 +621,48 @@ static int launch_norm(NormArgs a, float *dgain, float *dnext, cudaStream_t st)
     return cudaGetLastError() == cudaSuccess ? K3MOE_OK : K3MOE_ERR_CUDA;
 }
 
-template <class T, int V, bool GRAD, bool POST>
+template <class T, int V, bool GRAD, bool POST, bool LOOSE>
 static int launch_sized(const NormArgs &a, float *dgain, float *dnext, cudaStream_t st)
 {
-    if constexpr (V == 1) {
-        if (a.D <= 256) return launch_norm<T, V, 8, GRAD, POST, 256, 1, false>(a, dgain, dnext, st);
-        if (a.D <= NORM_NARROW * 16) return launch_norm<T, V, 16, GRAD, POST, 256, 1, false>(a, dgain, dnext, st);
-        if (a.D <= 8192) return launch_norm<T, V, 16, GRAD, POST, 512, 1, true>(a, dgain, dnext, st);
-    } else if constexpr (GRAD) {
-        if constexpr (POST) {
-            if (a.D <= NORM_NARROW * 8) return launch_norm<T, V, 8, true, true, 256, 3, false>(a, dgain, dnext, st);
-            if (a.D <= 3584) return launch_norm<T, V, 8, true, true, 448, 2, true>(a, dgain, dnext, st);
-            if (a.D <= 7168) return launch_norm<T, V, 8, true, true, 896, 1, true>(a, dgain, dnext, st);
-            if (a.D <= 8192) return launch_norm<T, V, 8, true, true, 1024, 1, true>(a, dgain, dnext, st);
-        } else {
-            if (a.D <= NORM_NARROW * 8) return launch_norm<T, V, 8, true, false, 256, 3, false>(a, dgain, dnext, st);
-            if (a.D <= NORM_NARROW * 16) return launch_norm<T, V, 16, true, false, 256, 3, false>(a, dgain, dnext, st);
-            if (a.D <= 8192) return launch_norm<T, V, 16, true, false, 512, 2, true>(a, dgain, dnext, st);
+    auto go = [&](auto elems, auto threads, auto ctas, auto one) {
+        return launch_norm<T, V, elems.value, GRAD, POST, threads.value, ctas.value, one.value, LOOSE>(a, dgain, dnext, st);
+    };
+    using std::integral_constant;
+    const integral_constant<int, 8> e8;
+    const integral_constant<int, 16> e16;
+    const std::true_type one;
+    const std::false_type several;
+    // (threads, CTAs an SM) that the registers are counted for
+    if constexpr (GRAD && POST) {
+        if (a.D <= NORM_NARROW * 8) return go(e8, integral_constant<int, 256>(), integral_constant<int, 3>(), several);
+        if constexpr (!LOOSE) {
+            if (a.D <= 3584) return go(e8, integral_constant<int, 448>(), integral_constant<int, 2>(), one);
+            if (a.D <= 7168) return go(e8, integral_constant<int, 896>(), integral_constant<int, 1>(), one);
         }
+        if (a.D <= 8192) return go(e8, integral_constant<int, 1024>(), integral_constant<int, 1>(), one);
     } else {
-        if (a.D <= 256) return launch_norm<T, V, 8, false, POST, 256, 4, false>(a, dgain, dnext, st);
-        if (a.D <= NORM_NARROW * 16) return launch_norm<T, V, 16, false, POST, 256, 4, false>(a, dgain, dnext, st);
-        if (a.D <= 8192) return launch_norm<T, V, 16, false, POST, 512, 2, true>(a, dgain, dnext, st);
+        // (65,536 x 512 forwards: 22 us with 16 elements a thread, 30 with 8; 131,072 x 64: 27 and 7)
+        if (a.D <= (GRAD ? NORM_NARROW * 8 : 256)) return go(e8, integral_constant<int, 256>(), integral_constant<int, GRAD ? 3 : 4>(), several);
+        if (a.D <= NORM_NARROW * 16) return go(e16, integral_constant<int, 256>(), integral_constant<int, GRAD ? 3 : 4>(), several);
+        if (a.D <= 8192) return go(e16, integral_constant<int, 512>(), integral_constant<int, 2>(), one);
     }
-    return launch_norm<T, V, 16, GRAD, POST, 1024, 1, true>(a, dgain, dnext, st);
+    return go(e16, integral_constant<int, 1024>(), integral_constant<int, 1>(), one);
 }
 
 template <class T, int V, bool GRAD>
-static int launch_post(const NormArgs &a, bool post, float *dgain, float *dnext, cudaStream_t st)
+static int launch_post(const NormArgs &a, bool post, bool vec, float *dgain, float *dnext, cudaStream_t st)
 {
-    return post ? launch_sized<T, V, GRAD, true>(a, dgain, dnext, st) : launch_sized<T, V, GRAD, false>(a, dgain, dnext, st);
+    if (post) return vec ? launch_sized<T, V, GRAD, true, false>(a, dgain, dnext, st) : launch_sized<T, V, GRAD, true, true>(a, dgain, dnext, st);
+    return vec ? launch_sized<T, V, GRAD, false, false>(a, dgain, dnext, st) : launch_sized<T, V, GRAD, false, true>(a, dgain, dnext, st);
 }
 
 template <bool GRAD>
 static int launch_typed(NormArgs a, bool post, int dtype, bool vec, float *dgain, float *dnext, cudaStream_t st)
 {
     a.inv_d = 1.0f / (float)a.D;
-    if (dtype == K3MOE_TYPE_F32)
-        return vec ? launch_post<float, 4, GRAD>(a, post, dgain, dnext, st) : launch_post<float, 1, GRAD>(a, post, dgain, dnext, st);
-    if (dtype == K3MOE_TYPE_BF16)
-        return vec ? launch_post<__nv_bfloat16, 8, GRAD>(a, post, dgain, dnext, st)
-                   : launch_post<__nv_bfloat16, 1, GRAD>(a, post, dgain, dnext, st);
-    return vec ? launch_post<__half, 8, GRAD>(a, post, dgain, dnext, st) : launch_post<__half, 1, GRAD>(a, post, dgain, dnext, st);
+    if (dtype == K3MOE_TYPE_F32) return launch_post<float, 4, GRAD>(a, post, vec, dgain, dnext, st);
+    if (dtype == K3MOE_TYPE_BF16) return launch_post<__nv_bfloat16, 8, GRAD>(a, post, vec, dgain, dnext, st);
+    return launch_post<__half, 8, GRAD>(a, post, vec, dgain, dnext, st);
 }
 
 // Checks shared by the calls.

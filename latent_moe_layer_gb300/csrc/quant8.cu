@@ -105,24 +105,25 @@ struct QuantRows {
     int rows, n, blocks;
     uint8_t *codes, *scales;
     int vec_x, vec_c;
-    int64_t row_step;                                    // from a half-warp's block to its next: row_step rows and block_step
+    int64_t row_step;                                    // from a block to the next of the same lanes: row_step rows and block_step
     int block_step;                                      // blocks on, a row more where that is past the row's end
 };
 
-// Half a warp a block of 128, eight elements a lane, QR_UNROLL blocks in flight a half-warp.  The blocks are walked without a
-// division (with one a block, 65,536 x 3584 took 208 us).
-constexpr int QR_THREADS = 256, QR_UNROLL = 4, QR_CTAS = 5;
+// Eight lanes a block of 128, lane l its pieces of eight elements l and l + 8 (half a warp with a piece a lane takes more
+// instructions for the maximum), QR_UNROLL blocks in flight.  The blocks are walked without a division (with one a block,
+// 65,536 x 3584 took 208 us).
+constexpr int QR_THREADS = 256, QR_LANES = 8, QR_UNROLL = 2, QR_CTAS = 5;
 template <class T, int KIND>
 __global__ void __launch_bounds__(QR_THREADS, QR_CTAS) quant_rows_kernel(const QuantRows a)
 {
     griddep_enter();
-    const int lane = threadIdx.x & 15;
-    const uint32_t first = blockIdx.x * (QR_THREADS / 16) + (threadIdx.x >> 4);
+    const int lane = threadIdx.x & (QR_LANES - 1);
+    const uint32_t first = (blockIdx.x * QR_THREADS + threadIdx.x) / QR_LANES;
     int64_t at = first / (uint32_t)a.blocks;             // the next block's row
     int block = (int)(first - (uint32_t)at * (uint32_t)a.blocks);
-    // whole warps take part in every round: a half without a block works on zeros
+    // whole warps take part in every round: lanes without a block work on zeros
     while (__any_sync(0xffffffffu, at < a.rows)) {
-        Vec<T, 8> v[QR_UNROLL];
+        Vec<T, 8> v[QR_UNROLL][2];
         int64_t row[QR_UNROLL];
         int col[QR_UNROLL], n[QR_UNROLL];
 #pragma unroll
@@ -130,20 +131,25 @@ __global__ void __launch_bounds__(QR_THREADS, QR_CTAS) quant_rows_kernel(const Q
             row[u] = at;
             col[u] = block * 128 + lane * 8;
             n[u] = at < a.rows ? a.n - col[u] : 0;
-            v[u] = load8<T>(static_cast<const T *>(a.x) + (n[u] > 0 ? at * a.ldx + col[u] : 0), n[u], a.vec_x);
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+                v[u][h] = load8<T>(static_cast<const T *>(a.x) + (n[u] > 64 * h ? at * a.ldx + col[u] + 64 * h : 0), n[u] - 64 * h, a.vec_x);
             at += a.row_step;
             block += a.block_step;
             if (block >= a.blocks) block -= a.blocks, ++at;
         }
 #pragma unroll
         for (int u = 0; u < QR_UNROLL; ++u) {
-            bool infinite;
-            uint32_t m = amax_bits<T>(v[u], infinite);
+            bool infinite[2];
+            uint32_t m = max(amax_bits<T>(v[u][0], infinite[0]), amax_bits<T>(v[u][1], infinite[1]));
 #pragma unroll
-            for (int o = 8; o; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
+            for (int o = QR_LANES / 2; o; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
             const uint32_t s = scale_byte<KIND>(from_bits<T>(m));
             if (n[u] > 0) {
-                store8(a.codes + row[u] * a.ldc + col[u], codes8<T, KIND>(v[u], unscale(s), infinite), n[u], a.vec_c);
+                uint8_t *c = a.codes + row[u] * a.ldc + col[u];
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+                    store8(c + 64 * h, codes8<T, KIND>(v[u][h], unscale(s), infinite[h]), n[u] - 64 * h, a.vec_c);
                 if (lane == 0) a.scales[row[u] * a.lds + (col[u] >> 7)] = (uint8_t)s;
             }
         }
@@ -281,9 +287,9 @@ extern "C" int k3moe_quant8_rows(const void *x, int64_t ldx, int rows, int n, in
     if (rows == 0) return K3MOE_OK;
     const int sms = k3_num_sms();
     if (!sms) return K3MOE_ERR_CUDA;
-    const int64_t ctas = ((int64_t)rows * blocks + QR_THREADS / 16 - 1) / (QR_THREADS / 16);
+    const int64_t ctas = ((int64_t)rows * blocks + QR_THREADS / QR_LANES - 1) / (QR_THREADS / QR_LANES);
     const unsigned grid = (unsigned)std::min<int64_t>(ctas, QR_CTAS * (int64_t)sms);
-    const int64_t step = (int64_t)grid * (QR_THREADS / 16);
+    const int64_t step = (int64_t)grid * (QR_THREADS / QR_LANES);
     const QuantRows a = {x, ldx, ldc, lds, rows, n, blocks, codes, scales, k3_rows16(x, ldx, dtype), bytes_by(codes, ldc, 0, 8),
                          step / blocks, (int)(step % blocks)};
     return by_type(dtype, kind, [&](auto t, auto k) {
