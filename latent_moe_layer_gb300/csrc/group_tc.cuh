@@ -59,8 +59,8 @@ constexpr int64_t GT_L2_ROWS = 32 << 20;
 // bytes of a box of 16 rows of 16 16-bit values, the second eight rows 32 bytes further so that both halves' stores miss
 // each other's banks
 constexpr int GT_BOX16 = 16 * 32 + 32;
-// 8-bit products: scale words (four blocks of the contraction) of 128 rows of A and of 256 of B: four slots in shared memory,
-// two in tensor memory (4 and 8 columns each)
+// 8-bit products: scale words (four blocks of the contraction) of 128 rows of A and of 256 of B: four slots in shared memory
+// (with two, 65,536 rows over 112 experts take 1,203 us for 1,132), two in tensor memory (4 and 8 columns each)
 constexpr int GT_SF_BYTES = 512 + 1024, GT_SF_SLOTS = 4, GT_SF_COL = 2 * 240, GT_SF_COLS = 16;
 
 template <int MODE, bool FOLD>
@@ -625,38 +625,43 @@ __global__ void __launch_bounds__(GroupSmem<MODE, FOLD>::THREADS, 1)
                 const bool sf_begin = F8 && (s == s0 || (s & 3) == 0), sf_end = F8 && (s == s1 - 1 || (s & 3) == 3);
                 if constexpr (F8)
                     if (sf_begin) {
-                        ok = ok && pair_wait(smem_u32(sfull + sf.slot), sf.phase, abort_flag, args.status, 67);
+                        ok = ok && pair_wait_written(smem_u32(sfull + sf.slot), sf.phase, abort_flag, args.status, 67);
                         // its slot in tensor memory: the MMAs of the word two before have read it
                         const uint32_t two = (sf.slot + 2) % GT_SF_SLOTS, p2 = sf.slot < 2 ? sf.phase ^ 1 : sf.phase;
                         if (words++ >= 2) ok = ok && pair_wait(smem_u32(sempty + two), p2, abort_flag, args.status, 70);
                     }
                 ok = ok && pair_wait(smem_u32(full + p.slot), p.phase, abort_flag, args.status, 64);
                 if (!ok) break;
-                if constexpr (F8)
-                    if (sf_begin) mbar_try_wait_cluster(smem_u32(sfull + sf.slot), sf.phase);        // written by threads
                 // a tail was written by threads of either CTA, not by the copy engine
                 if (W && last && (j.last & 15)) mbar_try_wait_cluster(smem_u32(full + p.slot), p.phase);
                 tc_fence_after();
                 const uint32_t d = tmem + acc.slot * TILE_N;
                 const uint64_t ad = ad0 + p.slot * (GT_STAGE / 16), bd = bd0 + p.slot * (GT_STAGE / 16);
                 const int kk_n = last ? (j.last + STEP - 1) / STEP : 4;
-                const uint32_t sfa = tmem + GT_SF_COL + (sf.slot & 1) * GT_SF_COLS, sfb = sfa + 4;
-                const uint32_t sf_id = (uint32_t)(s & 3) << 29 | (uint32_t)(s & 3) << 4;
                 if (one) {
-                    if constexpr (F8)
+                    if constexpr (F8) {
+                        const uint32_t sfa = tmem + GT_SF_COL + (sf.slot & 1) * GT_SF_COLS, sfb = sfa + 4;
                         if (sf_begin) {
                             const uint64_t sd = smem_desc_plain(smem_u32(smem + SM::OFF_SF) + sf.slot * GT_SF_BYTES);
                             tc_copy_scales_pair(sfa, sd);
                             tc_copy_scales_pair(sfb, sd + 512 / 16);
                             if (j.n > 128) tc_copy_scales_pair(sfb + 4, sd + 1024 / 16);
                         }
+                        // (a stage's MMAs take 2 N cycles and their issue some 250: what the loop does beside them counts)
+                        const uint32_t id = idesc | (uint32_t)(s & 3) << 29 | (uint32_t)(s & 3) << 4;
+                        if (kk_n == 4) {
+                            tc_mma_mx_pair(d, ad, bd, id, sfa, sfb, !begin);
 #pragma unroll
-                    for (int kk = 0; kk < 4; ++kk)
-                        if (kk < kk_n) {
-                            const uint32_t more = (!begin || kk > 0) ? 1u : 0u;
-                            if constexpr (F8) tc_mma_mx_pair(d, ad + a_step * kk, bd + b_step * kk, idesc | sf_id, sfa, sfb, more);
-                            else tc_mma_f16_pair(d, ad + a_step * kk, bd + b_step * kk, idesc, more);
+                            for (int kk = 1; kk < 4; ++kk) tc_mma_mx_pair(d, ad + a_step * kk, bd + b_step * kk, id, sfa, sfb, 1u);
+                        } else {
+                            for (int kk = 0; kk < kk_n; ++kk)
+                                tc_mma_mx_pair(d, ad + a_step * kk, bd + b_step * kk, id, sfa, sfb, !begin || kk > 0);
                         }
+                    } else {
+#pragma unroll
+                        for (int kk = 0; kk < 4; ++kk)
+                            if (kk < kk_n) tc_mma_f16_pair(d, ad + a_step * kk, bd + b_step * kk, idesc, (!begin || kk > 0) ? 1u : 0u);
+                    }
                     tc_commit_pair(smem_u32(empty + p.slot), lead);
                     if constexpr (F8)
                         if (sf_end) tc_commit_pair(smem_u32(sempty + sf.slot), lead);
@@ -760,7 +765,7 @@ __global__ void __launch_bounds__(GroupSmem<MODE, FOLD>::THREADS, 1)
                 at[64] = make_uint4(word(4), word(5), word(6), word(7));
                 fence_proxy_async_smem();
                 __syncwarp();
-                if (lane == 0) mbar_arrive_cluster(sfull0 + sf.slot * 8);
+                if (lane == 0) mbar_arrive_written(sfull0 + sf.slot * 8);
                 ++used;
                 sf.next();
             }

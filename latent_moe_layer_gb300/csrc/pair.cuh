@@ -53,6 +53,16 @@ __device__ __forceinline__ void mbar_arrive_cluster(uint32_t cluster_bar)
     asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_bar) : "memory");
 }
 
+// The same for shared memory that this thread (and threads that it has synchronised with) have written: the release covers
+// nothing else.  (The full one waits for all of the warp's memory operations, 0.8 us.)
+__device__ __forceinline__ void mbar_arrive_written(uint32_t cluster_bar)
+{
+    asm volatile(
+        "fence.release.sync_restrict::shared::cta.cluster;\n\t"
+        "mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_bar)
+        : "memory");
+}
+
 // Relaxed: it announces bytes of the copy engine and orders no write of this thread (the release form
 // waits for the thread's earlier memory operations at every stage).
 __device__ __forceinline__ void mbar_expect_tx_cluster(uint32_t cluster_bar, uint32_t bytes)
@@ -89,6 +99,15 @@ __device__ __forceinline__ bool pair_wait(uint32_t bar, uint32_t parity, volatil
     set_status(status, K3MOE_ERR_TIMEOUT, where);
     *abort_flag = 1;
     return false;
+}
+
+// The same where threads of either CTA have written what the barrier stands for (mbar_arrive_written).
+__device__ __forceinline__ bool pair_wait_written(uint32_t bar, uint32_t parity, volatile int *abort_flag, int *status,
+                                                  int where)
+{
+    const bool ok = pair_wait(bar, parity, abort_flag, status, where);
+    asm volatile("fence.acquire.sync_restrict::shared::cluster.cluster;" ::: "memory");
+    return ok;
 }
 
 // TMA loads into the executing CTA's shared memory; the barrier may be the pair's other CTA's.
