@@ -279,6 +279,7 @@ extern "C" int k3moe_quant8_rows(const void *x, int64_t ldx, int rows, int n, in
 {
     if (rows < 0 || n < 1 || (rows > 0 && (!x || !codes || !scales))) return K3MOE_ERR_ARG;
     if (bad_types(dtype, kind)) return K3MOE_ERR_UNSUPPORTED;
+    if (n > INT32_MAX - 256) return K3MOE_ERR_SHAPE;         // columns are counted in 32 bits, blocks rounded up
     const int blocks = (int)(((int64_t)n + 127) / 128);
     if (ldx < n || ldc < n || lds < blocks) return K3MOE_ERR_ARG;
     const size_t nx = k3_span(rows, n, ldx, dtype), nc = rows ? (size_t)(rows - 1) * ldc + n : 0,
@@ -307,6 +308,7 @@ extern "C" int k3moe_quant8_weights(const void *w, int64_t ldw, int64_t stride_w
     const int64_t sw = (int64_t)(n_out - 1) * ldw + n_in, sc = (int64_t)(n_out - 1) * ldc + n_in,
                   stt = codes_t ? (int64_t)(n_in - 1) * ldt + n_out : 0;
     if (n_experts > 1 && (stride_w < 0 || stride_c < sc || (codes_t && stride_t < stt))) return K3MOE_ERR_ARG;
+    if (n_out > INT32_MAX - 256 || n_in > INT32_MAX - 256) return K3MOE_ERR_SHAPE;
     const int nb = (int)(((int64_t)n_out + 127) / 128), kb = (int)(((int64_t)n_in + 127) / 128);
     const double tiles = (double)n_experts * nb * kb;
     if (tiles >= 2147483648.0) return K3MOE_ERR_SHAPE;

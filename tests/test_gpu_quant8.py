@@ -157,6 +157,25 @@ def test_products(sizes, K, N, out_dtype):
     _check(off_d, off, q, qs, w, ws, out_dtype)
 
 
+@pytest.mark.parametrize("sizes,K,N", [([37, 0, 260], 3584, 264), ([5, 9], 2100, 72), ([700], 520, 40)])
+def test_scale_rows_on_4_byte_boundaries(sizes, K, N):
+    # scales of another origin: rows of ceil(K / 128) bytes rounded up to 4, not to 16, from any such place
+    off_d, off, q, qs, (w, ws, wt), _ = _operands(sizes, K, N)
+    want = ex.group_mm8(q, qs, w, ws, off_d)
+    n = qs.shape[1]
+    for start in (0, 4):
+        narrow = torch.full((qs.shape[0], -(-n // 4) * 4 + 8), 255, dtype=torch.uint8, device="cuda")[:, start:start + n]
+        narrow[:] = qs
+        assert torch.equal(ex.group_mm8(q, narrow, w, ws, off_d), want)
+
+
+def test_many_experts():
+    rng = np.random.default_rng(0)
+    sizes = (rng.integers(0, 4, 1024) * (rng.random(1024) < 0.5)).tolist()
+    off_d, off, q, qs, (w, ws, wt), _ = _operands(sizes, 160, 72)
+    _check(off_d, off, q, qs, w, ws, BF)
+
+
 @pytest.mark.parametrize("xk,wk", [("e4m3", "e5m2"), ("e5m2", "e4m3"), ("e5m2", "e5m2")])
 def test_products_of_either_kind(xk, wk):
     off_d, off, q, qs, (w, ws, wt), _ = _operands([70, 3, 140], 300, 200, xk, wk)
