@@ -607,7 +607,6 @@ __global__ void __launch_bounds__(GroupSmem<MODE, FOLD>::THREADS, 1)
         RingPos<NS> p;
         RingPos<2> acc;
         RingPos<GT_SF_SLOTS> sf;
-        uint32_t words = 0;
         bool ok = true;
         for (GroupWalk<MODE> walk(args, s_off, s_tile, mb, cb, jobs); walk.valid() && ok; walk.next()) {
             const GroupJob j = walk.get();
@@ -624,12 +623,7 @@ __global__ void __launch_bounds__(GroupSmem<MODE, FOLD>::THREADS, 1)
                 // a scale word covers four stages
                 const bool sf_begin = F8 && (s == s0 || (s & 3) == 0), sf_end = F8 && (s == s1 - 1 || (s & 3) == 3);
                 if constexpr (F8)
-                    if (sf_begin) {
-                        ok = ok && pair_wait_written(smem_u32(sfull + sf.slot), sf.phase, abort_flag, args.status, 67);
-                        // its slot in tensor memory: the MMAs of the word two before have read it
-                        const uint32_t two = (sf.slot + 2) % GT_SF_SLOTS, p2 = sf.slot < 2 ? sf.phase ^ 1 : sf.phase;
-                        if (words++ >= 2) ok = ok && pair_wait(smem_u32(sempty + two), p2, abort_flag, args.status, 70);
-                    }
+                    if (sf_begin) ok = ok && pair_wait_written(smem_u32(sfull + sf.slot), sf.phase, abort_flag, args.status, 67);
                 ok = ok && pair_wait(smem_u32(full + p.slot), p.phase, abort_flag, args.status, 64);
                 if (!ok) break;
                 // a tail was written by threads of either CTA, not by the copy engine
@@ -699,8 +693,8 @@ __global__ void __launch_bounds__(GroupSmem<MODE, FOLD>::THREADS, 1)
         // ------------------------------------------------------------ scales (each CTA its A rows and all of B's)
         // A word holds a row's scales of four blocks of the contraction, the MMA picks the byte.  In shared memory word i of
         // row 32 i + l of 128 is lane l's i-th; A's rows of a CTA lie in one block of the weights and share one word.
-        // 16 blocks are loaded at a time, while the 16 before them are handed on: an arrival that releases to the cluster
-        // waits for all of the thread's loads (with a load for every word, 8192^3 took 443 us).
+        // 16 blocks are loaded at a time, while the 16 before them are handed on (with a load for every word, 8192^3 took
+        // 443 us; with the loads before the first word of the 16, tiles of 28 stages began 900 cycles late).
         const uint32_t sfull0 = cluster_addr(smem_u32(sfull), lead);
         RingPos<GT_SF_SLOTS> sf;
         uint32_t used = 0;
@@ -724,9 +718,11 @@ __global__ void __launch_bounds__(GroupSmem<MODE, FOLD>::THREADS, 1)
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
                 next_x[i] = make_uint4(0, 0, 0, 0);
+                const int row = j.c0 + lane + 32 * i;
                 if (lane + 32 * i >= j.n) continue;
-                const uint8_t *p = args.xs + (int64_t)(j.c0 + lane + 32 * i) * args.ldxs + b;
-                if (args.xs16 && nb == 16) {
+                const uint8_t *p = args.xs + (int64_t)row * args.ldxs + b;
+                // (past the row's blocks lies the rest of its stride, but behind the last row)
+                if (args.xs16 && (nb == 16 || row < args.rows - 1)) {
                     next_x[i] = *reinterpret_cast<const uint4 *>(p);
                     continue;
                 }
@@ -748,16 +744,10 @@ __global__ void __launch_bounds__(GroupSmem<MODE, FOLD>::THREADS, 1)
 #pragma unroll
             for (int i = 0; i < 8; ++i) x[i] = next_x[i];
             g = (g | 3) + 1;
-            if (g > g_end) walk.next();
-            load();
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
                 if (k < from || k > to) continue;
                 const uint32_t w = __reduce_or_sync(0xffffffffu, (lane >> 2) == k ? aw : 0u);
-                if (!pair_wait(smem_u32(sempty + sf.slot), sf.phase ^ 1, abort_flag, args.status, 68)) {
-                    ok = false;
-                    break;
-                }
                 auto word = [&](int i) { return k == 0 ? x[i].x : k == 1 ? x[i].y : k == 2 ? x[i].z : x[i].w; };
                 uint4 *at = reinterpret_cast<uint4 *>(smem + SM::OFF_SF + sf.slot * GT_SF_BYTES) + lane;
                 at[0] = make_uint4(w, w, w, w);
@@ -765,9 +755,20 @@ __global__ void __launch_bounds__(GroupSmem<MODE, FOLD>::THREADS, 1)
                 at[64] = make_uint4(word(4), word(5), word(6), word(7));
                 fence_proxy_async_smem();
                 __syncwarp();
+                // its slot in tensor memory, and the next one in shared memory: the MMAs of the word two before have read them
+                const uint32_t two = (sf.slot + 2) % GT_SF_SLOTS, p2 = sf.slot < 2 ? sf.phase ^ 1 : sf.phase;
+                if (used >= 2 && !pair_wait(smem_u32(sempty + two), p2, abort_flag, args.status, 68)) {
+                    ok = false;
+                    break;
+                }
                 if (lane == 0) mbar_arrive_written(sfull0 + sf.slot * 8);
                 ++used;
                 sf.next();
+                // the next 16 blocks, while the MMAs have this word's to do
+                if (k == from) {
+                    if (g > g_end) walk.next();
+                    load();
+                }
             }
         }
         // the last releases of this CTA's slots land before it may exit
