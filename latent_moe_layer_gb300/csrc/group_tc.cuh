@@ -597,8 +597,8 @@ __global__ void __launch_bounds__(GroupSmem<MODE, FOLD>::THREADS, 1)
     } else if (warp == 1 && rank == 0) {
         // ------------------------------------------------------------ MMA issuer (even CTA, for both)
         const uint32_t major = (A_K ? 0 : IDESC_A_MN) | (W ? IDESC_B_MN : 0);
-        // a step of 16 (8-bit: 32) contraction values: 32 bytes along a K-major row, 16 rows of 128 bytes MN-major
-        constexpr int a_step = A_K ? 2 : 128, b_step = W ? 128 : 2, STEP = BK / 4;
+        // a step of 16 contraction values: 32 bytes along a K-major row, 16 rows of 128 bytes MN-major
+        constexpr int a_step = A_K ? 2 : 128, b_step = W ? 128 : 2;
         const uint32_t a0 = smem_u32(smem);
         const uint64_t ad0 = A_K ? smem_desc_sw128(a0) : smem_desc_mn_sw128(a0, GT_A_BYTES / 2);
         const uint64_t bd0 = W ? smem_desc_mn_sw128(a0 + GT_A_BYTES, GT_A_BYTES / 2) : smem_desc_sw128(a0 + GT_A_BYTES);
@@ -606,12 +606,10 @@ __global__ void __launch_bounds__(GroupSmem<MODE, FOLD>::THREADS, 1)
         const int part_mask = (1 << args.part) - 1;
         RingPos<NS> p;
         RingPos<2> acc;
-        RingPos<GT_SF_SLOTS> sf;
         bool ok = true;
-        for (GroupWalk<MODE> walk(args, s_off, s_tile, mb, cb, jobs); walk.valid() && ok; walk.next()) {
+        for (GroupWalk<MODE> walk(args, s_off, s_tile, mb, cb, jobs); !F8 && walk.valid() && ok; walk.next()) {
             const GroupJob j = walk.get();
-            const uint32_t idesc = F8 ? idesc_mx(GT_TILE_M, (j.n + 15) & ~15, args.a_type, args.b_type, 0, 0)
-                                      : idesc_f16(GT_TILE_M, (j.n + 15) & ~15, args.bf16) | major;
+            const uint32_t idesc = idesc_f16(GT_TILE_M, (j.n + 15) & ~15, args.bf16) | major;
             const int s0 = first_stage(j), s1 = end_stage(j);
             for (int s = s0; s < s1; ++s, p.next()) {
                 const bool begin = s == s0 || (FOLD && (s & part_mask) == 0), last = s == j.steps - 1;
@@ -620,10 +618,6 @@ __global__ void __launch_bounds__(GroupSmem<MODE, FOLD>::THREADS, 1)
                     ok = pair_wait(smem_u32(tempty + acc.slot), acc.phase ^ 1, abort_flag, args.status, 63);
                     tc_fence_after();
                 }
-                // a scale word covers four stages
-                const bool sf_begin = F8 && (s == s0 || (s & 3) == 0), sf_end = F8 && (s == s1 - 1 || (s & 3) == 3);
-                if constexpr (F8)
-                    if (sf_begin) ok = ok && pair_wait_written(smem_u32(sfull + sf.slot), sf.phase, abort_flag, args.status, 67);
                 ok = ok && pair_wait(smem_u32(full + p.slot), p.phase, abort_flag, args.status, 64);
                 if (!ok) break;
                 // a tail was written by threads of either CTA, not by the copy engine
@@ -631,39 +625,77 @@ __global__ void __launch_bounds__(GroupSmem<MODE, FOLD>::THREADS, 1)
                 tc_fence_after();
                 const uint32_t d = tmem + acc.slot * TILE_N;
                 const uint64_t ad = ad0 + p.slot * (GT_STAGE / 16), bd = bd0 + p.slot * (GT_STAGE / 16);
-                const int kk_n = last ? (j.last + STEP - 1) / STEP : 4;
+                const int kk_n = last ? (j.last + 15) >> 4 : 4;
                 if (one) {
-                    if constexpr (F8) {
-                        const uint32_t sfa = tmem + GT_SF_COL + (sf.slot & 1) * GT_SF_COLS, sfb = sfa + 4;
-                        if (sf_begin) {
-                            const uint64_t sd = smem_desc_plain(smem_u32(smem + SM::OFF_SF) + sf.slot * GT_SF_BYTES);
-                            tc_copy_scales_pair(sfa, sd);
-                            tc_copy_scales_pair(sfb, sd + 512 / 16);
-                            if (j.n > 128) tc_copy_scales_pair(sfb + 4, sd + 1024 / 16);
-                        }
-                        // (a stage's MMAs take 2 N cycles and their issue some 250: what the loop does beside them counts)
-                        const uint32_t id = idesc | (uint32_t)(s & 3) << 29 | (uint32_t)(s & 3) << 4;
-                        if (kk_n == 4) {
-                            tc_mma_mx_pair(d, ad, bd, id, sfa, sfb, !begin);
 #pragma unroll
-                            for (int kk = 1; kk < 4; ++kk) tc_mma_mx_pair(d, ad + a_step * kk, bd + b_step * kk, id, sfa, sfb, 1u);
-                        } else {
-                            for (int kk = 0; kk < kk_n; ++kk)
-                                tc_mma_mx_pair(d, ad + a_step * kk, bd + b_step * kk, id, sfa, sfb, !begin || kk > 0);
-                        }
-                    } else {
-#pragma unroll
-                        for (int kk = 0; kk < 4; ++kk)
-                            if (kk < kk_n) tc_mma_f16_pair(d, ad + a_step * kk, bd + b_step * kk, idesc, (!begin || kk > 0) ? 1u : 0u);
-                    }
+                    for (int kk = 0; kk < 4; ++kk)
+                        if (kk < kk_n) tc_mma_f16_pair(d, ad + a_step * kk, bd + b_step * kk, idesc, (!begin || kk > 0) ? 1u : 0u);
                     tc_commit_pair(smem_u32(empty + p.slot), lead);
-                    if constexpr (F8)
-                        if (sf_end) tc_commit_pair(smem_u32(sempty + sf.slot), lead);
                     if (end) tc_commit_pair(smem_u32(tfull + acc.slot), lead);
                 }
                 __syncwarp();
                 if (end) acc.next();
-                if (F8 && sf_end) sf.next();
+            }
+        }
+        if constexpr (F8) {
+            // The same for 8-bit operands, a scale word (four stages, which are a part too) at a time.  The warp's own latency
+            // bounds this loop, some five cycles an instruction: written with the loop above, a stage took 500 cycles whatever
+            // its width (65,536 rows over 112 experts 1,036 us).
+            RingPos<GT_SF_SLOTS> sf;
+            const uint32_t full0 = smem_u32(full), empty0 = smem_u32(empty);
+            const uint32_t a_lo = (uint32_t)ad0, b_lo = (uint32_t)bd0;
+            const uint64_t a_hi = ad0 >> 32 << 32, b_hi = bd0 >> 32 << 32;
+            for (GroupWalk<MODE> walk(args, s_off, s_tile, mb, cb, jobs); walk.valid() && ok; walk.next()) {
+                const GroupJob j = walk.get();
+                const uint32_t idesc = idesc_mx(GT_TILE_M, (j.n + 15) & ~15, args.a_type, args.b_type, 0, 0);
+                const int s1 = end_stage(j), cut = j.last <= 96 ? j.steps - 1 : -1;      // a stage of less than four MMAs
+                bool begin = true;
+                for (int s = first_stage(j); s < s1 && ok;) {
+                    if (begin) ok = pair_wait(smem_u32(tempty + acc.slot), acc.phase ^ 1, abort_flag, args.status, 63);
+                    ok = ok && pair_wait_written(smem_u32(sfull + sf.slot), sf.phase, abort_flag, args.status, 67);
+                    if (!ok) break;
+                    tc_fence_after();
+                    const int end = min(s1, (s | 3) + 1);
+                    const uint32_t d = tmem + acc.slot * TILE_N, sfa = tmem + GT_SF_COL + (sf.slot & 1) * GT_SF_COLS, sfb = sfa + 4;
+                    if (one) {
+                        const uint64_t sd = smem_desc_plain(smem_u32(smem + SM::OFF_SF) + sf.slot * GT_SF_BYTES);
+                        tc_copy_scales_pair(sfa, sd);
+                        tc_copy_scales_pair(sfb, sd + 512 / 16);
+                        if (j.n > 128) tc_copy_scales_pair(sfb + 4, sd + 1024 / 16);
+                    }
+                    uint32_t id = idesc | (uint32_t)(s & 3) << 29 | (uint32_t)(s & 3) << 4;
+                    for (; s < end; ++s, p.next(), id += 1u << 29 | 1u << 4) {
+                        if (!mbar_try_wait(full0 + p.slot * 8, p.phase) &&
+                            !pair_wait(full0 + p.slot * 8, p.phase, abort_flag, args.status, 64)) {
+                            ok = false;
+                            break;
+                        }
+                        tc_fence_after();
+                        const uint64_t ad = a_hi | (a_lo + p.slot * (GT_STAGE / 16)), bd = b_hi | (b_lo + p.slot * (GT_STAGE / 16));
+                        if (one) {
+                            if (s != cut) {
+                                tc_mma_mx_pair(d, ad, bd, id, sfa, sfb, !begin);
+#pragma unroll
+                                for (int kk = 1; kk < 4; ++kk) tc_mma_mx_pair(d, ad + 2 * kk, bd + 2 * kk, id, sfa, sfb, 1u);
+                            } else {
+                                for (int kk = 0; kk < (j.last + 31) >> 5; ++kk)
+                                    tc_mma_mx_pair(d, ad + 2 * kk, bd + 2 * kk, id, sfa, sfb, !begin || kk > 0);
+                            }
+                            tc_commit_pair(empty0 + p.slot * 8, lead);
+                        }
+                        __syncwarp();
+                        begin = false;
+                    }
+                    if (!ok) break;
+                    if (one) tc_commit_pair(smem_u32(sempty + sf.slot), lead);
+                    sf.next();
+                    if (FOLD || s == s1) {
+                        if (one) tc_commit_pair(smem_u32(tfull + acc.slot), lead);
+                        acc.next();
+                        begin = true;
+                    }
+                    __syncwarp();
+                }
             }
         }
         // every issued MMA completes before TMEM is released
