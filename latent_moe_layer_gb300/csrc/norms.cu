@@ -9,6 +9,11 @@
 //   dy    = rs(y) (gain s - y' mean(gain s y'))
 // The means are computed again from y and h, which the gradient reads anyway: nothing is kept for it but h.  rms_norm
 // is the second half alone (h = x given).
+//
+// One read of every input, one write of every output: HBM should bind, and does forwards (8192 x 7168 bf16 with an
+// elementwise gate and the next norm: 95-99 us, 5.9-6.2 TB/s; 16,384 x 3584: 92 us).  The gradient (162 and 156 us, 5.8 and
+// 6.0 TB/s) is near what its instructions take: two dependent sums a row over all of a CTA's warps, some 450 warp
+// instructions for eight elements of five inputs.  16 rows of 7168 take 6 us, a launch.
 #include "glu.cuh"
 
 namespace k3 {
