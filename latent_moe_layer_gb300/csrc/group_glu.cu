@@ -9,8 +9,9 @@
 // operations, instead of reading 4 bytes an element of them that the forward pass would have had to write.
 //
 // Bound as the products: 251 rows over 112 experts, 3584 to 3072: 650 us, the weights at 6.8 TB/s (product and unit
-// apart: 650 + 8); 32,768 rows over 56 experts 998-1,018 us, 1.42-1.45 PFLOP/s under the power cap (apart: 1,000 + 90); the
-// gradient of 16,381 rows over 28 experts with both products that follow it 1,622 us.
+// apart: 650 + 5); 32,768 rows over 56 experts 889 us, 1.62 PFLOP/s, in short runs (apart: 880 + 94) and 998-1,045 under the
+// power cap; the gradient of 16,381 rows over 28 experts 496 us (the unit's alone, from stored projections: 76, after 446
+// for the product that stores them).
 #include "group_tc.cuh"
 
 using namespace k3;
