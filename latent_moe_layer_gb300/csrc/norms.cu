@@ -193,8 +193,8 @@ constexpr int norm_slots() { return LOOSE ? 0 : std::min(2, (kMaxSmem - 1024) / 
 
 // A group of threads holds a row, P pieces of V elements a thread, and walks over the rows (ONE: the group is the CTA, so that
 // rows' addresses are the same for all its threads).  With 16-byte pieces every thread copies its pieces of the next row into
-// shared memory (its own slots: nothing is synchronised): with two slots while this row is worked on, with one as soon as
-// this row is in registers.
+// shared memory (its own slots: nothing is synchronised): with two slots while this row is worked on, with one when all
+// of this row's pieces have been used (a slot is never written while a load of it may be under way).
 template <class T, int V, int P, bool GRAD, bool POST, int MAXT, int CTAS, bool ONE, bool LOOSE>
 __global__ void __launch_bounds__(MAXT, CTAS) norm_kernel(const NormArgs a)
 {
@@ -449,7 +449,6 @@ __global__ void __launch_bounds__(MAXT, CTAS) norm_kernel(const NormArgs a)
                 }
                 float ss[1] = {sq.x + sq.y};
                 row_sum<ONE>(ss, group, buf, turn);
-                if (SLOTS == 1) fetch(row + step, 0);
                 float r = rsqrtf(fmaf(ss[0], a.inv_d, a.eps));
                 if constexpr (POST) {
                     F2 h[P][H], s2 = f2(0.0f);
@@ -477,6 +476,7 @@ __global__ void __launch_bounds__(MAXT, CTAS) norm_kernel(const NormArgs a)
                         }
                         put(on, row, a.h, a.ld_h, p, o);
                     }
+                    if (SLOTS == 1) fetch(row + step, 0);
                     if (a.next) {
                         float s[1] = {s2.x + s2.y};
                         row_sum<ONE>(s, group, buf, turn);
@@ -508,15 +508,16 @@ __global__ void __launch_bounds__(MAXT, CTAS) norm_kernel(const NormArgs a)
                         }
                         put(on, row, a.n, a.ld_n, p, o);
                     }
+                    if (SLOTS == 1) fetch(row + step, 0);
                 }
             } else {
                 float s[3];
                 grad_sums(in, s[0], s[1], s[2]);
                 row_sum<ONE>(s, group, buf, turn);
-                if (SLOTS == 1) fetch(row + step, 0);
                 const float rh = a.next ? rsqrtf(fmaf(s[0], a.inv_d, a.eps)) : 0.0f;
                 const float ry = POST ? rsqrtf(fmaf(s[2], a.inv_d, a.eps)) : 0.0f;
                 float u[1] = {grad_middle(in, on, row, rh, s[1] * a.inv_d, ry, row_gate, gt)};
+                if (SLOTS == 1) fetch(row + step, 0);
                 if constexpr (POST) {
                     row_sum<ONE>(u, group, buf, turn);
                     grad_last(in, on, row, u[0], ry, row_gate, gt);

@@ -199,7 +199,7 @@ def norm_residual_grad(dh, dn, y, h, gain=None, gate=None, residual_scale=1.0, n
 
     dh and dn are the gradients for h and n (either may be None, not both); h is norm_residual's (may be None without
     dn).  dgain and dnext_gain are fp32 [D], dgate of the gate's shape and type."""
-    if stream is not None and y.device != stream.device:         # dh may be None
+    if stream is not None and getattr(y, "device", stream.device) != stream.device:         # dh may be None
         raise K3Error(ERR_CODE["ARG"], "stream: one of the tensors' device")
     return _call("norm_residual_grad", stream, dh, dn, y, h, gain, gate, residual_scale, next_gain, eps)
 

@@ -157,6 +157,13 @@ def test_products(sizes, K, N, out_dtype):
     _check(off_d, off, q, qs, w, ws, out_dtype)
 
 
+@pytest.mark.parametrize("out_dtype", [BF, F16], ids=["bf16", "f16"])
+@pytest.mark.parametrize("sizes,K,N", [([40], 8320, 72), ([300, 0, 5], 8224, 300), ([1], 16384, 128), ([7] * 40, 8256, 264)])
+def test_contractions_that_16_bit_outputs_take_in_parts(sizes, K, N, out_dtype):
+    off_d, off, q, qs, (w, ws, wt), _ = _operands(sizes, K, N)
+    _check(off_d, off, q, qs, w, ws, out_dtype)
+
+
 @pytest.mark.parametrize("sizes,K,N", [([37, 0, 260], 3584, 264), ([5, 9], 2100, 72), ([700], 520, 40)])
 def test_scale_rows_on_4_byte_boundaries(sizes, K, N):
     # scales of another origin: rows of ceil(K / 128) bytes rounded up to 4, not to 16, from any such place
