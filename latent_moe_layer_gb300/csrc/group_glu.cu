@@ -33,7 +33,7 @@ static bool encode_glu(GroupMaps &maps, GroupTcArgs &a, const K3Group &g, int64_
 int k3_group_glu_tc(const K3Group &g, const K3GroupGlu &u, cudaStream_t st)
 {
     GroupMaps maps;
-    GroupTcArgs a = {};
+    GroupGluTcArgs a = {};
     a.offsets = g.offsets;
     a.E = g.E;
     a.rows = g.rows;

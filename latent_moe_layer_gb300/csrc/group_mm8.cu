@@ -44,7 +44,7 @@ extern "C" int k3moe_group_mm8(const int32_t *offsets, int n_experts, int rows, 
         return K3MOE_ERR_ALIAS;
     if (rows == 0) return K3MOE_OK;
     GroupMaps maps;
-    GroupTcArgs a = {};
+    GroupMm8Args a = {};
     a.offsets = offsets;
     a.E = E;
     a.rows = rows;

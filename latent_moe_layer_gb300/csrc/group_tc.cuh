@@ -108,16 +108,25 @@ struct GroupTcArgs {
     void *out;
     int64_t ldo, stride_o;
     int *status;
-    // gated block: the unit, its constants; the gradient's da
-    int situ, da16;
+};
+// What only the gated block and the 8-bit products need stands in arguments of their own: with one struct for all, mm and grad_x
+// took 108 registers for 84 and spilled 24 bytes past GT_LONG values, and grad_w 12 with four pairs a tile.  (In time the same:
+// 4,096 rows, 16,384 to 4096, 353-365 and 361-387 us; 65,536 rows over 112 experts, 3584 to 6144, 1.97-2.00 ms both.)
+struct GroupGluTcArgs : GroupTcArgs {
+    int situ, da16;          // the unit, its constants; the gradient's da
     GluArgs glu;
     const void *da;
     int64_t ldda;
-    // 8-bit products: scales of x [rows, blocks] (row stride ldxs) and of w (expert, row block, block); types of the codes
+};
+struct GroupMm8Args : GroupTcArgs {
+    // scales of x [rows, blocks] (row stride ldxs) and of w (expert, row block, block); types of the codes
     const uint8_t *xs, *ws;
     int64_t ldxs, sse, sso, ssi;
     int blocks, xs16, a_type, b_type;
 };
+template <int MODE>
+using GroupArgs = std::conditional_t<group_is_glu(MODE), GroupGluTcArgs,
+                                     std::conditional_t<MODE == K3_GROUP_MM8, GroupMm8Args, GroupTcArgs>>;
 
 struct GroupJob {
     int m0, c0, n, steps, last;      // first row and column of the tile; columns; stages; contraction values of the last stage
@@ -209,7 +218,8 @@ __device__ __forceinline__ void load_rows(const CUtensorMap *maps, uint32_t dst,
 }
 
 // (a, b) += (c, d), both sums in one instruction.  Sums that begin at zero and take a part in eight columns at a time leave
-// no register spilled, which the issuing loop would pay (251 rows over 112 experts, fp32 output: 745 us with 16, 734 with 8).
+// no register of mm and grad_x spilled, which the issuing loop would pay (251 rows over 112 experts, fp32 output: 745 us with 16,
+// 734 with 8); parts of the 8-bit products spill 24 to 36 bytes, of the gated block with one pair a tile 40 and 48.
 __device__ __forceinline__ void add2(float &a, float &b, uint32_t c, uint32_t d)
 {
     asm("{\n\t.reg .b64 x, y;\n\tmov.b64 x, {%0, %1};\n\tmov.b64 y, {%2, %3};\n\tadd.rn.f32x2 x, x, y;\n\t"
@@ -225,7 +235,7 @@ __device__ __forceinline__ uint8_t *box16_row(uint8_t *box, int row) { return bo
 
 // da's eight columns from m8 of the tile's row r, whole or cut at the last column; zeros outside.
 template <class O>
-__device__ __forceinline__ uint4 load_da(const GroupTcArgs &args, const GroupJob &j, int m8, int r)
+__device__ __forceinline__ uint4 load_da(const GroupGluTcArgs &args, const GroupJob &j, int m8, int r)
 {
     uint4 v = make_uint4(0, 0, 0, 0);
     if (r >= j.n || m8 >= args.M) return v;
@@ -244,7 +254,7 @@ __device__ __forceinline__ uint4 load_da(const GroupTcArgs &args, const GroupJob
 }
 
 template <int MODE, class O>
-__device__ __forceinline__ void store_glu(const GroupTcArgs &args, const GroupJob &j, int m0, int c, const uint32_t (&v)[16],
+__device__ __forceinline__ void store_glu(const GroupGluTcArgs &args, const GroupJob &j, int m0, int c, const uint32_t (&v)[16],
                                           uint8_t *box)
 {
     constexpr bool GRAD = MODE == K3_GROUP_GLU_GRAD;
@@ -319,7 +329,7 @@ __device__ __forceinline__ void store_glu(const GroupTcArgs &args, const GroupJo
 // is done with), and the pairs add up the parts of a share of the tile each, in a fixed order, and store it.
 template <int MODE, class O, bool CUT, int SPLIT, bool FOLD>
 __global__ void __launch_bounds__(GroupSmem<MODE, FOLD>::THREADS, 1)
-    group_tc_kernel(const __grid_constant__ GroupMaps maps, const GroupTcArgs args)
+    group_tc_kernel(const __grid_constant__ GroupMaps maps, const GroupArgs<MODE> args)
 {
     using SM = GroupSmem<MODE, FOLD>;
     constexpr int NS = SM::NS;
@@ -722,91 +732,93 @@ __global__ void __launch_bounds__(GroupSmem<MODE, FOLD>::THREADS, 1)
             if (lane == 0) mbar_arrive_cluster(cluster_addr(smem_u32(full + slot), lead));
         }
     } else if (F8 && warp == 2) {
-        // ------------------------------------------------------------ scales (each CTA its A rows and all of B's)
-        // A word holds a row's scales of four blocks of the contraction, the MMA picks the byte.  In shared memory word i of
-        // row 32 i + l of 128 is lane l's i-th; A's rows of a CTA lie in one block of the weights and share one word.
-        // 16 blocks are loaded at a time, while the 16 before them are handed on (with a load for every word, 8192^3 took
-        // 443 us; with the loads before the first word of the 16, tiles of 28 stages began 900 cycles late).
-        const uint32_t sfull0 = cluster_addr(smem_u32(sfull), lead);
-        RingPos<GT_SF_SLOTS> sf;
-        uint32_t used = 0;
-        bool ok = true;
-        const int m_blocks = (args.M + 127) / 128;
-        GroupWalk<MODE> walk(args, s_off, s_tile, mb, cb, jobs);
-        GroupJob j;
-        int g = 0, g_end = -1;                               // the first of the next 16 blocks' words, the job's last word
-        uint32_t next_w = 0;                                 // the lane's block of A's 16
-        uint4 next_x[8];                                     // 16 blocks of rows lane + 32 i of B
-        auto load = [&]() {
-            if (g > g_end && walk.valid()) {
-                j = walk.get();
-                g = first_stage(j) >> 2;
-                g_end = (end_stage(j) - 1) >> 2;
-            }
-            if (g > g_end) return;
-            const int b = 16 * (g >> 2), nb = min(16, args.blocks - b), m_block = j.m0 / 128 + (int)rank;
-            next_w = 127u;
-            if (lane < nb && m_block < m_blocks) next_w = args.ws[walk.e * args.sse + m_block * args.sso + (b + lane) * args.ssi];
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                next_x[i] = make_uint4(0, 0, 0, 0);
-                const int row = j.c0 + lane + 32 * i;
-                if (lane + 32 * i >= j.n) continue;
-                const uint8_t *p = args.xs + (int64_t)row * args.ldxs + b;
-                // (past the row's blocks lies the rest of its stride, but behind the last row)
-                if (args.xs16 && (nb == 16 || row < args.rows - 1)) {
-                    next_x[i] = *reinterpret_cast<const uint4 *>(p);
-                    continue;
+        if constexpr (F8) {
+            // ------------------------------------------------------------ scales (each CTA its A rows and all of B's)
+            // A word holds a row's scales of four blocks of the contraction, the MMA picks the byte.  In shared memory word i of
+            // row 32 i + l of 128 is lane l's i-th; A's rows of a CTA lie in one block of the weights and share one word.
+            // 16 blocks are loaded at a time, while the 16 before them are handed on (with a load for every word, 8192^3 took
+            // 443 us; with the loads before the first word of the 16, tiles of 28 stages began 900 cycles late).
+            const uint32_t sfull0 = cluster_addr(smem_u32(sfull), lead);
+            RingPos<GT_SF_SLOTS> sf;
+            uint32_t used = 0;
+            bool ok = true;
+            const int m_blocks = (args.M + 127) / 128;
+            GroupWalk<MODE> walk(args, s_off, s_tile, mb, cb, jobs);
+            GroupJob j;
+            int g = 0, g_end = -1;                               // the first of the next 16 blocks' words, the job's last word
+            uint32_t next_w = 0;                                 // the lane's block of A's 16
+            uint4 next_x[8];                                     // 16 blocks of rows lane + 32 i of B
+            auto load = [&]() {
+                if (g > g_end && walk.valid()) {
+                    j = walk.get();
+                    g = first_stage(j) >> 2;
+                    g_end = (end_stage(j) - 1) >> 2;
                 }
-                uint32_t x[4] = {};
-#pragma unroll
+                if (g > g_end) return;
+                const int b = 16 * (g >> 2), nb = min(16, args.blocks - b), m_block = j.m0 / 128 + (int)rank;
+                next_w = 127u;
+                if (lane < nb && m_block < m_blocks) next_w = args.ws[walk.e * args.sse + m_block * args.sso + (b + lane) * args.ssi];
+    #pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    next_x[i] = make_uint4(0, 0, 0, 0);
+                    const int row = j.c0 + lane + 32 * i;
+                    if (lane + 32 * i >= j.n) continue;
+                    const uint8_t *p = args.xs + (int64_t)row * args.ldxs + b;
+                    // (past the row's blocks lies the rest of its stride, but behind the last row)
+                    if (args.xs16 && (nb == 16 || row < args.rows - 1)) {
+                        next_x[i] = *reinterpret_cast<const uint4 *>(p);
+                        continue;
+                    }
+                    uint32_t x[4] = {};
+    #pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        if (4 * k + 4 <= nb) x[k] = *reinterpret_cast<const uint32_t *>(p + 4 * k);
+                        else
+                            for (int q = 4 * k; q < nb; ++q) x[k] |= (uint32_t)p[q] << (8 * (q & 3));
+                    }
+                    next_x[i] = make_uint4(x[0], x[1], x[2], x[3]);
+                }
+            };
+            load();
+            while (g <= g_end && ok) {
+                const uint32_t aw = next_w << (8 * (lane & 3));
+                const int from = g & 3, to = min(3, g_end - (g & ~3));
+                uint4 x[8];
+    #pragma unroll
+                for (int i = 0; i < 8; ++i) x[i] = next_x[i];
+                g = (g | 3) + 1;
+    #pragma unroll
                 for (int k = 0; k < 4; ++k) {
-                    if (4 * k + 4 <= nb) x[k] = *reinterpret_cast<const uint32_t *>(p + 4 * k);
-                    else
-                        for (int q = 4 * k; q < nb; ++q) x[k] |= (uint32_t)p[q] << (8 * (q & 3));
-                }
-                next_x[i] = make_uint4(x[0], x[1], x[2], x[3]);
-            }
-        };
-        load();
-        while (g <= g_end && ok) {
-            const uint32_t aw = next_w << (8 * (lane & 3));
-            const int from = g & 3, to = min(3, g_end - (g & ~3));
-            uint4 x[8];
-#pragma unroll
-            for (int i = 0; i < 8; ++i) x[i] = next_x[i];
-            g = (g | 3) + 1;
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                if (k < from || k > to) continue;
-                const uint32_t w = __reduce_or_sync(0xffffffffu, (lane >> 2) == k ? aw : 0u);
-                auto word = [&](int i) { return k == 0 ? x[i].x : k == 1 ? x[i].y : k == 2 ? x[i].z : x[i].w; };
-                uint4 *at = reinterpret_cast<uint4 *>(smem + SM::OFF_SF + sf.slot * GT_SF_BYTES) + lane;
-                at[0] = make_uint4(w, w, w, w);
-                at[32] = make_uint4(word(0), word(1), word(2), word(3));
-                at[64] = make_uint4(word(4), word(5), word(6), word(7));
-                fence_proxy_async_smem();
-                __syncwarp();
-                // its slot in tensor memory, and the next one in shared memory: the MMAs of the word two before have read them
-                const uint32_t two = (sf.slot + 2) % GT_SF_SLOTS, p2 = sf.slot < 2 ? sf.phase ^ 1 : sf.phase;
-                if (used >= 2 && !pair_wait(smem_u32(sempty + two), p2, abort_flag, args.status, 68)) {
-                    ok = false;
-                    break;
-                }
-                if (lane == 0) mbar_arrive_written(sfull0 + sf.slot * 8);
-                ++used;
-                sf.next();
-                // the next 16 blocks, while the MMAs have this word's to do
-                if (k == from) {
-                    if (g > g_end) walk.next();
-                    load();
+                    if (k < from || k > to) continue;
+                    const uint32_t w = __reduce_or_sync(0xffffffffu, (lane >> 2) == k ? aw : 0u);
+                    auto word = [&](int i) { return k == 0 ? x[i].x : k == 1 ? x[i].y : k == 2 ? x[i].z : x[i].w; };
+                    uint4 *at = reinterpret_cast<uint4 *>(smem + SM::OFF_SF + sf.slot * GT_SF_BYTES) + lane;
+                    at[0] = make_uint4(w, w, w, w);
+                    at[32] = make_uint4(word(0), word(1), word(2), word(3));
+                    at[64] = make_uint4(word(4), word(5), word(6), word(7));
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    // its slot in tensor memory, and the next one in shared memory: the MMAs of the word two before have read them
+                    const uint32_t two = (sf.slot + 2) % GT_SF_SLOTS, p2 = sf.slot < 2 ? sf.phase ^ 1 : sf.phase;
+                    if (used >= 2 && !pair_wait(smem_u32(sempty + two), p2, abort_flag, args.status, 68)) {
+                        ok = false;
+                        break;
+                    }
+                    if (lane == 0) mbar_arrive_written(sfull0 + sf.slot * 8);
+                    ++used;
+                    sf.next();
+                    // the next 16 blocks, while the MMAs have this word's to do
+                    if (k == from) {
+                        if (g > g_end) walk.next();
+                        load();
+                    }
                 }
             }
-        }
-        // the last releases of this CTA's slots land before it may exit
-        for (uint32_t q = 0; ok && q < min(used, (uint32_t)GT_SF_SLOTS); ++q, sf.next()) {
-            if (used < (uint32_t)GT_SF_SLOTS && q == 0) sf.slot = 0, sf.phase = 1;
-            ok = pair_wait(smem_u32(sempty + sf.slot), sf.phase ^ 1, abort_flag, args.status, 69);
+            // the last releases of this CTA's slots land before it may exit
+            for (uint32_t q = 0; ok && q < min(used, (uint32_t)GT_SF_SLOTS); ++q, sf.next()) {
+                if (used < (uint32_t)GT_SF_SLOTS && q == 0) sf.slot = 0, sf.phase = 1;
+                ok = pair_wait(smem_u32(sempty + sf.slot), sf.phase ^ 1, abort_flag, args.status, 69);
+            }
         }
     } else if (warp >= 3) {
         // ------------------------------------------------------------ epilogue (each CTA its 128 rows)
@@ -1049,7 +1061,7 @@ int fit_clusters(cudaLaunchConfig_t &cfg, cudaLaunchAttribute (&attr)[2], cudaSt
 }
 
 template <int MODE, class O, bool FOLD, bool CUT = false, int SPLIT = 1>
-int launch_tc(const GroupMaps &maps, GroupTcArgs a, int64_t max_jobs, cudaStream_t st)
+int launch_tc(const GroupMaps &maps, GroupArgs<MODE> a, int64_t max_jobs, cudaStream_t st)
 {
     if constexpr (MODE == K3_GROUP_GRAD_W && !CUT)
         if (a.Nc * sizeof(O) % 16) return launch_tc<MODE, O, FOLD, true>(maps, a, max_jobs, st);
@@ -1098,7 +1110,7 @@ inline int64_t tile_cycles(const GroupTcArgs &a, int split, int clusters)
 // that is faster: 1 row, 6144 to 64: 9.8 us with four, 14.5 with two, 22.8 with one; 16 experts of a row, 4096 to 512:
 // 12.7 with two, 17.1 with one; 1,024 rows, 1024 to 512: 10.8, 8.4, 8.0.
 template <int MODE, class O, bool FOLD>
-int launch_rows(const GroupMaps &maps, const GroupTcArgs &a, int64_t max_jobs, cudaStream_t st)
+int launch_rows(const GroupMaps &maps, const GroupArgs<MODE> &a, int64_t max_jobs, cudaStream_t st)
 {
     const int64_t tiles = most_tiles<MODE>(a, group_tile(MODE)), steps = (a.K + group_bk(MODE) - 1) / group_bk(MODE);
     const int pairs = k3_num_sms() / 2;
@@ -1148,7 +1160,7 @@ int launch_grad_w(const GroupMaps &maps, const GroupTcArgs &a, int64_t jobs, cud
 }
 
 template <int MODE, class O>
-int launch_mode(const GroupMaps &maps, const GroupTcArgs &a, int64_t max_jobs, cudaStream_t st)
+int launch_mode(const GroupMaps &maps, const GroupArgs<MODE> &a, int64_t max_jobs, cudaStream_t st)
 {
     if constexpr (MODE == K3_GROUP_GRAD_W) return launch_grad_w<O>(maps, a, max_jobs, st);
     else if (a.K > (sizeof(O) == 4 ? group_bk(MODE) << a.part : GT_LONG)) return launch_rows<MODE, O, true>(maps, a, max_jobs, st);
