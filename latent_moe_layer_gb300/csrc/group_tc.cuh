@@ -219,7 +219,7 @@ __device__ __forceinline__ void load_rows(const CUtensorMap *maps, uint32_t dst,
 
 // (a, b) += (c, d), both sums in one instruction.  Sums that begin at zero and take a part in eight columns at a time leave
 // no register of mm and grad_x spilled, which the issuing loop would pay (251 rows over 112 experts, fp32 output: 745 us with 16,
-// 734 with 8); parts of the 8-bit products spill 24 to 36 bytes, of the gated block with one pair a tile 40 and 48.
+// 734 with 8); parts of the 8-bit products spill 24 to 36 bytes, of the gated block with one pair a tile 36 and 44.
 __device__ __forceinline__ void add2(float &a, float &b, uint32_t c, uint32_t d)
 {
     asm("{\n\t.reg .b64 x, y;\n\tmov.b64 x, {%0, %1};\n\tmov.b64 y, {%2, %3};\n\tadd.rn.f32x2 x, x, y;\n\t"
@@ -279,10 +279,12 @@ __device__ __forceinline__ void store_glu(const GroupGluTcArgs &args, const Grou
         }
         g[i / 2] = {up ? other[0] : own[0], up ? other[1] : own[1]};
         u[i / 2] = {up ? own[0] : other[0], up ? own[1] : other[1]};
-        small = small && fabsf(g[i / 2].x) <= args.glu.g.small && fabsf(g[i / 2].y) <= args.glu.g.small &&
-                fabsf(u[i / 2].x) <= args.glu.u.small && fabsf(u[i / 2].y) <= args.glu.u.small;
+        auto within = [&](float gate, float lin) { return fabsf(gate) <= args.glu.g.small && fabsf(lin) <= args.glu.u.small; };
+        small = small && (c + mine + i >= j.n || within(g[i / 2].x, u[i / 2].x)) &&
+                (c + mine + i + 1 >= j.n || within(g[i / 2].y, u[i / 2].y));
     }
-    small = __all_sync(0xffffffffu, small);
+    // (what is not stored has no say: other experts' rows, and weight rows beside the last column)
+    small = __all_sync(0xffffffffu, small || m0 + col >= args.M);
     auto unit = [&](auto kind) {
         constexpr int K = decltype(kind)::value;             // 0 SiLU, 1 SiTU within its bounds, 2 SiTU
 #pragma unroll
