@@ -358,6 +358,7 @@ int k3moe_ep_dispatch(k3moe_handle *h, const int32_t *idx, int tokens_per_rank, 
  *   - status: device int32 [4], caller-owned and zeroed by the caller once: the first device-side
  *     error is recorded in it as in the handle's status word (K3MOE_ERR_RANGE: offsets or a row
  *     number outside its range; K3MOE_ERR_TIMEOUT).  With bad offsets a product writes nothing.
+ *   - Products grouped by expert take rows, n_in and n_out up to 2^31 - 257 (K3MOE_ERR_SHAPE beyond).
  *   - An output that overlaps an input is K3MOE_ERR_ALIAS, except where a call says otherwise.
  *   - Every call only enqueues kernels on `stream`: no allocation, no synchronisation (capturable). */
 #define K3MOE_TYPE_F32  0

@@ -122,5 +122,7 @@ int k3_group_generic(int mode, const K3Group &g, cudaStream_t st);
 // Whether the tensor-core kernels take it (every row on a 16-byte boundary), and their launch.
 bool k3_group_tc_fits(int mode, const K3Group &g);
 int k3_group_tc(int mode, const K3Group &g, cudaStream_t st);
+// Rows and widths of a product at most: tiles, blocks and stages round them up, and rows' tiles reach past the last row, in 32 bits.
+constexpr int K3_GROUP_MAX_SIZE = INT32_MAX - 256;
 // The argument checks that all products share: sizes, offsets and types; > 0: nothing to do.
 int k3_group_check(const K3Group &g, int mode);

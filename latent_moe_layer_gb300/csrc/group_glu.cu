@@ -83,6 +83,7 @@ static int glu_run(K3Group g, int act, float beta, float linear_beta, const void
     full.rows = 0;
     int rc = k3_group_check(full, K3_GROUP_MM);
     if (rc < 0) return rc;
+    if (g.rows > K3_GROUP_MAX_SIZE) return K3MOE_ERR_SHAPE;
     if (g.rows < 0 || (g.rows > 0 && (!g.a || !g.b || !g.out)) || g.lda < g.n_in) return K3MOE_ERR_ARG;
     const size_t no = k3_span(g.rows, cols, ldo, g.dtype);
     const size_t nw = k3_span(1, (g.E - 1) * g.stride_b + (int64_t)(g.n_out - 1) * g.ldb + g.n_in, 0, g.dtype);

@@ -210,7 +210,7 @@ int k3_group_glu_generic(const K3Group &g, const K3GroupGlu &u, cudaStream_t st)
 int k3_group_check(const K3Group &g, int mode)
 {
     if (g.E < 1 || g.rows < 0 || g.n_in < 1 || g.n_out < 1 || !g.offsets || !g.status) return K3MOE_ERR_ARG;
-    if (g.E > K3MOE_TRAIN_MAX_EXPERTS) return K3MOE_ERR_SHAPE;
+    if (g.E > K3MOE_TRAIN_MAX_EXPERTS || std::max({g.rows, g.n_in, g.n_out}) > K3_GROUP_MAX_SIZE) return K3MOE_ERR_SHAPE;
     if (g.dtype != K3MOE_TYPE_BF16 && g.dtype != K3MOE_TYPE_F16) return K3MOE_ERR_UNSUPPORTED;
     if (g.out_dtype != g.dtype && g.out_dtype != K3MOE_TYPE_F32) return K3MOE_ERR_UNSUPPORTED;
     const size_t noff = sizeof(int32_t) * ((size_t)g.E + 1);

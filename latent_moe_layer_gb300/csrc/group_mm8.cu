@@ -23,7 +23,7 @@ extern "C" int k3moe_group_mm8(const int32_t *offsets, int n_experts, int rows, 
 {
     const int E = n_experts;
     if (E < 1 || rows < 0 || n_in < 1 || n_out < 1 || !offsets || !status) return K3MOE_ERR_ARG;
-    if (E > K3MOE_TRAIN_MAX_EXPERTS) return K3MOE_ERR_SHAPE;
+    if (E > K3MOE_TRAIN_MAX_EXPERTS || std::max({rows, n_in, n_out}) > K3_GROUP_MAX_SIZE) return K3MOE_ERR_SHAPE;
     for (const int kind : {x_kind, w_kind})
         if (kind != K3MOE_F8_E4M3 && kind != K3MOE_F8_E5M2) return K3MOE_ERR_UNSUPPORTED;
     if (out_dtype != K3MOE_TYPE_F32 && out_dtype != K3MOE_TYPE_BF16 && out_dtype != K3MOE_TYPE_F16) return K3MOE_ERR_UNSUPPORTED;
