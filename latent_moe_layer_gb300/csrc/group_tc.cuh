@@ -760,7 +760,7 @@ __global__ void __launch_bounds__(GroupSmem<MODE, FOLD>::THREADS, 1)
                 const int b = 16 * (g >> 2), nb = min(16, args.blocks - b), m_block = j.m0 / 128 + (int)rank;
                 next_w = 127u;
                 if (lane < nb && m_block < m_blocks) next_w = args.ws[walk.e * args.sse + m_block * args.sso + (b + lane) * args.ssi];
-    #pragma unroll
+#pragma unroll
                 for (int i = 0; i < 8; ++i) {
                     next_x[i] = make_uint4(0, 0, 0, 0);
                     const int row = j.c0 + lane + 32 * i;
@@ -772,10 +772,12 @@ __global__ void __launch_bounds__(GroupSmem<MODE, FOLD>::THREADS, 1)
                         continue;
                     }
                     uint32_t x[4] = {};
-    #pragma unroll
+#pragma unroll
                     for (int k = 0; k < 4; ++k) {
                         if (4 * k + 4 <= nb) x[k] = *reinterpret_cast<const uint32_t *>(p + 4 * k);
                         else
+                            // few rows' last words (unrolled, the copies of this took the compiler 110 s)
+#pragma unroll 1
                             for (int q = 4 * k; q < nb; ++q) x[k] |= (uint32_t)p[q] << (8 * (q & 3));
                     }
                     next_x[i] = make_uint4(x[0], x[1], x[2], x[3]);
@@ -786,10 +788,10 @@ __global__ void __launch_bounds__(GroupSmem<MODE, FOLD>::THREADS, 1)
                 const uint32_t aw = next_w << (8 * (lane & 3));
                 const int from = g & 3, to = min(3, g_end - (g & ~3));
                 uint4 x[8];
-    #pragma unroll
+#pragma unroll
                 for (int i = 0; i < 8; ++i) x[i] = next_x[i];
                 g = (g | 3) + 1;
-    #pragma unroll
+#pragma unroll
                 for (int k = 0; k < 4; ++k) {
                     if (k < from || k > to) continue;
                     const uint32_t w = __reduce_or_sync(0xffffffffu, (lane >> 2) == k ? aw : 0u);
