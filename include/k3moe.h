@@ -471,7 +471,8 @@ int k3moe_group_glu_grad(const int32_t *offsets, int n_experts, int rows, int n_
                          float situ_beta, float situ_linear_beta, void *dgu, int64_t lddgu, int32_t *status,
                          cudaStream_t stream);
 
-/* Norms around a block, rs(v) = 1 / sqrt(mean v^2 + eps) over a row of D <= 16384 (eps > 0; squares in fp32):
+/* Norms around a block, rs(v) = 1 / sqrt(mean v^2 + eps) over a row of D <= 16384 (eps > 0; squares in fp32: a row
+ * whose squares add up to 2^128 or more has rs 0):
  *   rms_norm        out = gain x rs(x)
  *   norm_residual   h = residual_scale residual + gate (gain y rs(y)),  n = next_gain h rs(h)   (n NULL: h alone)
  * F32, F16 or BF16 rows; gains [D] of that type or F32 (gain_dtype), NULL for ones; n is computed from the h that is not

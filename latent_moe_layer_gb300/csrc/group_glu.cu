@@ -8,10 +8,13 @@
 // exchange between warps through shared memory.)  The gradient computes the projections again, 2 rows n_in 2 width
 // operations, instead of reading 4 bytes an element of them that the forward pass would have had to write.
 //
+// dgu leaves in the operands' 16 bits, as grad_x and grad_w take it: their results lie 2.3e-3 (bf16; f16 2.9e-4) of their norm
+// from 64 bits, against 1.66e-3 (2.1e-4) of the outputs' own rounding with dgu in fp32.
+//
 // Bound as the products: 251 rows over 112 experts, 3584 to 3072: 650 us, the weights at 6.8 TB/s (product and unit
 // apart: 650 + 5); 32,768 rows over 56 experts 889 us, 1.62 PFLOP/s, in short runs (apart: 880 + 94) and 998-1,045 under the
-// power cap; the gradient of 16,381 rows over 28 experts 496 us (the unit's alone, from stored projections: 76, after 446
-// for the product that stores them).
+// power cap.  One pass saves memory, not time, where there is a backward pass: 16,381 rows over 28 experts take 437 us and 471
+// for the gradient, with stored projections (group_mm, the unit, the unit's gradient) 457 + 50 + 76.
 #include "group_tc.cuh"
 
 using namespace k3;

@@ -578,7 +578,7 @@ __global__ void __launch_bounds__(512) norm_gain_kernel(const float *part, int g
 }
 
 // Elements a thread: 16; 8 for norm_residual's gradient up to 8192 columns, which keeps the sums of two gains and more in
-// registers (7168 columns: 896 threads of 72 registers).
+// registers.
 static int norm_group(int D, int elems)
 {
     int n = (D + elems - 1) / elems;
@@ -587,7 +587,10 @@ static int norm_group(int D, int elems)
     while (group < n) group *= 2;
     return group;
 }
-constexpr int NORM_NARROW = 96;                          // threads a row at most where a CTA has several rows
+// Threads a row at most where a CTA has several rows.  64, 96 and 128 (67 M elements, bf16): norm_residual_grad of 1024 columns
+// 203, 203, 226 us; rms_norm_grad of 768 columns 134, 120, 120, of 1536 146, 112, 111, of 1024 111, 111, 122; norm_residual of
+// 1536 columns 106, 111, 111, of 2048 102, 102, 112.
+constexpr int NORM_NARROW = 96;
 static int norm_rows(int group) { return group > NORM_NARROW ? 1 : 256 / group; }
 // CTAs of a gradient's grid at most, each with sums of its own.
 static int64_t norm_parts(int64_t rows) { return std::min<int64_t>(rows, 608); }
@@ -640,6 +643,12 @@ static int launch_sized(const NormArgs &a, float *dgain, float *dnext, cudaStrea
     const std::false_type several;
     // (threads, CTAs an SM) that the registers are counted for
     if constexpr (GRAD && POST) {
+        // A thread wants 72 registers, so an SM holds 28 warps: two CTAs of at most 14 (448 threads, 3584 columns), which in
+        // fp32 leaves room for two rows in shared memory, or one of at most 28 (896 threads, 7168 columns).  Wider rows take
+        // 1024 threads of 64 registers, which spill 52 bytes (fp32 72).  67 M elements (fp32 half), 448 | 896 | 1024 threads: bf16 1024
+        // columns 203 | 203 | 248 us, 3584: 175 | 175 | 207, 5120: 198 with 896, 218 with 1024, 7168: 182 and 220; fp32 1024
+        // columns 172 | 195 | 219, 3584: 170 | 172 | 179, 7168: 183 and 192.  (4096 columns, one CTA of 512 threads where 64
+        // registers would hold two: 217 and 200, fp32 196 and 174.)
         if (a.D <= NORM_NARROW * 8) return go(e8, integral_constant<int, 256>(), integral_constant<int, 3>(), several);
         if constexpr (!LOOSE) {
             if (a.D <= 3584) return go(e8, integral_constant<int, 448>(), integral_constant<int, 2>(), one);

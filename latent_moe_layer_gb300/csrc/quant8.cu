@@ -6,7 +6,7 @@
 // where m is above 0.75: bits of amax, no logarithm.  x 2^-k is exact, so a code is rounded once.
 //
 // Bound by HBM: 65,536 x 3584 bf16 rows in 107 us (6.6 TB/s), weights of 28 experts of 3584 x 3072 into both orders from one
-// read in 182 us (6.8 TB/s).
+// read in 182 us (6.8 TB/s).  Rows off 16-byte boundaries are loaded element by element: 171 us for the 107.
 #include <cuda_fp8.h>
 
 #include "glu.cuh"

@@ -135,14 +135,16 @@ def group_glu(x, w, offsets, act="silu", situ_beta=4.0, situ_linear_beta=25.0, o
     """a[r] = act(Wg x[r]) (Wu x[r]) for every expert's rows: both projections and the unit in one pass.
 
     x [rows, n_in], w [E, 2 width, n_in] = gate rows then up rows, of one 16-bit type -> a [rows, width].  The
-    projections are not rounded on the way (group_mm then glu_dropout rounds them, and draws a dropout mask)."""
+    projections are not rounded on the way (group_mm then glu_dropout rounds them, and draws a dropout mask).  Nothing is
+    kept for the gradient but x: less memory, and more time, than group_mm, glu_dropout and glu_dropout_grad."""
     return _call("group_glu", stream, x, w, offsets, act, situ_beta, situ_linear_beta, out)
 
 
 def group_glu_grad(da, x, w, offsets, act="silu", situ_beta=4.0, situ_linear_beta=25.0, out=None, stream=None):
     """Gradient of group_glu for its projections, which are computed again -> dgu [rows, 2 width].
 
-    The gradients for x and w are group_mm_grad_x(dgu, w, offsets) and group_mm_grad_w(dgu, x, offsets)."""
+    The gradients for x and w are group_mm_grad_x(dgu, w, offsets) and group_mm_grad_w(dgu, x, offsets), of dgu in x's
+    16 bits."""
     return _call("group_glu_grad", stream, da, x, w, offsets, act, situ_beta, situ_linear_beta, out)
 
 
@@ -168,8 +170,9 @@ def group_mm8(x, x_scales, w, w_scales, offsets, out=None, out_dtype=None, strea
     """y[r] = w[e] x[r] on 8-bit operands (quant8_rows, quant8_weights) -> [rows, n_out], bf16 (or `out`'s / `out_dtype`'s
     type: f16, fp32).
 
-    The gradient for the rows is the same call on the quantised dy with the transposed codes and scales.  Codes of rows
-    that are not on 16-byte boundaries are refused."""
+    The gradient for the rows is the same call on the quantised dy with the transposed codes and scales; that for the weights
+    is group_mm_grad_w on 16-bit rows.  Scales are powers of two alone (uint8 exponents).  Codes of rows that are not on
+    16-byte boundaries are refused, and x_scales' off 4-byte ones."""
     return _call("group_mm8", stream, x, x_scales, w, w_scales, offsets, out, out_dtype)
 
 
