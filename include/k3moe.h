@@ -360,6 +360,7 @@ int k3moe_ep_dispatch(k3moe_handle *h, const int32_t *idx, int tokens_per_rank, 
  *     number outside its range; K3MOE_ERR_TIMEOUT).  With bad offsets a product writes nothing.
  *   - Products grouped by expert take rows, n_in and n_out up to 2^31 - 257 (K3MOE_ERR_SHAPE beyond).
  *   - An output that overlaps an input is K3MOE_ERR_ALIAS, except where a call says otherwise.
+ *   - Every pointer is at a multiple of its elements' bytes (K3MOE_ERR_ALIGN).
  *   - Every call only enqueues kernels on `stream`: no allocation, no synchronisation (capturable). */
 #define K3MOE_TYPE_F32  0
 #define K3MOE_TYPE_BF16 1

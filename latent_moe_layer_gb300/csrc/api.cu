@@ -99,7 +99,7 @@ const char *k3moe_strerror(int code)
     case K3MOE_OK: return "ok";
     case K3MOE_ERR_ARG: return "invalid argument";
     case K3MOE_ERR_SHAPE: return "unsupported shape";
-    case K3MOE_ERR_ALIGN: return "pointer or row not 16-byte aligned";
+    case K3MOE_ERR_ALIGN: return "pointer or row not aligned as required";
     case K3MOE_ERR_BAD_SCALE: return "E8M0 scale byte 255 (NaN)";
     case K3MOE_ERR_ALIAS: return "output overlaps input";
     case K3MOE_ERR_WORKSPACE: return "workspace missing or too small";

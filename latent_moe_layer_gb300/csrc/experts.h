@@ -3,6 +3,7 @@
 #pragma once
 
 #include <algorithm>
+#include <initializer_list>
 #include <type_traits>
 
 #include "k3moe_internal.h"
@@ -85,6 +86,18 @@ inline bool k3_overlap(const void *a, size_t na, const void *b, size_t nb)
 {
     const uintptr_t x = (uintptr_t)a, y = (uintptr_t)b;
     return na && nb && x < y + nb && y < x + na;
+}
+
+// Whether all pointers are at multiples of their elements' bytes, as every load and store needs.
+struct K3Elements {
+    const void *p;
+    int bytes;
+};
+inline bool k3_aligned(std::initializer_list<K3Elements> all)
+{
+    for (const K3Elements &e : all)
+        if ((uintptr_t)e.p % e.bytes) return false;
+    return true;
 }
 
 // Rows that may be read in 16-byte pieces: base and leading dimension.

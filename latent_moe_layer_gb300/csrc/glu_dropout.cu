@@ -343,6 +343,8 @@ extern "C" int k3moe_dropout(const void *x, const void *residual, int64_t n, int
     const size_t nb = k3_span(1, n, n, dtype);
     if ((out != x && k3_overlap(out, nb, x, nb)) || (residual && out != residual && k3_overlap(out, nb, residual, nb)))
         return K3MOE_ERR_ALIAS;
+    const int es = k3_type_bytes(dtype);
+    if (!k3_aligned({{x, es}, {residual, es}, {out, es}})) return K3MOE_ERR_ALIGN;
     if (n == 0) return K3MOE_OK;
     const int sms = k3_num_sms();
     if (!sms) return K3MOE_ERR_CUDA;
@@ -408,6 +410,7 @@ static int glu_run(const void *da, int64_t ldda, const void *gu, int64_t ldgu, i
     const bool in_place = GRAD && out == gu && ldo == ldgu;
     if ((!in_place && k3_overlap(out, no, gu, ngu)) || (GRAD && k3_overlap(out, no, da, k3_span(rows, width, ldda, dtype))))
         return K3MOE_ERR_ALIAS;
+    if (!k3_aligned({{gu, 2}, {out, 2}, {da, 2}})) return K3MOE_ERR_ALIGN;
     if (rows == 0) return K3MOE_OK;
     const int sms = k3_num_sms();
     if (!sms) return K3MOE_ERR_CUDA;

@@ -94,6 +94,7 @@ static int glu_run(K3Group g, int act, float beta, float linear_beta, const void
         k3_overlap(g.out, no, g.offsets, sizeof(int32_t) * ((size_t)g.E + 1)) ||
         (grad && k3_overlap(g.out, no, da, k3_span(g.rows, width, ldda, g.dtype))))
         return K3MOE_ERR_ALIAS;
+    if (!k3_aligned({{g.out, 2}, {da, 2}})) return K3MOE_ERR_ALIGN;                      // (the others: above)
     if (g.rows == 0) return K3MOE_OK;
     g.n_out = width;
     const bool fits = k3_rows16(g.a, g.lda, g.dtype) && k3_rows16(g.b, g.ldb, g.dtype) && (g.E == 1 || (g.stride_b * 2) % 16 == 0);

@@ -214,6 +214,7 @@ int k3_group_check(const K3Group &g, int mode)
     if (g.dtype != K3MOE_TYPE_BF16 && g.dtype != K3MOE_TYPE_F16) return K3MOE_ERR_UNSUPPORTED;
     if (g.out_dtype != g.dtype && g.out_dtype != K3MOE_TYPE_F32) return K3MOE_ERR_UNSUPPORTED;
     const size_t noff = sizeof(int32_t) * ((size_t)g.E + 1);
+    const bool aligned = k3_aligned({{g.a, 2}, {g.b, 2}, {g.out, k3_type_bytes(g.out_dtype)}, {g.offsets, 4}, {g.status, 4}});
     if (mode == K3_GROUP_GRAD_W) {
         if (!g.out || (g.rows > 0 && (!g.a || !g.b))) return K3MOE_ERR_ARG;
         if (g.accumulate != 0 && g.accumulate != 1) return K3MOE_ERR_ARG;
@@ -224,7 +225,7 @@ int k3_group_check(const K3Group &g, int mode)
         if (k3_overlap(g.out, no, g.a, k3_span(g.rows, g.n_out, g.lda, g.dtype)) ||
             k3_overlap(g.out, no, g.b, k3_span(g.rows, g.n_in, g.ldb, g.dtype)) || k3_overlap(g.out, no, g.offsets, noff))
             return K3MOE_ERR_ALIAS;
-        return K3MOE_OK;
+        return aligned ? K3MOE_OK : K3MOE_ERR_ALIGN;
     }
     const int in = mode == K3_GROUP_MM ? g.n_in : g.n_out, out = mode == K3_GROUP_MM ? g.n_out : g.n_in;
     if (g.rows > 0 && (!g.a || !g.b || !g.out)) return K3MOE_ERR_ARG;
@@ -235,6 +236,7 @@ int k3_group_check(const K3Group &g, int mode)
     if (k3_overlap(g.out, no, g.a, k3_span(g.rows, in, g.lda, g.dtype)) || k3_overlap(g.out, no, g.b, nw) ||
         k3_overlap(g.out, no, g.offsets, noff))
         return K3MOE_ERR_ALIAS;
+    if (!aligned) return K3MOE_ERR_ALIGN;
     return g.rows == 0 ? 1 : K3MOE_OK;
 }
 

@@ -42,6 +42,7 @@ extern "C" int k3moe_group_mm8(const int32_t *offsets, int n_experts, int rows, 
     if (k3_overlap(y, no, x, nx) || k3_overlap(y, no, x_scales, nxs) || k3_overlap(y, no, w, nw) || k3_overlap(y, no, w_scales, nws) ||
         k3_overlap(y, no, offsets, sizeof(int32_t) * ((size_t)E + 1)))
         return K3MOE_ERR_ALIAS;
+    if (!k3_aligned({{y, k3_type_bytes(out_dtype)}, {offsets, 4}, {status, 4}})) return K3MOE_ERR_ALIGN;
     if (rows == 0) return K3MOE_OK;
     GroupMaps maps;
     GroupMm8Args a = {};

@@ -708,22 +708,26 @@ static int norm_check(int rows, int D, int dtype, int gain_dtype, float eps, std
     }
     return K3MOE_OK;
 }
-// Vectors (gains, row gates, gradients' sums, workspace) apart from every output.
+// Vectors (gains, row gates, gradients' sums, workspace) apart from every output; all pointers at their elements' bytes.
 struct NormVector {
     const void *p;
     size_t bytes;
     bool out;
+    int element;
 };
-static bool norm_apart(int rows, int D, int dtype, std::initializer_list<NormMatrix> ms, std::initializer_list<NormVector> vs)
+static int norm_vectors(int rows, int D, int dtype, std::initializer_list<NormMatrix> ms, std::initializer_list<NormVector> vs)
 {
+    bool aligned = true;
+    for (const NormMatrix &m : ms) aligned = aligned && k3_aligned({{m.p, k3_type_bytes(dtype)}});
     for (const NormVector &v : vs) {
         if (!v.p) continue;
+        aligned = aligned && k3_aligned({{v.p, v.element}});
         for (const NormMatrix &m : ms)
-            if (m.p && (m.out || v.out) && k3_overlap(v.p, v.bytes, m.p, k3_span(rows, D, m.ld, dtype))) return false;
+            if (m.p && (m.out || v.out) && k3_overlap(v.p, v.bytes, m.p, k3_span(rows, D, m.ld, dtype))) return K3MOE_ERR_ALIAS;
         for (const NormVector &w : vs)
-            if (&w != &v && w.p && (w.out || v.out) && k3_overlap(v.p, v.bytes, w.p, w.bytes)) return false;
+            if (&w != &v && w.p && (w.out || v.out) && k3_overlap(v.p, v.bytes, w.p, w.bytes)) return K3MOE_ERR_ALIAS;
     }
-    return true;
+    return aligned ? K3MOE_OK : K3MOE_ERR_ALIGN;
 }
 static bool aligned16(const void *p) { return ((uintptr_t)p & 15) == 0; }
 
@@ -736,9 +740,10 @@ extern "C" int k3moe_rms_norm(const void *x, int64_t ldx, const void *gain, int 
 {
     bool vec = false;
     const std::initializer_list<NormMatrix> ms = {{x, ldx, false, true}, {out, ldo, true, true}};
-    const int rc = norm_check(rows, D, dtype, gain_dtype, eps, ms, vec);
+    int rc = norm_check(rows, D, dtype, gain_dtype, eps, ms, vec);
     if (rc) return rc;
-    if (!norm_apart(rows, D, dtype, ms, {{gain, (size_t)D * k3_type_bytes(gain_dtype), false}})) return K3MOE_ERR_ALIAS;
+    const int eg = k3_type_bytes(gain_dtype);
+    if ((rc = norm_vectors(rows, D, dtype, ms, {{gain, (size_t)D * eg, false, eg}}))) return rc;
     if (rows == 0) return K3MOE_OK;
     NormArgs a = {};
     a.y = x, a.ld_y = ldx;
@@ -760,12 +765,13 @@ extern "C" int k3moe_norm_residual(const void *y, int64_t ldy, const void *resid
     const std::initializer_list<NormMatrix> ms = {{y, ldy, false, true}, {residual, ldr, false, true},
                                                   {full ? gate : nullptr, ldgate, false, full}, {h, ldh, true, true},
                                                   {n, ldn, true, false}};
-    const int rc = norm_check(rows, D, dtype, gain_dtype, eps, ms, vec);
+    int rc = norm_check(rows, D, dtype, gain_dtype, eps, ms, vec);
     if (rc) return rc;
-    const size_t ng = (size_t)D * k3_type_bytes(gain_dtype);
-    if (!norm_apart(rows, D, dtype, ms, {{gain, ng, false}, {next_gain, ng, false},
-                                         {gate_kind == NORM_GATE_ROW ? gate : nullptr, (size_t)rows * 4, false}}))
-        return K3MOE_ERR_ALIAS;
+    const int eg = k3_type_bytes(gain_dtype);
+    const size_t ng = (size_t)D * eg;
+    if ((rc = norm_vectors(rows, D, dtype, ms, {{gain, ng, false, eg}, {next_gain, ng, false, eg},
+                                                {gate_kind == NORM_GATE_ROW ? gate : nullptr, (size_t)rows * 4, false, 4}})))
+        return rc;
     if (rows == 0) return K3MOE_OK;
     NormArgs a = {};
     a.y = y, a.ld_y = ldy;
@@ -790,13 +796,14 @@ extern "C" int k3moe_rms_norm_grad(const void *dy, int64_t lddy, const void *x, 
     bool vec = false;
     const std::initializer_list<NormMatrix> ms = {{dy, lddy, false, true}, {x, ldx, false, true}, {add, ldadd, false, false},
                                                   {dx, lddx, true, true}};
-    const int rc = norm_check(rows, D, dtype, gain_dtype, eps, ms, vec);
+    int rc = norm_check(rows, D, dtype, gain_dtype, eps, ms, vec);
     if (rc) return rc;
     const size_t need = k3moe_norm_grad_workspace_bytes(rows, D);
     if (!workspace || workspace_bytes < need || ((uintptr_t)workspace & 3)) return K3MOE_ERR_WORKSPACE;
-    if (!norm_apart(rows, D, dtype, ms, {{gain, (size_t)D * k3_type_bytes(gain_dtype), false}, {dgain, (size_t)D * 4, true},
-                                         {workspace, need, true}}))
-        return K3MOE_ERR_ALIAS;
+    const int eg = k3_type_bytes(gain_dtype);
+    if ((rc = norm_vectors(rows, D, dtype, ms, {{gain, (size_t)D * eg, false, eg}, {dgain, (size_t)D * 4, true, 4},
+                                                {workspace, need, true, 4}})))
+        return rc;
     NormArgs a = {};
     a.dn = dy, a.ld_dn = lddy;
     a.hin = x, a.ld_hin = ldx;
@@ -826,15 +833,17 @@ extern "C" int k3moe_norm_residual_grad(const void *dh, int64_t lddh, const void
         {dh, lddh, false, false}, {dn, lddn, false, false}, {y, ldy, false, true}, {h, ldh, false, dn != nullptr},
         {full ? gate : nullptr, ldgate, false, full}, {dy, lddy, true, true}, {dresidual, lddr, true, true},
         {full ? dgate : nullptr, lddgate, true, full}};
-    const int rc = norm_check(rows, D, dtype, gain_dtype, eps, ms, vec);
+    int rc = norm_check(rows, D, dtype, gain_dtype, eps, ms, vec);
     if (rc) return rc;
     const size_t need = k3moe_norm_grad_workspace_bytes(rows, D);
     if (!workspace || workspace_bytes < need || ((uintptr_t)workspace & 3)) return K3MOE_ERR_WORKSPACE;
-    const size_t ng = (size_t)D * k3_type_bytes(gain_dtype);
-    if (!norm_apart(rows, D, dtype, ms, {{gain, ng, false}, {next_gain, ng, false}, {by_row ? gate : nullptr, (size_t)rows * 4, false},
-                                         {by_row ? dgate : nullptr, (size_t)rows * 4, true}, {dgain, (size_t)D * 4, true},
-                                         {dnext_gain, (size_t)D * 4, true}, {workspace, need, true}}))
-        return K3MOE_ERR_ALIAS;
+    const int eg = k3_type_bytes(gain_dtype);
+    const size_t ng = (size_t)D * eg;
+    if ((rc = norm_vectors(rows, D, dtype, ms, {{gain, ng, false, eg}, {next_gain, ng, false, eg},
+                                                {by_row ? gate : nullptr, (size_t)rows * 4, false, 4},
+                                                {by_row ? dgate : nullptr, (size_t)rows * 4, true, 4}, {dgain, (size_t)D * 4, true, 4},
+                                                {dnext_gain, (size_t)D * 4, true, 4}, {workspace, need, true, 4}})))
+        return rc;
     NormArgs a = {};
     a.dh = dh, a.ld_dh = lddh;
     a.dn = dn, a.ld_dn = lddn;

@@ -288,6 +288,7 @@ extern "C" int k3moe_quant8_rows(const void *x, int64_t ldx, int rows, int n, in
     const size_t nx = k3_span(rows, n, ldx, dtype), nc = rows ? (size_t)(rows - 1) * ldc + n : 0,
                  ns = rows ? (size_t)(rows - 1) * lds + blocks : 0;
     if (k3_overlap(codes, nc, x, nx) || k3_overlap(scales, ns, x, nx) || k3_overlap(codes, nc, scales, ns)) return K3MOE_ERR_ALIAS;
+    if (!k3_aligned({{x, 2}})) return K3MOE_ERR_ALIGN;
     if (rows == 0) return K3MOE_OK;
     const int sms = k3_num_sms();
     if (!sms) return K3MOE_ERR_CUDA;
@@ -321,6 +322,7 @@ extern "C" int k3moe_quant8_weights(const void *w, int64_t ldw, int64_t stride_w
     if (k3_overlap(codes, nc, w, nw) || k3_overlap(codes_t, nt, w, nw) || k3_overlap(scales, ns, w, nw) ||
         k3_overlap(codes, nc, codes_t, nt) || k3_overlap(codes, nc, scales, ns) || k3_overlap(codes_t, nt, scales, ns))
         return K3MOE_ERR_ALIAS;
+    if (!k3_aligned({{w, 2}})) return K3MOE_ERR_ALIGN;
     const bool one = n_experts == 1;
     const QuantWeights a = {w, ldw, stride_w, ldc, stride_c, ldt, stride_t, n_experts, n_out, n_in, nb, kb, codes, codes_t, scales,
                             k3_rows16(w, ldw, dtype) && (one || stride_w * 2 % 16 == 0), bytes_by(codes, ldc, one ? 0 : stride_c, 8),

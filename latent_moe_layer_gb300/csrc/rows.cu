@@ -353,6 +353,7 @@ extern "C" int k3moe_rows_plan(const int32_t *idx, int T, int K, int first_exper
     if (k3_overlap(idx, nb, pos, nb) || k3_overlap(idx, nb, offsets, no) || k3_overlap(pos, nb, offsets, no) ||
         k3_overlap(workspace, nw, idx, nb) || k3_overlap(workspace, nw, pos, nb) || k3_overlap(workspace, nw, offsets, no))
         return K3MOE_ERR_ALIAS;
+    if (!k3_aligned({{idx, 4}, {offsets, 4}, {pos, 4}})) return K3MOE_ERR_ALIGN;
     const int blocks = n > 0 ? (int)((n + per - 1) / per) : 1;
     int32_t *counts = blocks > 1 ? static_cast<int32_t *>(workspace) : nullptr;
     static unsigned long long attr_set = 0;
@@ -396,6 +397,7 @@ extern "C" int k3moe_rows_gather(const void *x, int64_t ldx, const int32_t *pos,
     if (ldx < D || ldo < D) return K3MOE_ERR_ARG;
     const size_t no = k3_span(n_rows, D, ldo, dtype);
     if (k3_overlap(out, no, x, k3_span(T, D, ldx, dtype)) || k3_overlap(out, no, pos, (size_t)T * K * 4)) return K3MOE_ERR_ALIAS;
+    if (!k3_aligned({{x, 2}, {out, 2}, {pos, 4}, {status, 4}})) return K3MOE_ERR_ALIGN;
     if (T == 0) return K3MOE_OK;
     const int sms = k3_num_sms();
     if (!sms) return K3MOE_ERR_CUDA;
@@ -422,6 +424,7 @@ extern "C" int k3moe_rows_combine(const void *y, int64_t ldy, int n_rows, const 
     const size_t nz = k3_span(T, D, ldz, dtype), nt = (size_t)T * K * 4;
     if (k3_overlap(z, nz, y, k3_span(n_rows, D, ldy, dtype)) || k3_overlap(z, nz, pos, nt) || k3_overlap(z, nz, weights, weights ? nt : 0))
         return K3MOE_ERR_ALIAS;
+    if (!k3_aligned({{y, 2}, {z, 2}, {pos, 4}, {weights, 4}, {status, 4}})) return K3MOE_ERR_ALIGN;
     if (T == 0) return K3MOE_OK;
     const int sms = k3_num_sms();
     if (!sms) return K3MOE_ERR_CUDA;
@@ -454,6 +457,7 @@ extern "C" int k3moe_rows_combine_grad(const void *dz, int64_t lddz, const void 
         k3_overlap(dy, ndy, weights, nt) || k3_overlap(dweights, nt, dy, ndy) || k3_overlap(dweights, nt, dz, nz) ||
         k3_overlap(dweights, nt, y, ny) || k3_overlap(dweights, nt, pos, nt) || k3_overlap(dweights, nt, weights, nt))
         return K3MOE_ERR_ALIAS;
+    if (!k3_aligned({{dz, 2}, {y, 2}, {dy, 2}, {pos, 4}, {weights, 4}, {dweights, 4}, {status, 4}})) return K3MOE_ERR_ALIGN;
     if (T == 0) return K3MOE_OK;
     const bool vec = D % 8 == 0 && k3_rows16(dz, lddz, dtype) && k3_rows16(y, ldy, dtype) && k3_rows16(dy, lddy, dtype);
     with_types(dtype, vec, [&](auto t, auto v) {
