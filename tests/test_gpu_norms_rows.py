@@ -122,3 +122,16 @@ def test_rows_strides_past_31_bits(gate):
     assert torch.equal(dx, ex.rms_norm_grad(v["dn"], v["y"], v["gain"], add=v["dh"])[0])
     del big, other, w, hw, h, dxw, dx
     torch.cuda.empty_cache()
+
+
+@pytest.mark.parametrize("dt", [BF, F32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("D", [64, 1001, 7168])
+def test_rows_whose_squares_leave_fp32_have_norm_zero(D, dt):
+    v = _inputs(9, D, "none", dt)
+    v["y"][4] = 2.0 ** 70
+    h, n = ex.norm_residual(v["y"], v["res"], gain=v["gain"], residual_scale=0.5, next_gain=v["next_gain"])
+    assert torch.equal(h[4], (0.5 * v["res"][4].float()).to(dt)) and torch.isfinite(n).all()
+    assert not ex.rms_norm(v["y"], v["gain"])[4].any()
+    other = [0, 1, 2, 3, 5, 6, 7, 8]
+    w = {k: (t[other] if torch.is_tensor(t) and t.shape[0] == 9 else t) for k, t in v.items()}
+    assert torch.equal(h[other], _check_forward(w, 0.5))
